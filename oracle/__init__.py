@@ -44,3 +44,4 @@ from .row_equalizer import (  # noqa: F401
     muon_step_equalized,
     muon_run_equalized,
 )
+from .adamw import adamw_step, grad_norm  # noqa: F401

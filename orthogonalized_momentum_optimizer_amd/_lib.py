@@ -1,5 +1,4 @@
-"""ctypes binding of libmuon.so (the C ABI of include/muon.h and include/cautious_adam.h),
-with the same names.
+"""ctypes binding of libmuon.so (the C ABI of the headers under include/), with the same names.
 
 Only argument marshalling happens here: every step of the optimizer runs in the HIP
 kernels of the library. PyTorch's HIP runtime is loaded first (``import torch``) so the
@@ -35,8 +34,14 @@ EXPORTED = (
     "muon_plan_read_profile", "muon_status_string", "muon_last_error",
     "muon_adam_config_default", "muon_cautious_adam_step", "muon_step_noalloc",
     "muon_plan_set_concurrency", "muon_plan_set_fused",
+    "muon_adamw_config_default", "muon_adamw_plan_create", "muon_adamw_step",
+    "muon_adamw_plan_destroy", "muon_grad_plan_create", "muon_grad_plan_workspace_size",
+    "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
 )
 MUON_MAX_STREAMS = 4
+MUON_ADAMW_F32 = 0
+MUON_ADAMW_8BIT = 1
+MUON_ADAMW_BLOCK = 256
 MUON_STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -101,6 +106,36 @@ class muon_adam_config(ctypes.Structure):
     ]
 
 
+class muon_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p),
+        ("exp_avg_sq_scale", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int),
+        ("grad_dtype", ctypes.c_int),
+        ("wd_mul", ctypes.c_float),
+    ]
+
+
+class muon_adamw_config(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float),
+        ("beta1", ctypes.c_float),
+        ("beta2", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("step", ctypes.c_int64),
+        ("grad_scale", ctypes.c_void_p),
+        ("skip_nonfinite", ctypes.c_int),
+        ("stochastic", ctypes.c_int),
+        ("seed", ctypes.c_uint64),
+    ]
+
+
 _lib = None
 
 
@@ -147,6 +182,27 @@ def lib() -> ctypes.CDLL:
     L.muon_cautious_adam_step.argtypes = [ctypes.POINTER(muon_adam_tensor), i64,
                                           ctypes.POINTER(muon_adam_config), vp]
     L.muon_cautious_adam_step.restype = ctypes.c_int
+    L.muon_adamw_config_default.argtypes = [ctypes.POINTER(muon_adamw_config)]
+    L.muon_adamw_config_default.restype = None
+    L.muon_adamw_plan_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(muon_adamw_tensor),
+                                         i64, ctypes.c_int]
+    L.muon_adamw_plan_create.restype = ctypes.c_int
+    L.muon_adamw_step.argtypes = [vp, ctypes.POINTER(vp), i64,
+                                  ctypes.POINTER(muon_adamw_config), vp]
+    L.muon_adamw_step.restype = ctypes.c_int
+    L.muon_adamw_plan_destroy.argtypes = [vp]
+    L.muon_adamw_plan_destroy.restype = None
+    L.muon_grad_plan_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(i64),
+                                        ctypes.POINTER(ctypes.c_int), i64]
+    L.muon_grad_plan_create.restype = ctypes.c_int
+    L.muon_grad_plan_workspace_size.argtypes = [vp]
+    L.muon_grad_plan_workspace_size.restype = sz
+    L.muon_grad_norm.argtypes = [vp, ctypes.POINTER(vp), i64, ctypes.c_float, vp, vp, vp, sz, vp]
+    L.muon_grad_norm.restype = ctypes.c_int
+    L.muon_grad_scale.argtypes = [vp, ctypes.POINTER(vp), i64, vp, vp]
+    L.muon_grad_scale.restype = ctypes.c_int
+    L.muon_grad_plan_destroy.argtypes = [vp]
+    L.muon_grad_plan_destroy.restype = None
     L.muon_status_string.argtypes = [ctypes.c_int]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_last_error.argtypes = []
@@ -268,3 +324,67 @@ def make_adam_tensors(entries) -> ctypes.Array:
     for i, e in enumerate(entries):
         arr[i] = muon_adam_tensor(*e)
     return arr
+
+
+def muon_adamw_config_default() -> muon_adamw_config:
+    cfg = muon_adamw_config()
+    lib().muon_adamw_config_default(ctypes.byref(cfg))
+    return cfg
+
+
+def make_adamw_tensors(entries) -> ctypes.Array:
+    """entries: iterable of (param, master, exp_avg, exp_avg_sq, exp_avg_scale,
+    exp_avg_sq_scale, numel, pdt, gdt, wd_mul)."""
+    entries = list(entries)
+    arr = (muon_adamw_tensor * max(len(entries), 1))()
+    for i, e in enumerate(entries):
+        arr[i] = muon_adamw_tensor(*e)
+    return arr
+
+
+def make_pointers(pointers: Sequence) -> ctypes.Array:
+    return (ctypes.c_void_p * max(len(pointers), 1))(*pointers)
+
+
+def muon_adamw_plan_create(tensors, n: int, state: int) -> int:
+    """``tensors``: a ctypes array of muon_adamw_tensor (or None when n == 0)."""
+    plan = ctypes.c_void_p()
+    _check(lib().muon_adamw_plan_create(ctypes.byref(plan), tensors, n, int(state)))
+    return plan.value
+
+
+def muon_adamw_step(plan: int, grads, n: int, cfg: muon_adamw_config, stream: int) -> None:
+    """``grads``: a ctypes array of pointers (make_pointers)."""
+    _check(lib().muon_adamw_step(plan, grads, n, ctypes.byref(cfg), stream))
+
+
+def muon_adamw_plan_destroy(plan: int) -> None:
+    lib().muon_adamw_plan_destroy(plan)
+
+
+def muon_grad_plan_create(numel: Sequence[int], dtype: Sequence[int]) -> int:
+    n = len(numel)
+    if len(dtype) != n:
+        raise ValueError("numel and dtype must have the same length")
+    plan = ctypes.c_void_p()
+    _check(lib().muon_grad_plan_create(ctypes.byref(plan), (ctypes.c_int64 * max(n, 1))(*numel),
+                                       (ctypes.c_int * max(n, 1))(*dtype), n))
+    return plan.value
+
+
+def muon_grad_plan_workspace_size(plan: int) -> int:
+    return int(lib().muon_grad_plan_workspace_size(plan))
+
+
+def muon_grad_norm(plan: int, grads, n: int, max_norm: float, out: int, norms, workspace: int,
+                   workspace_bytes: int, stream: int) -> None:
+    _check(lib().muon_grad_norm(plan, grads, n, max_norm, out, norms, workspace, workspace_bytes,
+                                stream))
+
+
+def muon_grad_scale(plan: int, grads, n: int, scale: int, stream: int) -> None:
+    _check(lib().muon_grad_scale(plan, grads, n, scale, stream))
+
+
+def muon_grad_plan_destroy(plan: int) -> None:
+    lib().muon_grad_plan_destroy(plan)

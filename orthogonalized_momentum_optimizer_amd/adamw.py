@@ -1,0 +1,394 @@
+"""AdamW over many tensors at once (fp32 or 8-bit states) and the gradient norm that clips it:
+PyTorch-facing wrappers of include/adamw.h and include/grad_norm.h.
+
+``AdamWPlan`` and ``GradNormPlan`` hold a plan of the library for a fixed list of tensors;
+``AdamW`` is the ``torch.optim`` front end, ``clip_grad_norm_`` the in-place form for the other
+optimizers. PyTorch supplies device memory and the current stream; every step runs in
+libmuon.so.
+"""
+from __future__ import annotations
+
+import contextlib
+import math
+from typing import Iterable, List, Optional, Sequence, Union
+
+import torch
+
+from . import _lib as L
+from .optim import dtype_code
+
+_Tensor = torch.Tensor
+
+
+def make_adamw_config(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
+                      skip_nonfinite=False, stochastic=True, seed=0) -> L.muon_adamw_config:
+    """A muon_adamw_config; ``step`` is the index t >= 1 of the step in the bias corrections.
+    ``stochastic`` and ``seed``: how 8-bit states round the second moment."""
+    cfg = L.muon_adamw_config_default()
+    cfg.lr, cfg.beta1, cfg.beta2 = lr, betas[0], betas[1]
+    cfg.eps, cfg.weight_decay, cfg.step = eps, weight_decay, int(step)
+    cfg.skip_nonfinite, cfg.stochastic = int(bool(skip_nonfinite)), int(bool(stochastic))
+    cfg.seed = int(seed) & (2 ** 64 - 1)
+    return cfg
+
+
+def _one_device(tensors: Sequence[torch.Tensor]) -> torch.device:
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("CUDA tensors expected")
+        if t.device != tensors[0].device:
+            raise ValueError("all tensors must be on one device")
+    if tensors:
+        return tensors[0].device
+    return torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_available() else 0)
+
+
+class _TensorList:
+    """The device and gradient layout shared by the two plans."""
+
+    def _set_list(self, device, numels, dtypes):
+        self.device = device
+        self._numels = [int(x) for x in numels]
+        self._dtypes = list(dtypes)
+        self._index = [device.index] * len(self._numels)
+
+    def _pointers(self, grads: Sequence[Optional[torch.Tensor]]):
+        """The gradients' addresses, after checking them against the plan."""
+        if not isinstance(grads, (list, tuple)):
+            grads = list(grads)
+        n = len(self._numels)
+        if len(grads) != n:
+            raise ValueError(f"expected {n} gradients, got {len(grads)}")
+        try:
+            ptrs = list(map(_Tensor.data_ptr, grads))
+        except TypeError:
+            return self._pointers_with_none(grads)
+        if (list(map(_Tensor.numel, grads)) != self._numels
+                or [g.dtype for g in grads] != self._dtypes
+                or list(map(_Tensor.get_device, grads)) != self._index
+                or not all(map(_Tensor.is_contiguous, grads))):
+            for i, g in enumerate(grads):
+                self._check_grad(i, g)
+        return L.make_pointers(ptrs)
+
+    def _pointers_with_none(self, grads):
+        for i, g in enumerate(grads):
+            if g is not None:
+                self._check_grad(i, g)
+        return L.make_pointers([None if g is None else g.data_ptr() for g in grads])
+
+    def _check_grad(self, i, g):
+        if not isinstance(g, _Tensor):
+            raise TypeError(f"gradient {i}: a tensor or None expected")
+        if g.numel() != self._numels[i] or not g.is_contiguous() or g.device != self.device:
+            raise ValueError(f"gradient {i}: a contiguous tensor of {self._numels[i]} elements "
+                             f"on {self.device} expected")
+        if g.dtype != self._dtypes[i]:
+            raise TypeError(f"gradient {i}: {self._dtypes[i]} expected, got {g.dtype}")
+
+    def _check_scalar(self, name, x):
+        if x.numel() != 1 or x.dtype != torch.float32 or x.device != self.device:
+            raise ValueError(f"{name} must be one float32 on {self.device}")
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The plan's device as the current one, and ``stream`` (or the current stream) as its
+        current stream; yields its handle."""
+        with contextlib.ExitStack() as stack:
+            if torch.cuda.current_device() != self.device.index:
+                stack.enter_context(torch.cuda.device(self.device))
+            if stream is not None:
+                if stream.device != self.device:
+                    raise ValueError(f"the stream must be one of {self.device}")
+                stack.enter_context(torch.cuda.stream(stream))
+            yield torch.cuda.current_stream(self.device).cuda_stream
+
+
+class AdamWPlan(_TensorList):
+    """A plan of the library for a fixed list of parameters and their states, which it holds.
+
+    ``exp_avgs`` and ``exp_avg_sqs``: float32, or all float8_e4m3fn (the 8-bit states, the
+    second one holding sqrt(v)) with ``exp_avg_scales`` and ``exp_avg_sq_scales``, one
+    float8_e8m0fnu per 256 elements of a tensor. ``grad_dtypes``: of the gradients that steps
+    will receive. ``masters``: per parameter None or, for a bfloat16 one, its
+    float32 master copy. ``wd_muls``: per parameter the multiplier of the weight decay (default 1). All contiguous; all states and
+    scales zero before step 1."""
+
+    def __init__(self, params: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
+                 exp_avg_sqs: Sequence[torch.Tensor], grad_dtypes: Sequence[torch.dtype],
+                 masters: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                 exp_avg_scales: Optional[Sequence[torch.Tensor]] = None,
+                 exp_avg_sq_scales: Optional[Sequence[torch.Tensor]] = None,
+                 wd_muls: Optional[Sequence[float]] = None):
+        self.handle = None
+        n = len(params)
+        masters = [None] * n if masters is None else list(masters)
+        wd_muls = [1.0] * n if wd_muls is None else [float(w) for w in wd_muls]
+        if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+            raise ValueError("give both scales or neither")
+        small = exp_avg_scales is not None
+        scales_m = list(exp_avg_scales) if small else [None] * n
+        scales_r = list(exp_avg_sq_scales) if small else [None] * n
+        lists = (exp_avgs, exp_avg_sqs, grad_dtypes, masters, scales_m, scales_r, wd_muls)
+        if any(len(x) != n for x in lists):
+            raise ValueError("one state, gradient dtype, master, scale and wd_mul per parameter")
+        state_dtype = torch.float8_e4m3fn if small else torch.float32
+        held, entries = [], []
+        for i in range(n):
+            p, w, m, v, ms, vs = (params[i], masters[i], exp_avgs[i], exp_avg_sqs[i], scales_m[i],
+                                  scales_r[i])
+            mine = [t for t in (p, w, m, v, ms, vs) if t is not None]
+            for t in (p, w, m, v):
+                if t is not None and t.numel() != p.numel():
+                    raise ValueError(f"parameter {i}: tensors of {p.numel()} elements expected")
+            if any(not t.is_contiguous() for t in mine):
+                raise ValueError(f"parameter {i}: contiguous tensors expected")
+            if m.dtype != state_dtype or v.dtype != state_dtype:
+                raise TypeError(f"parameter {i}: states must be {state_dtype} "
+                                f"{'beside' if small else 'without'} scales")
+            if w is not None and w.dtype != torch.float32:
+                raise TypeError(f"parameter {i}: the master copy must be float32")
+            for t in (ms, vs):
+                if t is None:
+                    continue
+                if t.dtype != torch.float8_e8m0fnu:
+                    raise TypeError(f"parameter {i}: scales must be float8_e8m0fnu")
+                if t.numel() != -(-p.numel() // L.MUON_ADAMW_BLOCK):
+                    raise ValueError(f"parameter {i}: one scale per {L.MUON_ADAMW_BLOCK} elements")
+            held += mine
+            ptr = [t.data_ptr() if t is not None else None for t in (p, w, m, v, ms, vs)]
+            entries.append((*ptr, p.numel(), dtype_code(p.dtype), dtype_code(grad_dtypes[i]),
+                            wd_muls[i]))
+        self._set_list(_one_device(held), [p.numel() for p in params], grad_dtypes)
+        self.state_bits = 8 if small else 32
+        self._held = held
+        self.handle = L.muon_adamw_plan_create(L.make_adamw_tensors(entries) if n else None, n,
+                                               L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
+
+    def step(self, grads: Sequence[Optional[torch.Tensor]], cfg: L.muon_adamw_config,
+             grad_scale: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> None:
+        """One step. A gradient may be None: its parameter is left out. ``grad_scale``: one
+        float32 on the device that every gradient is multiplied by (``GradNormPlan.norm``'s)."""
+        ptrs = self._pointers(grads)
+        if grad_scale is not None:
+            self._check_scalar("grad_scale", grad_scale)
+            cfg = L.muon_adamw_config.from_buffer_copy(cfg)
+            cfg.grad_scale = grad_scale.data_ptr()
+        with self._on(stream) as handle:
+            L.muon_adamw_step(self.handle, ptrs, len(self._numels), cfg, handle)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            L.muon_adamw_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class GradNormPlan(_TensorList):
+    """A plan of the library for gradients like those given (their sizes, dtypes and device;
+    the tensors themselves are not kept)."""
+
+    def __init__(self, grads: Sequence[torch.Tensor]):
+        self.handle = None
+        grads = list(grads)
+        self._set_list(_one_device(grads), [g.numel() for g in grads], [g.dtype for g in grads])
+        self.handle = L.muon_grad_plan_create(self._numels, [dtype_code(d) for d in self._dtypes])
+        self.ws_bytes = L.muon_grad_plan_workspace_size(self.handle)
+
+    def norm(self, grads: Sequence[Optional[torch.Tensor]], max_norm: float = math.inf,
+             per_tensor: bool = False, stream: Optional[torch.cuda.Stream] = None):
+        """(norm, scale), or with ``per_tensor`` (norm, scale, norms): float32 on the device,
+        new tensors each call. scale = min(1, max_norm / norm), NaN for a norm that is not
+        finite. A gradient that is None counts as zero. The workspace belongs to the call."""
+        ptrs = self._pointers(grads)
+        n = len(self._numels)
+        with self._on(stream) as handle:
+            out = torch.empty(2 + (n if per_tensor else 0), dtype=torch.float32, device=self.device)
+            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            base = out.data_ptr()
+            L.muon_grad_norm(self.handle, ptrs, n, max_norm, base,
+                             base + 8 if per_tensor and n else None, ws.data_ptr() or None,
+                             self.ws_bytes, handle)
+        if per_tensor:
+            return out[0], out[1], out[2:]
+        return out[0], out[1]
+
+    def scale_(self, grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Multiplies every gradient by ``scale`` (one float32 on the device) in place; where it
+        is 1 nothing is read or written."""
+        ptrs = self._pointers(grads)
+        self._check_scalar("scale", scale)
+        with self._on(stream) as handle:
+            L.muon_grad_scale(self.handle, ptrs, len(self._numels), scale.data_ptr(), handle)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            L.muon_grad_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def grad_norm(grads: Iterable[torch.Tensor], max_norm: float = math.inf):
+    """(norm, scale) of a list of CUDA gradients (bfloat16 or float32, contiguous)."""
+    grads = list(grads)
+    return GradNormPlan(grads).norm(grads, max_norm)
+
+
+def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]],
+                    max_norm: float) -> torch.Tensor:
+    """Scales the gradients of ``parameters`` in place to a global 2-norm of at most
+    ``max_norm`` and returns their norm before it (a float32 on the device; nothing
+    synchronises). If the norm is not finite, every gradient becomes NaN."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    plan = GradNormPlan(grads)
+    norm, scale = plan.norm(grads, max_norm)
+    plan.scale_(grads, scale)
+    return norm
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW with decoupled weight decay for any parameters (bfloat16 or float32, contiguous,
+    one device per group), one pass over all tensors of a group.
+
+    ``state_bits``: 32, or 8 for e4m3 moments with a power-of-two scale per 256 elements
+    (``stochastic``, ``seed``: the rounding of the second one). ``master_weights``: bfloat16
+    parameters get a float32 master copy (``refresh_masters`` rereads it after the parameters
+    were set from outside). ``wd_mul``: multiplier of ``weight_decay``. These and the
+    hyper-parameters may differ by group. ``max_grad_norm``: clips the gradients' global norm
+    over all groups, inside the step (the gradients themselves stay as they are);
+    ``skip_nonfinite`` then leaves a step out whose norm is not finite (its index still
+    counts). ``last_grad_norm`` is the norm of the last step, on the device."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, wd_mul: float = 1.0, state_bits: int = 32,
+                 master_weights: bool = False, stochastic: bool = True, seed: int = 0,
+                 max_grad_norm: Optional[float] = None, skip_nonfinite: bool = False):
+        defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
+                        wd_mul=wd_mul, state_bits=state_bits, master_weights=master_weights,
+                        stochastic=stochastic, seed=seed)
+        self._plans = {}
+        self.max_grad_norm = max_grad_norm
+        self.skip_nonfinite = skip_nonfinite
+        self.last_grad_norm = None
+        super().__init__(params, defaults)
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        if self.param_groups[-1]["state_bits"] not in (8, 32):
+            self.param_groups.pop()
+            raise ValueError("state_bits must be 8 or 32")
+
+    def __getstate__(self):
+        state = super().__getstate__()
+        state.update(max_grad_norm=self.max_grad_norm, skip_nonfinite=self.skip_nonfinite)
+        return state
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}
+        self.last_grad_norm = None
+
+    def load_state_dict(self, state_dict):
+        """As the base class's, except that states keep the dtypes they were saved with."""
+        super().load_state_dict(state_dict)
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        ps = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(ids, ps):
+            for k, v in state_dict["state"].get(i, {}).items():
+                if isinstance(v, torch.Tensor):
+                    self.state[p][k] = v.detach().clone().to(p.device)
+        self._plans = {}
+
+    def _init_state(self, p, group):
+        st = self.state[p]
+        st["step"] = 0
+        zeros = lambda shape, dt: torch.zeros(  # noqa: E731
+            shape, dtype=torch.uint8 if dt.itemsize == 1 else dt, device=p.device).view(dt)
+        if group["state_bits"] == 8:
+            blocks = -(-p.numel() // L.MUON_ADAMW_BLOCK)
+            for k in ("exp_avg", "exp_avg_sq"):
+                st[k] = zeros(p.shape, torch.float8_e4m3fn)
+                st[k + "_scale"] = zeros((blocks,), torch.float8_e8m0fnu)
+        else:
+            for k in ("exp_avg", "exp_avg_sq"):
+                st[k] = zeros(p.shape, torch.float32)
+        if group["master_weights"] and p.dtype == torch.bfloat16:
+            st["master"] = p.detach().float()
+
+    @torch.no_grad()
+    def refresh_masters(self):
+        """Sets the master copies to the parameters' present values."""
+        for p, st in self.state.items():
+            if "master" in st:
+                st["master"].copy_(p)
+
+    def _plan(self, gi, group, ps: List[torch.Tensor], grads):
+        states = [self.state[p] for p in ps]
+        key = [(p.data_ptr(), p.numel(), p.dtype, g.dtype, st["exp_avg"].data_ptr())
+               for p, g, st in zip(ps, grads, states)]
+        key.append(group["wd_mul"])
+        cached = self._plans.get(gi)
+        if cached is None or cached[0] != key:
+            small = "exp_avg_scale" in states[0]
+            plan = AdamWPlan([p.detach() for p in ps], [s["exp_avg"] for s in states],
+                             [s["exp_avg_sq"] for s in states], [g.dtype for g in grads],
+                             [s.get("master") for s in states],
+                             [s["exp_avg_scale"] for s in states] if small else None,
+                             [s["exp_avg_sq_scale"] for s in states] if small else None,
+                             [group["wd_mul"]] * len(ps))
+            cached = self._plans[gi] = (key, plan)
+        return cached[1]
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        todo = []
+        for gi, group in enumerate(self.param_groups):
+            ps = [p for p in group["params"] if p.grad is not None]
+            grads = [p.grad for p in ps]
+            for p, g in zip(ps, grads):
+                if not p.is_contiguous() or not g.is_contiguous():
+                    raise ValueError("AdamW needs contiguous parameters and gradients")
+                if "step" not in self.state[p]:
+                    self._init_state(p, group)
+            if ps:
+                todo.append((gi, group, ps, grads))
+        scale = None
+        if self.max_grad_norm is not None and todo:
+            every = [g for _, _, _, grads in todo for g in grads]
+            key = [(g.numel(), g.dtype, g.get_device()) for g in every]
+            cached = self._plans.get("norm")
+            if cached is None or cached[0] != key:
+                cached = self._plans["norm"] = (key, GradNormPlan(every))
+            self.last_grad_norm, scale = cached[1].norm(every, self.max_grad_norm)
+        for gi, group, ps, grads in todo:
+            plan = self._plan(gi, group, ps, grads)
+            at = [self.state[p]["step"] + 1 for p in ps]
+            for t in sorted(set(at)):
+                cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],
+                                        group["weight_decay"], t,
+                                        self.skip_nonfinite and scale is not None,
+                                        group["stochastic"], group["seed"])
+                mine = grads if len(set(at)) == 1 else [g if k == t else None
+                                                        for g, k in zip(grads, at)]
+                plan.step(mine, cfg, scale)
+            for p, t in zip(ps, at):
+                self.state[p]["step"] = t
+        return loss

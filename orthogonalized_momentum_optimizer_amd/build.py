@@ -28,7 +28,7 @@ PROBE_SOURCES = ["mfma_loop.hip"]
 
 SOURCES = ["plan.hip", "elementwise.hip", "ns_gemm_bf16.hip", "ns_sym256_bf16.hip",
            "ns_quad_bf16.hip", "ns_apply_bf16.hip", "ns_fused_bf16.hip", "ns_gemm_f32.hip",
-           "cautious_adam.hip", "noalloc.hip"]
+           "cautious_adam.hip", "noalloc.hip", "adamw.hip", "grad_norm.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

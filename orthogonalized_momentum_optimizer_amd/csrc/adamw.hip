@@ -1,0 +1,542 @@
+// AdamW over many tensors at once, with fp32 or 8-bit states: host side and kernels of the C
+// ABI in include/adamw.h.
+//
+// One pass over HBM either way: every buffer is read once and written once. Bytes per element:
+//   fp32 states   g + 2p + 16:    22 for bf16 p and g, 28 for fp32; 28 for bf16 with a master
+//   8-bit states  g + 2p + 4:     10 for bf16 p and g, 16 for fp32; 16 for bf16 with a master
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <vector>
+
+#include "adamw.h"
+#include "tensor_list.h"
+
+struct muon_adamw_plan {
+  std::vector<muon_adamw_tensor> tensors;
+  std::vector<muon::Range> ranges;   // the plan's buffers, ascending (all written)
+  std::vector<int> of[3][2];         // tensors of each (parameter mode, gradient dtype)
+  muon_adamw_state state = MUON_ADAMW_F32;
+};
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 4096;                     // elements per block
+constexpr int kMaxItems = 48;                    // tensors per launch (passed by value)
+constexpr int64_t kMaxBlocks = kMaxTensorElems / kChunk;  // per launch
+
+// Parameter modes: a bf16 parameter, an fp32 one, a bf16 one with an fp32 master copy.
+enum { kBf16 = 0, kF32 = 1, kMaster = 2 };
+
+struct Item {
+  void* p;
+  float* w;                                      // master
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* ms;                                   // scales of the 8-bit states
+  uint8_t* vs;
+  int64_t numel;
+  float lam;                                     // weight_decay * wd_mul
+};
+
+struct Step {
+  float lr, beta1, beta2, eps;
+  float inv_bc1;                                 // 1 / (1 - beta1^t)
+  float inv_sqrt_bc2;                            // 1 / sqrt(1 - beta2^t)
+  const float* grad_scale;
+  int skip_nonfinite;
+  int stochastic;
+  uint32_t key;
+};
+
+struct AdamwLaunch {
+  Item item[kMaxItems];
+  int first[64];                                 // first block of each; unused: INT_MAX
+  Step s;
+};
+
+// The gradient scale; false when the step is to be skipped.
+__device__ __forceinline__ bool read_scale(const Step& S, float& scale) {
+  scale = 1.f;
+  if (!S.grad_scale) return true;
+  scale = *S.grad_scale;
+  return !(S.skip_nonfinite && !(fabsf(scale) <= 3.402823466e38f));
+}
+
+// p <- p - lr (u + lam p) from the new m and sqrt(v)
+__device__ __forceinline__ float updated(const Step& S, float lam, float p, float m, float r) {
+  const float u = (m * S.inv_bc1) / fmaf(r, S.inv_sqrt_bc2, S.eps);
+  return fmaf(-S.lr, fmaf(lam, p, u), p);
+}
+
+// ---- fp32 states -----------------------------------------------------------------------------
+
+__device__ __forceinline__ void step_f32(const Step& S, float scale, float lam, float& p, float g,
+                                         float& m, float& v) {
+  g *= scale;
+  m = fmaf(S.beta1, m, (1.f - S.beta1) * g);
+  v = fmaf(S.beta2, v, (1.f - S.beta2) * (g * g));
+  p = updated(S, lam, p, m, sqrtf(v));
+}
+
+template <int PM, int GD>
+__global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L) {
+  constexpr int kVec = 8, kUnroll = kChunk / (kThreads * kVec);
+  constexpr int PD = PM == kBf16 ? 0 : 1;        // what p is read from
+  const int b = blockIdx.x;
+  const int q = find_tensor(L.first, b);
+  const Item& I = L.item[q];
+  float scale;
+  if (!read_scale(L.s, scale)) return;
+  const float lam = I.lam;
+  const int64_t n = I.numel;
+  const int64_t base = int64_t(b - L.first[q]) * kChunk;
+  void* const P = PM == kMaster ? I.w : I.p;
+  float* const M = static_cast<float*>(I.m);
+  float* const V = static_cast<float*>(I.v);
+  const int t = threadIdx.x;
+
+  if (base + kChunk <= n) {
+    float p[kUnroll][kVec], g[kUnroll][kVec], m[kUnroll][kVec], v[kUnroll][kVec];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = base + int64_t(u * kThreads + t) * kVec;
+      load_vec<PD>(P, i, p[u]);
+      load_vec<GD>(I.g, i, g[u]);
+      load_vec<1>(M, i, m[u]);
+      load_vec<1>(V, i, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = base + int64_t(u * kThreads + t) * kVec;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) step_f32(L.s, scale, lam, p[u][e], g[u][e], m[u][e], v[u][e]);
+      store_vec<PD>(P, i, p[u]);
+      if (PM == kMaster) store_vec<0>(I.p, i, p[u]);
+      store_vec<1>(M, i, m[u]);
+      store_vec<1>(V, i, v[u]);
+    }
+    return;
+  }
+  // the last chunk of a tensor, element by element
+  for (int64_t i = base + t; i < n; i += kThreads) {
+    float p = load_one<PD>(P, i), m = M[i], v = V[i];
+    step_f32(L.s, scale, lam, p, load_one<GD>(I.g, i), m, v);
+    store_one<PD>(P, i, p);
+    if (PM == kMaster) store_one<0>(I.p, i, p);
+    M[i] = m;
+    V[i] = v;
+  }
+}
+
+// ---- 8-bit states ----------------------------------------------------------------------------
+//
+// A block of 256 elements is 16 lanes x 16 elements: one row of the wavefront's data-parallel
+// primitives, so that the largest |x| of a block takes four rotations within the row and the
+// codes of a lane are one 16-byte access.
+
+constexpr int kLane = 16;                        // elements per lane
+
+template <int CTRL>
+__device__ __forceinline__ float row_rotate(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+
+// The largest of x over the lane's row of 16, in every lane. NaN only where all are.
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, row_rotate<0x128>(x));
+  x = fmaxf(x, row_rotate<0x124>(x));
+  x = fmaxf(x, row_rotate<0x122>(x));
+  return fmaxf(x, row_rotate<0x121>(x));
+}
+
+// The smallest scale byte b with top <= T * 2^(b - 127): top = 2^(E - 127) * f has b = E - 8,
+// or E - 7 if f is over T's significand 1 + 0x629146 / 2^23.
+__device__ __forceinline__ int scale_byte(float top) {
+  const int e = int((__float_as_uint(top) + (0x7fffffu - 0x629146u)) >> 23) - 8;
+  return max(e, 0);
+}
+__device__ __forceinline__ float scale_of(int b) {            // 2^(b - 127)
+  return __uint_as_float(b == 0 ? 0x00400000u : uint32_t(b) << 23);
+}
+__device__ __forceinline__ float inverse_scale_of(int b) {    // 2^(127 - b), b <= 247
+  return __uint_as_float(uint32_t(254 - b) << 23);
+}
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0xEB26D985u;
+  x = (x ^ (x >> 15)) * 0x4A08C6EDu;
+  return x ^ (x >> 16);
+}
+
+// 16 codes <-> floats. The hardware's conversions round to nearest even.
+__device__ __forceinline__ void decode(const u32x4 c, float scale, float (&x)[kLane]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[k]), false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[k]), true);
+    x[4 * k] = a[0] * scale;
+    x[4 * k + 1] = a[1] * scale;
+    x[4 * k + 2] = b[0] * scale;
+    x[4 * k + 3] = b[1] * scale;
+  }
+}
+__device__ __forceinline__ u32x4 encode(const float (&y)[kLane]) {
+  u32x4 c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], w, true);
+    c[k] = uint32_t(w);
+  }
+  return c;
+}
+
+// r's value in the format (0 <= y, in units of the scale). bits: what is added below the
+// format's last place before the cut, 20 bits wide; nearest: left to the conversion.
+template <bool NEAREST>
+__device__ __forceinline__ float held_r(float y, uint32_t bits) {
+  float z = y > 448.f ? 448.f : y;
+  if (!NEAREST) {
+    // below 2^-6 the format's values are multiples of 2^-9, as fp32's last 20 bits away from
+    // [2^-6, 2^-5)
+    const float shift = z < 0.015625f ? 0.015625f : 0.f;
+    z = __uint_as_float((__float_as_uint(z + shift) + bits) & 0xfff00000u) - shift;
+  }
+  return y > 0.f ? fmaxf(z, 0.001953125f) : y;   // NaN and 0 as they are
+}
+
+// The new m and v, each operation rounded to fp32 (the stored codes are then a function of the
+// inputs alone, whatever a compiler fuses).
+__device__ __forceinline__ void moments(const Step& S, float g, float& m, float& v) {
+#pragma clang fp contract(off)
+  const float a = S.beta1 * m, b = (1.f - S.beta1) * g;
+  m = a + b;
+  const float c = S.beta2 * v, gg = g * g;
+  const float d = (1.f - S.beta2) * gg;
+  v = c + d;
+}
+
+template <int PM, int GD, bool FULL>
+__device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float scale, int64_t i) {
+  constexpr int PD = PM == kBf16 ? 0 : 1;
+  const int64_t n = I.numel;
+  const int cnt = FULL ? kLane : int(min<int64_t>(max<int64_t>(n - i, 0), kLane));
+  void* const P = PM == kMaster ? I.w : I.p;
+  uint8_t* const M = static_cast<uint8_t*>(I.m);
+  uint8_t* const V = static_cast<uint8_t*>(I.v);
+  const int64_t blk = i / MUON_ADAMW_BLOCK;
+
+  float p[kLane], g[kLane], m[kLane], r[kLane];
+  u32x4 mc = {0, 0, 0, 0}, rc = {0, 0, 0, 0};
+  int mb = 0, rb = 0;
+  if (cnt > 0) {
+    mb = I.ms[blk];
+    rb = I.vs[blk];
+  }
+  if (cnt == kLane) {
+    load_vec<PD>(P, i, p);
+    load_vec<GD>(I.g, i, g);
+    mc = *reinterpret_cast<const u32x4*>(M + i);
+    rc = *reinterpret_cast<const u32x4*>(V + i);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) {
+      p[e] = g[e] = 0.f;
+      if (e < cnt) {
+        p[e] = load_one<PD>(P, i + e);
+        g[e] = load_one<GD>(I.g, i + e);
+        mc[e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
+        rc[e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
+      }
+    }
+  }
+  decode(mc, scale_of(mb), m);
+  decode(rc, scale_of(rb), r);
+
+  float mtop = 0.f, rtop = 0.f;
+#pragma unroll
+  for (int e = 0; e < kLane; ++e) {
+    float v = r[e] * r[e];
+    moments(S, g[e] * scale, m[e], v);
+    r[e] = sqrtf(v);
+    p[e] = updated(S, I.lam, p[e], m[e], r[e]);
+    mtop = fmaxf(mtop, fabsf(m[e]));
+    rtop = fmaxf(rtop, r[e]);
+  }
+  mb = scale_byte(row_max(mtop));
+  rb = scale_byte(row_max(rtop));
+  const float mi = inverse_scale_of(mb), ri = inverse_scale_of(rb);
+  const uint64_t pair = uint64_t(i) >> 1;
+  const uint32_t key = S.key ^ uint32_t(pair >> 32) * 0xEB26D985u;
+#pragma unroll
+  for (int e = 0; e < kLane; ++e) m[e] *= mi;
+  if (S.stochastic) {
+#pragma unroll
+    for (int e = 0; e < kLane; e += 2) {
+      const uint32_t h = mix32((uint32_t(pair) + e / 2) ^ key);
+      r[e] = held_r<false>(r[e] * ri, (h & 0xffffu) << 4 | 8u);
+      r[e + 1] = held_r<false>(r[e + 1] * ri, (h >> 16) << 4 | 8u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) r[e] = held_r<true>(r[e] * ri, 0);
+  }
+  mc = encode(m);
+  rc = encode(r);
+
+  if (cnt == kLane) {
+    store_vec<PD>(P, i, p);
+    if (PM == kMaster) store_vec<0>(I.p, i, p);
+    *reinterpret_cast<u32x4*>(M + i) = mc;
+    *reinterpret_cast<u32x4*>(V + i) = rc;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kLane; ++e)
+      if (e < cnt) {
+        store_one<PD>(P, i + e, p[e]);
+        if (PM == kMaster) store_one<0>(I.p, i + e, p[e]);
+        M[i + e] = uint8_t(mc[e >> 2] >> (8 * (e & 3)));
+        V[i + e] = uint8_t(rc[e >> 2] >> (8 * (e & 3)));
+      }
+  }
+  if ((threadIdx.x & 15) == 0 && cnt > 0) {
+    I.ms[blk] = uint8_t(mb);
+    I.vs[blk] = uint8_t(rb);
+  }
+}
+
+template <int PM, int GD>
+__global__ __launch_bounds__(kThreads) void adamw_8bit_kernel(const AdamwLaunch L) {
+  static_assert(kChunk == kThreads * kLane, "one vector per lane");
+  const int b = blockIdx.x;
+  const int q = find_tensor(L.first, b);
+  const Item& I = L.item[q];
+  float scale;
+  if (!read_scale(L.s, scale)) return;
+  const int64_t base = int64_t(b - L.first[q]) * kChunk;
+  const int64_t i = base + int64_t(threadIdx.x) * kLane;
+  if (base + kChunk <= I.numel) step_8bit<PM, GD, true>(I, L.s, scale, i);
+  else step_8bit<PM, GD, false>(I, L.s, scale, i);
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+typedef void (*AdamwKernel)(AdamwLaunch);
+
+AdamwKernel kernel_of(muon_adamw_state st, int pm, int gd) {
+  static const AdamwKernel f32[3][2] = {
+      {adamw_f32_kernel<kBf16, 0>, adamw_f32_kernel<kBf16, 1>},
+      {adamw_f32_kernel<kF32, 0>, adamw_f32_kernel<kF32, 1>},
+      {adamw_f32_kernel<kMaster, 0>, adamw_f32_kernel<kMaster, 1>}};
+  static const AdamwKernel e8[3][2] = {
+      {adamw_8bit_kernel<kBf16, 0>, adamw_8bit_kernel<kBf16, 1>},
+      {adamw_8bit_kernel<kF32, 0>, adamw_8bit_kernel<kF32, 1>},
+      {adamw_8bit_kernel<kMaster, 0>, adamw_8bit_kernel<kMaster, 1>}};
+  return (st == MUON_ADAMW_F32 ? f32 : e8)[pm][gd];
+}
+
+int check_tensor(const muon_adamw_tensor& T, int64_t i, muon_adamw_state state,
+                 std::vector<Range>& rs) {
+  if (T.numel < 0 || T.numel > kMaxTensorElems)
+    return fail(T.numel < 0 ? MUON_ERR_INVALID_ARG : MUON_ERR_UNSUPPORTED,
+                "tensor %lld: numel %lld outside [0, 2^35]", (long long)i, (long long)T.numel);
+  if (!dtype_known(T.param_dtype) || !dtype_known(T.grad_dtype))
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: unknown dtype (%d, %d)", (long long)i,
+                (int)T.param_dtype, (int)T.grad_dtype);
+  if (!std::isfinite(T.wd_mul))
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: wd_mul must be finite", (long long)i);
+  if (T.numel == 0) return MUON_OK;
+  const bool e8 = state == MUON_ADAMW_8BIT;
+  if (!T.param || !T.exp_avg || !T.exp_avg_sq)
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: param, exp_avg and exp_avg_sq must be non-NULL",
+                (long long)i);
+  if (e8 && (!T.exp_avg_scale || !T.exp_avg_sq_scale))
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: 8-bit states need both scale buffers",
+                (long long)i);
+  if (T.master && T.param_dtype != MUON_DT_BF16)
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: a master copy is for bf16 parameters",
+                (long long)i);
+  if (!is_aligned16(T.param) || !is_aligned16(T.master) || !is_aligned16(T.exp_avg) ||
+      !is_aligned16(T.exp_avg_sq))
+    return fail(MUON_ERR_INVALID_ARG, "tensor %lld: buffers must be 16-byte aligned", (long long)i);
+  auto add = [&](const void* p, size_t bytes) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    rs.push_back({lo, lo + bytes, true});
+  };
+  const size_t n = (size_t)T.numel, blocks = (n + MUON_ADAMW_BLOCK - 1) / MUON_ADAMW_BLOCK;
+  add(T.param, n * dtype_bytes(T.param_dtype));
+  if (T.master) add(T.master, n * 4);
+  add(T.exp_avg, e8 ? n : n * 4);
+  add(T.exp_avg_sq, e8 ? n : n * 4);
+  if (e8) {
+    add(T.exp_avg_scale, blocks);
+    add(T.exp_avg_sq_scale, blocks);
+  }
+  return MUON_OK;
+}
+
+int check_config(const muon_adamw_config* cfg) {
+  if (!cfg) return fail(MUON_ERR_INVALID_ARG, "cfg is NULL");
+  if (!std::isfinite(cfg->lr) || !std::isfinite(cfg->eps) || !std::isfinite(cfg->weight_decay))
+    return fail(MUON_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite");
+  if (cfg->eps < 0.f) return fail(MUON_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!(cfg->beta1 >= 0.f && cfg->beta1 < 1.f) || !(cfg->beta2 >= 0.f && cfg->beta2 < 1.f))
+    return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must lie in [0, 1)");
+  if (cfg->step < 1) return fail(MUON_ERR_INVALID_ARG, "step = %lld < 1", (long long)cfg->step);
+  if ((cfg->skip_nonfinite & ~1) || (cfg->stochastic & ~1))
+    return fail(MUON_ERR_INVALID_ARG, "skip_nonfinite and stochastic must be 0 or 1");
+  if (cfg->skip_nonfinite && !cfg->grad_scale)
+    return fail(MUON_ERR_INVALID_ARG, "skip_nonfinite needs grad_scale");
+  if (reinterpret_cast<uintptr_t>(cfg->grad_scale) & 3)
+    return fail(MUON_ERR_INVALID_ARG, "grad_scale must be 4-byte aligned");
+  return MUON_OK;
+}
+
+// Whether [lo, hi) meets one of the plan's buffers.
+bool meets(const std::vector<Range>& rs, uintptr_t lo, uintptr_t hi) {
+  auto it = std::upper_bound(rs.begin(), rs.end(), lo,
+                             [](uintptr_t x, const Range& r) { return x < r.hi; });
+  return it != rs.end() && it->lo < hi;
+}
+
+uint32_t key_of(uint64_t seed, int64_t step) {
+  uint64_t z = seed + (uint64_t)step * 0x1493FA689CA113ADull;
+  for (int k = 0; k < 2; ++k) z = (z ^ (z >> 32)) * 0xE9F8AC216EBC06F5ull;
+  return uint32_t(z ^ (z >> 32));
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+void muon_adamw_config_default(muon_adamw_config* cfg) {
+  if (!cfg) return;
+  *cfg = muon_adamw_config{};
+  cfg->lr = 1e-3f;
+  cfg->beta1 = 0.9f;
+  cfg->beta2 = 0.999f;
+  cfg->eps = 1e-8f;
+  cfg->weight_decay = 0.01f;
+  cfg->step = 1;
+  cfg->stochastic = 1;
+}
+
+int muon_adamw_plan_create(muon_adamw_plan** out, const muon_adamw_tensor* tensors, int64_t n,
+                           muon_adamw_state state) {
+  return c_entry([&]() -> int {
+    if (!out) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    if (n < 0) return fail(MUON_ERR_INVALID_ARG, "n = %lld < 0", (long long)n);
+    if (n > (int64_t(1) << 24))
+      return fail(MUON_ERR_UNSUPPORTED, "n = %lld: at most 2^24 tensors", (long long)n);
+    if (n > 0 && !tensors) return fail(MUON_ERR_INVALID_ARG, "tensors is NULL");
+    if (state != MUON_ADAMW_F32 && state != MUON_ADAMW_8BIT)
+      return fail(MUON_ERR_INVALID_ARG, "unknown state %d", (int)state);
+    muon_adamw_plan made;
+    made.state = state;
+    for (int64_t i = 0; i < n; ++i) {
+      const muon_adamw_tensor& T = tensors[i];
+      if (int st = check_tensor(T, i, state, made.ranges)) return st;
+      if (T.numel == 0) continue;
+      const int pm = T.master ? kMaster : T.param_dtype == MUON_DT_F32 ? kF32 : kBf16;
+      made.of[pm][T.grad_dtype == MUON_DT_F32].push_back((int)i);
+    }
+    if (int st = check_overlaps(made.ranges)) return st;   // sorts them
+    made.tensors.assign(tensors, tensors + n);
+    *out = new muon_adamw_plan(std::move(made));
+    return MUON_OK;
+  });
+}
+
+void muon_adamw_plan_destroy(muon_adamw_plan* plan) { delete plan; }
+
+int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64_t n,
+                    const muon_adamw_config* cfg, hipStream_t stream) {
+  return c_entry([&]() -> int {
+    if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+    if (n != (int64_t)plan->tensors.size())
+      return fail(MUON_ERR_INVALID_ARG, "n = %lld but the plan has %zu tensors", (long long)n,
+                  plan->tensors.size());
+    if (int st = check_config(cfg)) return st;
+    if (n > 0 && !grads) return fail(MUON_ERR_INVALID_ARG, "grads is NULL");
+    for (int64_t i = 0; i < n; ++i) {
+      const muon_adamw_tensor& T = plan->tensors[i];
+      if (!std::isfinite(cfg->weight_decay * T.wd_mul))
+        return fail(MUON_ERR_INVALID_ARG, "tensor %lld: weight_decay * wd_mul overflows",
+                    (long long)i);
+      if (T.numel == 0 || !grads[i]) continue;
+      if (!is_aligned16(grads[i]))
+        return fail(MUON_ERR_INVALID_ARG, "gradient %lld must be 16-byte aligned", (long long)i);
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
+      if (meets(plan->ranges, lo, lo + (size_t)T.numel * dtype_bytes(T.grad_dtype)))
+        return fail(MUON_ERR_INVALID_ARG, "gradient %lld overlaps a buffer of the plan",
+                    (long long)i);
+    }
+    if (cfg->grad_scale) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+      if (meets(plan->ranges, lo, lo + sizeof(float)))
+        return fail(MUON_ERR_INVALID_ARG, "grad_scale overlaps a buffer of the plan");
+    }
+
+    AdamwLaunch L;
+    L.s.lr = cfg->lr;
+    L.s.beta1 = cfg->beta1;
+    L.s.beta2 = cfg->beta2;
+    L.s.eps = cfg->eps;
+    const double t = (double)cfg->step;
+    L.s.inv_bc1 = (float)(1.0 / (1.0 - std::pow((double)cfg->beta1, t)));
+    L.s.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow((double)cfg->beta2, t)));
+    L.s.grad_scale = cfg->grad_scale;
+    L.s.skip_nonfinite = cfg->skip_nonfinite;
+    L.s.stochastic = cfg->stochastic;
+    L.s.key = key_of(cfg->seed, cfg->step);
+    for (int pm = 0; pm < 3; ++pm)
+      for (int gd = 0; gd < 2; ++gd) {
+        const AdamwKernel k = kernel_of(plan->state, pm, gd);
+        int count = 0;
+        int64_t blocks = 0;
+        auto flush = [&]() -> int {
+          if (count == 0) return MUON_OK;
+          for (int c = count; c < 64; ++c) L.first[c] = INT_MAX;
+          hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(kThreads), 0, stream, L);
+          const hipError_t e = hipGetLastError();
+          count = 0;
+          blocks = 0;
+          if (e != hipSuccess)
+            return fail(MUON_ERR_HIP, "launch of the AdamW kernel failed: %s",
+                        hipGetErrorString(e));
+          return MUON_OK;
+        };
+        for (int i : plan->of[pm][gd]) {
+          const muon_adamw_tensor& T = plan->tensors[i];
+          if (!grads[i]) continue;
+          const int64_t nb = (T.numel + kChunk - 1) / kChunk;
+          if (count == kMaxItems || blocks + nb > kMaxBlocks)
+            if (int st = flush()) return st;
+          Item& I = L.item[count];
+          I.p = T.param;
+          I.w = T.master;
+          I.g = grads[i];
+          I.m = T.exp_avg;
+          I.v = T.exp_avg_sq;
+          I.ms = T.exp_avg_scale;
+          I.vs = T.exp_avg_sq_scale;
+          I.numel = T.numel;
+          I.lam = cfg->weight_decay * T.wd_mul;
+          L.first[count++] = (int)blocks;
+          blocks += nb;
+        }
+        if (int st = flush()) return st;
+      }
+    return MUON_OK;
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,311 @@
+"""Host side of the AdamW step and the gradient norm: defaults, validation, refusals of the
+Python front end (no GPU needed; validation errors are raised before any HIP call). Calls that
+pass fake device addresses run only where no GPU is present."""
+import ctypes
+import math
+import os
+import subprocess
+
+import pytest
+import torch
+
+import orthogonalized_momentum_optimizer_amd as om
+from orthogonalized_momentum_optimizer_amd import _lib as L
+
+no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
+                                 reason="fake device addresses are only used without a GPU")
+BF16, F32 = L.MUON_DT_BF16, L.MUON_DT_F32
+BASE = 1 << 40                                   # fake device addresses, never dereferenced
+
+
+def entries(state=L.MUON_ADAMW_8BIT):
+    """Three tensors of 1000, 0 and 4096 elements, 1 MiB between buffers."""
+    out, at = [], BASE
+    for i, n in enumerate((1000, 0, 4096)):
+        ptr = [at + (k << 20) for k in range(6)]
+        at += 8 << 20
+        e = dict(param=ptr[0], master=None if i else ptr[1], exp_avg=ptr[2], exp_avg_sq=ptr[3],
+                 exp_avg_scale=ptr[4], exp_avg_sq_scale=ptr[5], numel=n, pdt=BF16, gdt=F32, wd=1.0)
+        if n == 0:
+            e.update(param=None, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None,
+                     exp_avg_sq_scale=None)
+        if state == L.MUON_ADAMW_F32:
+            e.update(exp_avg_scale=None, exp_avg_sq_scale=None)
+        out.append(e)
+    return out
+
+
+def create(ents, state=L.MUON_ADAMW_8BIT, n=None):
+    arr = L.make_adamw_tensors([tuple(e.values()) for e in ents])
+    return L.muon_adamw_plan_create(arr, len(ents) if n is None else n, state)
+
+
+def status_of(fn, *args, **kw):
+    with pytest.raises(L.MuonError) as e:
+        fn(*args, **kw)
+    return e.value.status, str(e.value)
+
+
+@pytest.mark.parametrize("state", [L.MUON_ADAMW_F32, L.MUON_ADAMW_8BIT])
+def test_plan_of_legal_tensors(state):
+    L.muon_adamw_plan_destroy(create(entries(state), state))
+    empty = L.muon_adamw_plan_create(None, 0, state)
+    L.muon_adamw_step(empty, None, 0, L.muon_adamw_config_default(), 0)   # no work, no HIP call
+    L.muon_adamw_plan_destroy(empty)
+
+
+def test_config_default():
+    c = L.muon_adamw_config_default()
+    assert [round(x, 9) for x in (c.lr, c.beta1, c.beta2, c.eps, c.weight_decay)] == [
+        0.001, 0.899999976, 0.999000013, 1e-8, 0.01]
+    assert (c.step, c.grad_scale, c.skip_nonfinite, c.stochastic, c.seed) == (1, None, 0, 1, 0)
+    L.lib().muon_adamw_config_default(None)
+    c = om.make_adamw_config(seed=-1, skip_nonfinite=True, stochastic=False, step=9)
+    assert (c.step, c.skip_nonfinite, c.stochastic, c.seed) == (9, 1, 0, 2 ** 64 - 1)
+
+
+INV, UNS, WS = L.MUON_ERR_INVALID_ARG, L.MUON_ERR_UNSUPPORTED, L.MUON_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(numel=-1), INV), (dict(numel=2 ** 35 + 1), UNS), (dict(pdt=7), INV), (dict(pdt=F32), INV), (dict(gdt=-1), INV),
+    (dict(wd=math.inf), INV), (dict(wd=math.nan), INV), (dict(param=None), INV),
+    (dict(exp_avg=None), INV), (dict(exp_avg_sq=None), INV), (dict(exp_avg_scale=None), INV),
+    (dict(exp_avg_sq_scale=None), INV), (dict(param=BASE + 8), INV), (dict(master=BASE + 4), INV),
+    (dict(exp_avg=BASE + (2 << 20) + 1), INV), (dict(exp_avg_sq=BASE + (2 << 20)), INV),
+    (dict(exp_avg_scale=BASE + (2 << 20) + 999), INV),     # the last byte of exp_avg
+    (dict(exp_avg_scale=BASE + (5 << 20) + 3), INV),       # its own 4 bytes meet the other scales
+], ids=str)
+def test_plan_rejects_tensors(change, status):
+    ents = entries()
+    ents[0].update(change)
+    got, msg = status_of(create, ents)
+    assert got == status, msg
+
+
+def test_scales_need_no_alignment():
+    ents = entries()
+    ents[0].update(exp_avg_scale=BASE + (2 << 20) + 1000)   # right behind exp_avg
+    L.muon_adamw_plan_destroy(create(ents))
+
+
+def test_plan_rejects_counts_and_states():
+    assert status_of(create, entries(), n=-1)[0] == INV
+    assert status_of(create, entries(), n=2 ** 60)[0] == UNS
+    assert status_of(create, entries(), state=2)[0] == INV
+    assert status_of(L.muon_adamw_plan_create, None, 2, 0)[0] == INV
+    assert L.lib().muon_adamw_plan_create(None, None, 0, 0) == INV
+    L.lib().muon_adamw_plan_destroy(None)
+
+
+@pytest.mark.parametrize("field,value", [
+    ("lr", math.nan), ("eps", -1e-9), ("eps", math.inf), ("weight_decay", math.inf),
+    ("beta1", 1.0), ("beta1", -0.1), ("beta2", 1.0), ("beta2", math.nan), ("step", 0),
+    ("step", -3), ("skip_nonfinite", 2), ("stochastic", -1), ("skip_nonfinite", 1),
+    ("grad_scale", BASE + 2), ("grad_scale", BASE), ("grad_scale", BASE + (8 << 21) + 8188)])
+def test_step_rejects_config(field, value):
+    plan = create(entries())
+    cfg = L.muon_adamw_config_default()
+    setattr(cfg, field, value)
+    grads = L.make_pointers([None] * 3)                     # no gradient: nothing to enqueue
+    status, msg = status_of(L.muon_adamw_step, plan, grads, 3, cfg, 0)
+    assert status == INV, msg
+    L.muon_adamw_plan_destroy(plan)
+
+
+def test_step_rejects_decay_overflow_and_null():
+    ents = entries()
+    ents[2]["wd"] = 3e38
+    plan = create(ents)
+    cfg = L.muon_adamw_config_default()
+    cfg.weight_decay = 10.0
+    grads = L.make_pointers([None] * 3)
+    assert status_of(L.muon_adamw_step, plan, grads, 3, cfg, 0)[0] == INV
+    cfg.weight_decay = 0.0
+    L.muon_adamw_step(plan, grads, 3, cfg, 0)               # every tensor left out: no HIP call
+    assert status_of(L.muon_adamw_step, plan, grads, 2, cfg, 0)[0] == INV
+    assert status_of(L.muon_adamw_step, plan, None, 3, cfg, 0)[0] == INV
+    assert status_of(L.muon_adamw_step, None, grads, 3, cfg, 0)[0] == INV
+    assert L.lib().muon_adamw_step(plan, grads, 3, None, 0) == INV
+    L.muon_adamw_plan_destroy(plan)
+
+
+@no_gpu_only
+@pytest.mark.parametrize("grad", [
+    BASE + (64 << 20) + 2,                                  # not 16-byte aligned
+    BASE,                                                   # the parameter
+    BASE + (2 << 20) - 16,                                  # its end meets exp_avg
+    BASE + (4 << 20),                                       # the scales
+    BASE + (16 << 20) + 8176])                              # the last elements of tensor 2
+def test_step_rejects_gradients(grad):
+    plan = create(entries())
+    grads = L.make_pointers([grad, None, None])
+    status, msg = status_of(L.muon_adamw_step, plan, grads, 3, L.muon_adamw_config_default(), 0)
+    assert status == INV and "gradient 0" in msg
+    L.muon_adamw_plan_destroy(plan)
+
+
+# ---- gradient norm ---------------------------------------------------------------------------
+
+def test_grad_plan_rejects():
+    for numel, dtype, status in (([-1], [F32], INV), ([2 ** 35 + 1], [F32], UNS), ([4], [2], INV)):
+        assert status_of(L.muon_grad_plan_create, numel, dtype)[0] == status
+    lib, out = L.lib(), ctypes.c_void_p()
+    one = (ctypes.c_int64 * 1)(4)
+    assert lib.muon_grad_plan_create(None, one, None, 1) == INV
+    assert lib.muon_grad_plan_create(ctypes.byref(out), one, None, 1) == INV
+    assert lib.muon_grad_plan_create(ctypes.byref(out), None, None, -1) == INV
+    assert lib.muon_grad_plan_create(ctypes.byref(out), one, (ctypes.c_int * 1)(0), 2 ** 50) == UNS
+    assert out.value is None
+    lib.muon_grad_plan_destroy(None)
+    with pytest.raises(ValueError):
+        L.muon_grad_plan_create([1], [F32, F32])
+
+
+def test_grad_plan_workspace():
+    assert L.muon_grad_plan_workspace_size(None) == 0
+    empty = L.muon_grad_plan_create([], [])
+    assert L.muon_grad_plan_workspace_size(empty) == 0
+    L.muon_grad_plan_destroy(empty)
+    for numel in ([1], [0, 0], [10 ** 6, 3], [2 ** 35] * 3):
+        plan = L.muon_grad_plan_create(numel, [BF16] * len(numel))
+        size = L.muon_grad_plan_workspace_size(plan)
+        assert 0 < size <= 1 << 20                          # a bounded number of partial sums
+        L.muon_grad_plan_destroy(plan)
+
+
+def norm_call(mutate=lambda a: None):
+    plan = L.muon_grad_plan_create([1000, 0, 64], [BF16, F32, F32])
+    size = L.muon_grad_plan_workspace_size(plan)
+    a = dict(plan=plan, grads=[BASE, None, BASE + (1 << 20)], n=3, max_norm=1.0, out=BASE + (2 << 20),
+             norms=BASE + (3 << 20), workspace=BASE + (4 << 20), workspace_bytes=size, stream=0)
+    mutate(a)
+    a["grads"] = None if a["grads"] is None else L.make_pointers(a["grads"])
+    try:
+        return status_of(L.muon_grad_norm, **a)
+    finally:
+        L.muon_grad_plan_destroy(plan)
+
+
+@no_gpu_only
+@pytest.mark.parametrize("change,status", [
+    (dict(plan=None), INV), (dict(n=2), INV), (dict(grads=None), INV), (dict(max_norm=-1.0), INV),
+    (dict(max_norm=math.nan), INV), (dict(out=None), INV), (dict(workspace=None), WS),
+    (dict(workspace=BASE + (4 << 20) + 8), WS), (dict(workspace_bytes=3), WS),
+    (dict(out=BASE + 1992), INV), (dict(norms=BASE + (2 << 20) + 4), INV),
+    (dict(workspace=BASE + (3 << 20)), INV), (dict(grads=[BASE + 2, None, None]), INV)], ids=str)
+def test_grad_norm_rejects(change, status):
+    got, msg = norm_call(lambda a: a.update(change))
+    assert got == status, msg
+
+
+@no_gpu_only
+def test_grad_scale_rejects():
+    plan = L.muon_grad_plan_create([1000, 64], [BF16, F32])
+    P = L.make_pointers
+    for grads, n, scale in (([BASE, BASE + 1984], 2, BASE + 4096), ([BASE, BASE], 2, BASE + 4096),
+                            ([BASE, None], 2, None), ([BASE, None], 1, BASE + 4096),
+                            ([BASE + 4, None], 2, BASE + 4096), ([BASE, None], 2, BASE + 1996)):
+        assert status_of(L.muon_grad_scale, plan, P(grads), n, scale, 0)[0] == INV
+    L.muon_grad_scale(plan, P([None, None]), 2, BASE, 0)     # nothing to do: no HIP call
+    L.muon_grad_plan_destroy(plan)
+
+
+# ---- the Python front end --------------------------------------------------------------------
+
+def cpu_args(n=300, small=False):
+    z = torch.zeros
+    if small:
+        b = -(-n // 256)
+        return dict(params=[z(n)], exp_avgs=[z(n, dtype=torch.uint8).view(torch.float8_e4m3fn)],
+                    exp_avg_sqs=[z(n, dtype=torch.uint8).view(torch.float8_e4m3fn)],
+                    grad_dtypes=[torch.float32],
+                    exp_avg_scales=[z(b, dtype=torch.uint8).view(torch.float8_e8m0fnu)],
+                    exp_avg_sq_scales=[z(b, dtype=torch.uint8).view(torch.float8_e8m0fnu)])
+    return dict(params=[z(n)], exp_avgs=[z(n)], exp_avg_sqs=[z(n)], grad_dtypes=[torch.float32])
+
+
+@pytest.mark.parametrize("small,change,error", [
+    (False, {}, ValueError),                                            # CPU tensors
+    (False, dict(exp_avgs=[]), ValueError),
+    (False, dict(exp_avgs=[torch.zeros(301)]), ValueError),
+    (False, dict(params=[torch.zeros(600)[::2]]), ValueError),
+    (False, dict(exp_avgs=[torch.zeros(300, dtype=torch.bfloat16)]), TypeError),
+    (False, dict(params=[torch.zeros(300, dtype=torch.float16)]), TypeError),
+    (False, dict(grad_dtypes=[torch.float64]), TypeError),
+    (False, dict(masters=[torch.zeros(300, dtype=torch.bfloat16)]), TypeError),
+    (False, dict(wd_muls=[1.0, 2.0]), ValueError),
+    (True, {}, ValueError),
+    (True, dict(exp_avg_scales=None), ValueError),
+    (True, dict(exp_avg_scales=[torch.zeros(2, dtype=torch.uint8)]), TypeError),
+    (True, dict(exp_avg_scales=[torch.zeros(3, dtype=torch.uint8).view(torch.float8_e8m0fnu)]),
+     ValueError),
+    (True, dict(exp_avg_sqs=[torch.zeros(300)]), TypeError),
+], ids=str)
+def test_adamw_plan_refuses(small, change, error):
+    with pytest.raises(error):
+        om.AdamWPlan(**{**cpu_args(small=small), **change})
+
+
+def test_cpu_tensors_are_refused_not_stepped():
+    p = torch.nn.Parameter(torch.ones(5))
+    p.grad = torch.ones(5)
+    for fn in (lambda: om.grad_norm([p.grad]), lambda: om.clip_grad_norm_([p], 1.0),
+               lambda: om.AdamW([p]).step(), lambda: om.AdamW([p], state_bits=8).step()):
+        with pytest.raises(ValueError):
+            fn()
+    assert torch.equal(p.detach(), torch.ones(5)) and torch.equal(p.grad, torch.ones(5))
+
+
+def test_optimizer_options():
+    p = [torch.nn.Parameter(torch.ones(5)) for _ in range(2)]
+    with pytest.raises(ValueError):
+        om.AdamW(p, state_bits=16)
+    opt = om.AdamW([{"params": p[:1], "state_bits": 8}, {"params": p[1:], "wd_mul": 0.0}],
+                   max_grad_norm=1.0, seed=5)
+    assert [g["state_bits"] for g in opt.param_groups] == [8, 32]
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.ones(2))], "state_bits": 4})
+    assert len(opt.param_groups) == 2
+    opt.step()                                    # no gradients: nothing to do
+    assert opt.last_grad_norm is None
+
+
+def test_state_dict_keeps_the_states_dtypes():
+    def make():
+        p = [torch.nn.Parameter(torch.randn(300).to(torch.bfloat16)) for _ in range(2)]
+        opt = om.AdamW([{"params": p[:1], "state_bits": 8}, {"params": p[1:]}], master_weights=True)
+        for g in opt.param_groups:
+            opt._init_state(g["params"][0], g)
+        return p, opt
+    p, opt = make()
+    for st in opt.state.values():
+        st["step"] = 7
+        for k, v in st.items():
+            if torch.is_tensor(v):
+                raw = v.view(torch.uint8)
+                raw.copy_(torch.randint(0, 100, raw.shape, dtype=torch.uint8))
+    _, other = make()
+    other.load_state_dict(opt.state_dict())
+    for a, b in zip(opt.state.values(), other.state.values()):
+        assert b["step"] == 7 and a.keys() == b.keys()
+        for k, v in a.items():
+            if torch.is_tensor(v):
+                assert b[k].dtype == v.dtype and b[k].data_ptr() != v.data_ptr()
+                assert torch.equal(b[k].view(torch.uint8), v.view(torch.uint8))
+    assert opt.state[p[0]]["exp_avg"].dtype == torch.float8_e4m3fn
+    assert opt.state[p[1]]["exp_avg"].dtype == opt.state[p[0]]["master"].dtype == torch.float32
+
+
+def test_c_program_uses_the_abi(tmp_path):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    exe = tmp_path / "adamw_check"
+    pkg = os.path.dirname(L.LIB_PATH)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic",
+                    "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(root, "include"), "-isystem",
+                    os.path.join(rocm, "include"), os.path.join(root, "tests", "c_abi", "adamw_check.c"),
+                    "-o", str(exe), "-L", pkg, "-lmuon", f"-Wl,-rpath,{pkg}",
+                    f"-Wl,-rpath,{rocm}/lib", "-L", f"{rocm}/lib", "-lamdhip64"], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "abi ok" in r.stdout, r.stdout + r.stderr
