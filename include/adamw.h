@@ -39,9 +39,9 @@
  * Elements of equal index in different tensors draw the same bits.
  *
  * NaN and infinities are propagated and never leave their tensor. In the 8-bit form a NaN
- * stays NaN in m and v; an infinite m is held as NaN, an infinite v as the largest value of the
- * format, and an infinity takes its block's scale to the largest, so that the block's other
- * elements lose their state. cfg->skip_nonfinite is the guard against both.
+ * stays NaN in m and v; an infinite m is held as NaN and takes its block's scale to the
+ * largest, so that the block's other m become 0; a v beyond fp32's range is held as its largest
+ * value. cfg->skip_nonfinite is the guard against both. An eps below 2^-126 counts as 0.
  *
  * Conventions are those of muon.h: device buffers on the current HIP device, contiguous, owned
  * by the caller, 16-byte aligned base addresses (the scales' need no alignment); work enqueued

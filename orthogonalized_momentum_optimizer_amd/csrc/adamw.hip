@@ -66,9 +66,11 @@ __device__ __forceinline__ bool read_scale(const Step& S, float& scale) {
   return !(S.skip_nonfinite && !(fabsf(scale) <= 3.402823466e38f));
 }
 
-// p <- p - lr (u + lam p) from the new m and sqrt(v)
+// p <- p - lr (u + lam p) from the new m and sqrt(v). The reciprocal is the hardware's, off by at
+// most one unit in the last place: its argument is 0 or at least 2^-75 (the root of the smallest
+// fp32), so that no subnormal enters it. A division takes ten instructions more.
 __device__ __forceinline__ float updated(const Step& S, float lam, float p, float m, float r) {
-  const float u = (m * S.inv_bc1) / fmaf(r, S.inv_sqrt_bc2, S.eps);
+  const float u = (m * S.inv_bc1) * __builtin_amdgcn_rcpf(fmaf(r, S.inv_sqrt_bc2, S.eps));
   return fmaf(-S.lr, fmaf(lam, p, u), p);
 }
 
@@ -162,9 +164,6 @@ __device__ __forceinline__ int scale_byte(float top) {
 __device__ __forceinline__ float scale_of(int b) {            // 2^(b - 127)
   return __uint_as_float(b == 0 ? 0x00400000u : uint32_t(b) << 23);
 }
-__device__ __forceinline__ float inverse_scale_of(int b) {    // 2^(127 - b), b <= 247
-  return __uint_as_float(uint32_t(254 - b) << 23);
-}
 
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0xEB26D985u;
@@ -172,41 +171,57 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// 16 codes <-> floats. The hardware's conversions round to nearest even.
+// 16 codes <-> floats, by the hardware's scaled conversions: exact one way, to nearest even or
+// stochastically the other (up with the probability of what is cut off: the upper 20 of the 32
+// random bits are added below the format's last place). Measured over all codes and scales and
+// over random values, subnormals of the format included: bit by bit what adamw.h defines.
 __device__ __forceinline__ void decode(const u32x4 c, float scale, float (&x)[kLane]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[k]), false);
-    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[k]), true);
-    x[4 * k] = a[0] * scale;
-    x[4 * k + 1] = a[1] * scale;
-    x[4 * k + 2] = b[0] * scale;
-    x[4 * k + 3] = b[1] * scale;
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, true);
+    x[4 * k] = a[0];
+    x[4 * k + 1] = a[1];
+    x[4 * k + 2] = b[0];
+    x[4 * k + 3] = b[1];
   }
 }
-__device__ __forceinline__ u32x4 encode(const float (&y)[kLane]) {
+__device__ __forceinline__ u32x4 encode(const float (&x)[kLane], float scale) {
   u32x4 c;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], w, true);
+    i16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k], x[4 * k + 1], scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k + 2], x[4 * k + 3], scale, true);
+    c[k] = __builtin_bit_cast(uint32_t, w);
+  }
+  return c;
+}
+// Elements 2j and 2j + 1 take the halves of h(j ^ key): 16 random bits, then half of one.
+__device__ __forceinline__ u32x4 encode_stochastic(const float (&x)[kLane], float scale,
+                                                   uint32_t pair, uint32_t key) {
+  u32x4 c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t h0 = mix32((pair + 2 * k) ^ key), h1 = mix32((pair + 2 * k + 1) ^ key);
+    int w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k], h0 << 16 | 0x8000u, scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k + 1], (h0 & 0xffff0000u) | 0x8000u, scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k + 2], h1 << 16 | 0x8000u, scale, 2);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k + 3], (h1 & 0xffff0000u) | 0x8000u, scale, 3);
     c[k] = uint32_t(w);
   }
   return c;
 }
 
-// r's value in the format (0 <= y, in units of the scale). bits: what is added below the
-// format's last place before the cut, 20 bits wide; nearest: left to the conversion.
-template <bool NEAREST>
-__device__ __forceinline__ float held_r(float y, uint32_t bits) {
-  float z = y > 448.f ? 448.f : y;
-  if (!NEAREST) {
-    // below 2^-6 the format's values are multiples of 2^-9, as fp32's last 20 bits away from
-    // [2^-6, 2^-5)
-    const float shift = z < 0.015625f ? 0.015625f : 0.f;
-    z = __uint_as_float((__float_as_uint(z + shift) + bits) & 0xfff00000u) - shift;
-  }
-  return y > 0.f ? fmaxf(z, 0.001953125f) : y;   // NaN and 0 as they are
+// sqrt(v) rounded to nearest, for v = 0 and 2^-101 <= v < 2^128: one step of Newton's method from
+// the reciprocal root, whose residual v - s^2 is exact there. Compared with the compiler's sqrt
+// over every significand at even and odd exponents: equal (its own sequence, which also takes
+// the rest of the range, is twice as long, and the kernel is bound by instructions).
+__device__ __forceinline__ float root(float v) {
+  const float q = __builtin_amdgcn_rsqf(v + 0x1p-126f);       // v itself, but for 0
+  const float s = v * q;
+  return fmaf(fmaf(-s, s, v) * 0.5f, q, s);
 }
 
 // The new m and v, each operation rounded to fp32 (the stored codes are then a function of the
@@ -257,36 +272,43 @@ __device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float sc
   decode(mc, scale_of(mb), m);
   decode(rc, scale_of(rb), r);
 
-  float mtop = 0.f, rtop = 0.f;
+  float mtop = 0.f, vtop = 0.f;
+  uint32_t vlow = ~0u;                           // the smallest v over 0, less one unit
 #pragma unroll
   for (int e = 0; e < kLane; ++e) {
     float v = r[e] * r[e];
     moments(S, g[e] * scale, m[e], v);
-    r[e] = sqrtf(v);
-    p[e] = updated(S, I.lam, p[e], m[e], r[e]);
+    r[e] = v;
     mtop = fmaxf(mtop, fabsf(m[e]));
-    rtop = fmaxf(rtop, r[e]);
+    vtop = fmaxf(vtop, v);
+    vlow = min(vlow, __float_as_uint(v) - 1u);
   }
-  mb = scale_byte(row_max(mtop));
-  rb = scale_byte(row_max(rtop));
-  const float mi = inverse_scale_of(mb), ri = inverse_scale_of(rb);
-  const uint64_t pair = uint64_t(i) >> 1;
-  const uint32_t key = S.key ^ uint32_t(pair >> 32) * 0xEB26D985u;
+  // rare, and the whole wave's: a v that root() does not take
+  const bool wide = __any(vlow < 0x0d000000u - 1u || vtop > 3.402823466e38f);
+  if (wide) {
 #pragma unroll
-  for (int e = 0; e < kLane; ++e) m[e] *= mi;
-  if (S.stochastic) {
-#pragma unroll
-    for (int e = 0; e < kLane; e += 2) {
-      const uint32_t h = mix32((uint32_t(pair) + e / 2) ^ key);
-      r[e] = held_r<false>(r[e] * ri, (h & 0xffffu) << 4 | 8u);
-      r[e + 1] = held_r<false>(r[e + 1] * ri, (h >> 16) << 4 | 8u);
-    }
+    for (int e = 0; e < kLane; ++e) r[e] = sqrtf(r[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) r[e] = held_r<true>(r[e] * ri, 0);
+    for (int e = 0; e < kLane; ++e) r[e] = root(r[e]);
   }
-  mc = encode(m);
-  rc = encode(r);
+#pragma unroll
+  for (int e = 0; e < kLane; ++e) p[e] = updated(S, I.lam, p[e], m[e], r[e]);
+  mb = scale_byte(row_max(mtop));
+  // the largest r is the largest v's root; an infinite v is held as the largest finite one
+  rb = scale_byte(sqrtf(fminf(row_max(vtop), 3.402823466e38f)));
+  const float ms = scale_of(mb), rs = scale_of(rb);
+  const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, 0x1.fffffep63f);
+#pragma unroll
+  for (int e = 0; e < kLane; ++e)                // NaN and 0 as they are
+    r[e] = r[e] > 0.f ? __builtin_amdgcn_fmed3f(r[e], low, high) : r[e];
+  mc = encode(m, ms);
+  if (S.stochastic) {
+    const uint64_t pair = uint64_t(i) >> 1;
+    rc = encode_stochastic(r, rs, uint32_t(pair), S.key ^ uint32_t(pair >> 32) * 0xEB26D985u);
+  } else {
+    rc = encode(r, rs);
+  }
 
   if (cnt == kLane) {
     store_vec<PD>(P, i, p);

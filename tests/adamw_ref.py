@@ -50,10 +50,11 @@ def step_codes(g, mc, ms, rc, rs, beta1, beta2, seed, step, stochastic, grad_sca
         m = b1 * m + (F(1) - b1) * g
         v = b2 * (r * r) + (F(1) - b2) * (g * g)
         r = np.sqrt(v)
+        top = np.sqrt(np.finfo(np.float32).max)              # an infinite v is held as the largest
         assert m.dtype == r.dtype == np.float32
-        mb, rb = scale_bytes(m), scale_bytes(r)
+        mb, rb = scale_bytes(m), scale_bytes(np.minimum(r, top))
         y = m * np.ldexp(F(1), 127 - mb.astype(np.int32)).astype(np.float32)[:, None]
-        z = r * np.ldexp(F(1), 127 - rb.astype(np.int32)).astype(np.float32)[:, None]
+        z = np.minimum(r, top) * np.ldexp(F(1), 127 - rb.astype(np.int32)).astype(np.float32)[:, None]
         w = np.minimum(z, F(448))
         if stochastic:
             bits = oa.rounding_bits(np.arange(w.size), seed, step).reshape(w.shape)
