@@ -46,10 +46,10 @@
  * Conventions are those of muon.h: device buffers on the current HIP device, contiguous, owned
  * by the caller, 16-byte aligned base addresses (the scales' need no alignment); work enqueued
  * on `stream` without synchronising; arguments validated on the host before anything is
- * enqueued. A step allocates nothing and needs no workspace, and a plan is not changed by a
- * step: steps on one plan may be called from several host threads, but the buffers they update
- * are the plan's, so that the steps themselves must be ordered on the device. A captured step
- * replays with the cfg it was captured with, step index and seed included.
+ * enqueued. A step allocates nothing, and a plan is not changed by a step: steps on one plan
+ * may be called from several host threads, but the buffers they update are the plan's, so that
+ * the steps themselves must be ordered on the device. A captured step replays with the cfg it
+ * was captured with, step index and seed included.
  */
 #ifndef MUON_ADAMW_H
 #define MUON_ADAMW_H
@@ -121,6 +121,17 @@ void muon_adamw_config_default(muon_adamw_config *cfg);
  * *out owns the plan (release it with muon_adamw_plan_destroy); on failure *out is NULL. */
 int muon_adamw_plan_create(muon_adamw_plan **out, const muon_adamw_tensor *tensors, int64_t n,
                            muon_adamw_state state);
+
+/* Bytes of the plan's device table (what a step reads of the tensors but the gradients'
+ * addresses). 0 for a NULL plan and one without elements. */
+size_t muon_adamw_plan_table_size(const muon_adamw_plan *plan);
+
+/* Fills the table, 16-byte aligned device memory of the caller's that must stay allocated and
+ * untouched as long as the plan is used, by work on `stream`; steps on other streams have to be
+ * ordered behind it. Needed once before the plan's first step (unless its table size is 0). Not
+ * for a stream under capture: the table would first be filled by the graph's replay. */
+int muon_adamw_plan_upload(muon_adamw_plan *plan, void *table, size_t table_bytes,
+                           hipStream_t stream);
 
 /* One AdamW step over the plan's tensors with gradients grads[0..n-1] (n the plan's count;
  * grads[i] of tensor i's grad_dtype, read only, may be shared between tensors, must not

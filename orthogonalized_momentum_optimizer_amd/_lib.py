@@ -35,6 +35,7 @@ EXPORTED = (
     "muon_adam_config_default", "muon_cautious_adam_step", "muon_step_noalloc",
     "muon_plan_set_concurrency", "muon_plan_set_fused",
     "muon_adamw_config_default", "muon_adamw_plan_create", "muon_adamw_step",
+    "muon_adamw_plan_table_size", "muon_adamw_plan_upload",
     "muon_adamw_plan_destroy", "muon_grad_plan_create", "muon_grad_plan_workspace_size",
     "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
 )
@@ -137,6 +138,23 @@ class muon_adamw_config(ctypes.Structure):
 
 
 _lib = None
+_args = None
+
+
+def tensor_addresses(tensors, numels, dtypes, device: int):
+    """The addresses of a list of tensors (None: 0) as a ctypes array, or the index of the first
+    one that is not a contiguous tensor of its ``numels`` and ``dtypes`` entry on ``device``.
+    ``numels``, ``dtypes``: ctypes arrays of int64 and of muon_dtype as int32."""
+    global _args
+    if _args is None:
+        try:
+            from . import _tensor_args as _args
+        except ImportError as e:
+            raise RuntimeError("_tensor_args.so is missing: build it with `python -m "
+                               "orthogonalized_momentum_optimizer_amd.build`") from e
+    out = (ctypes.c_void_p * len(numels))()
+    bad = _args.addresses(tensors, numels, dtypes, device, out)
+    return out if bad < 0 else bad
 
 
 def lib() -> ctypes.CDLL:
@@ -190,6 +208,10 @@ def lib() -> ctypes.CDLL:
     L.muon_adamw_step.argtypes = [vp, ctypes.POINTER(vp), i64,
                                   ctypes.POINTER(muon_adamw_config), vp]
     L.muon_adamw_step.restype = ctypes.c_int
+    L.muon_adamw_plan_table_size.argtypes = [vp]
+    L.muon_adamw_plan_table_size.restype = sz
+    L.muon_adamw_plan_upload.argtypes = [vp, vp, sz, vp]
+    L.muon_adamw_plan_upload.restype = ctypes.c_int
     L.muon_adamw_plan_destroy.argtypes = [vp]
     L.muon_adamw_plan_destroy.restype = None
     L.muon_grad_plan_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(i64),
@@ -351,6 +373,14 @@ def muon_adamw_plan_create(tensors, n: int, state: int) -> int:
     plan = ctypes.c_void_p()
     _check(lib().muon_adamw_plan_create(ctypes.byref(plan), tensors, n, int(state)))
     return plan.value
+
+
+def muon_adamw_plan_table_size(plan: int) -> int:
+    return int(lib().muon_adamw_plan_table_size(plan))
+
+
+def muon_adamw_plan_upload(plan: int, table: int, table_bytes: int, stream: int) -> None:
+    _check(lib().muon_adamw_plan_upload(plan, table, table_bytes, stream))
 
 
 def muon_adamw_step(plan: int, grads, n: int, cfg: muon_adamw_config, stream: int) -> None:

@@ -9,7 +9,9 @@ libmuon.so.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import math
+import operator
 from typing import Iterable, List, Optional, Sequence, Union
 
 import torch
@@ -17,7 +19,7 @@ import torch
 from . import _lib as L
 from .optim import dtype_code
 
-_Tensor = torch.Tensor
+_NOTHING = contextlib.nullcontext()
 
 
 def make_adamw_config(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
@@ -47,61 +49,46 @@ class _TensorList:
     """The device and gradient layout shared by the two plans."""
 
     def _set_list(self, device, numels, dtypes):
+        n = len(numels)
         self.device = device
-        self._numels = [int(x) for x in numels]
-        self._dtypes = list(dtypes)
-        self._index = [device.index] * len(self._numels)
+        self._numels = (ctypes.c_int64 * n)(*numels)
+        self._dtypes = (ctypes.c_int32 * n)(*[dtype_code(d) for d in dtypes])
 
     def _pointers(self, grads: Sequence[Optional[torch.Tensor]]):
         """The gradients' addresses, after checking them against the plan."""
+        n = len(self._numels)
         if not isinstance(grads, (list, tuple)):
             grads = list(grads)
-        n = len(self._numels)
         if len(grads) != n:
             raise ValueError(f"expected {n} gradients, got {len(grads)}")
-        try:
-            ptrs = list(map(_Tensor.data_ptr, grads))
-        except TypeError:
-            return self._pointers_with_none(grads)
-        if (list(map(_Tensor.numel, grads)) != self._numels
-                or [g.dtype for g in grads] != self._dtypes
-                or list(map(_Tensor.get_device, grads)) != self._index
-                or not all(map(_Tensor.is_contiguous, grads))):
-            for i, g in enumerate(grads):
-                self._check_grad(i, g)
-        return L.make_pointers(ptrs)
-
-    def _pointers_with_none(self, grads):
-        for i, g in enumerate(grads):
-            if g is not None:
-                self._check_grad(i, g)
-        return L.make_pointers([None if g is None else g.data_ptr() for g in grads])
-
-    def _check_grad(self, i, g):
-        if not isinstance(g, _Tensor):
-            raise TypeError(f"gradient {i}: a tensor or None expected")
-        if g.numel() != self._numels[i] or not g.is_contiguous() or g.device != self.device:
-            raise ValueError(f"gradient {i}: a contiguous tensor of {self._numels[i]} elements "
+        out = L.tensor_addresses(grads, self._numels, self._dtypes, self.device.index)
+        if not isinstance(out, int):
+            return out
+        g = grads[out]
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"gradient {out}: a tensor or None expected")
+        if g.numel() != self._numels[out] or not g.is_contiguous() or g.device != self.device:
+            raise ValueError(f"gradient {out}: a contiguous tensor of {self._numels[out]} elements "
                              f"on {self.device} expected")
-        if g.dtype != self._dtypes[i]:
-            raise TypeError(f"gradient {i}: {self._dtypes[i]} expected, got {g.dtype}")
+        raise TypeError(f"gradient {out}: a dtype other than the plan's ({g.dtype})")
 
     def _check_scalar(self, name, x):
         if x.numel() != 1 or x.dtype != torch.float32 or x.device != self.device:
             raise ValueError(f"{name} must be one float32 on {self.device}")
 
-    @contextlib.contextmanager
     def _on(self, stream):
-        """The plan's device as the current one, and ``stream`` (or the current stream) as its
-        current stream; yields its handle."""
-        with contextlib.ExitStack() as stack:
-            if torch.cuda.current_device() != self.device.index:
-                stack.enter_context(torch.cuda.device(self.device))
-            if stream is not None:
-                if stream.device != self.device:
-                    raise ValueError(f"the stream must be one of {self.device}")
-                stack.enter_context(torch.cuda.stream(stream))
-            yield torch.cuda.current_stream(self.device).cuda_stream
+        """A context with the plan's device as the current one and ``stream`` (or the current
+        stream) as its current stream."""
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError(f"the stream must be one of {self.device}")
+            return torch.cuda.stream(stream)
+        if torch.cuda.current_device() != self.device.index:
+            return torch.cuda.device(self.device)
+        return _NOTHING
+
+    def _stream(self):
+        return torch.cuda.current_stream(self.device).cuda_stream
 
 
 class AdamWPlan(_TensorList):
@@ -161,9 +148,18 @@ class AdamWPlan(_TensorList):
                             wd_muls[i]))
         self._set_list(_one_device(held), [p.numel() for p in params], grad_dtypes)
         self.state_bits = 8 if small else 32
-        self._held = held
         self.handle = L.muon_adamw_plan_create(L.make_adamw_tensors(entries) if n else None, n,
                                                L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
+        self._held = held
+        size = L.muon_adamw_plan_table_size(self.handle)
+        if size:
+            with self._on(None):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("create the plan before the capture (AdamW: take a step "
+                                       "before it)")
+                self._table = torch.empty(size, dtype=torch.uint8, device=self.device)
+                L.muon_adamw_plan_upload(self.handle, self._table.data_ptr(), size, self._stream())
+                torch.cuda.current_stream(self.device).synchronize()   # steps on any stream
 
     def step(self, grads: Sequence[Optional[torch.Tensor]], cfg: L.muon_adamw_config,
              grad_scale: Optional[torch.Tensor] = None,
@@ -175,8 +171,8 @@ class AdamWPlan(_TensorList):
             self._check_scalar("grad_scale", grad_scale)
             cfg = L.muon_adamw_config.from_buffer_copy(cfg)
             cfg.grad_scale = grad_scale.data_ptr()
-        with self._on(stream) as handle:
-            L.muon_adamw_step(self.handle, ptrs, len(self._numels), cfg, handle)
+        with self._on(stream):
+            L.muon_adamw_step(self.handle, ptrs, len(ptrs), cfg, self._stream())
 
     def close(self):
         if getattr(self, "handle", None):
@@ -198,7 +194,7 @@ class GradNormPlan(_TensorList):
         self.handle = None
         grads = list(grads)
         self._set_list(_one_device(grads), [g.numel() for g in grads], [g.dtype for g in grads])
-        self.handle = L.muon_grad_plan_create(self._numels, [dtype_code(d) for d in self._dtypes])
+        self.handle = L.muon_grad_plan_create(list(self._numels), list(self._dtypes))
         self.ws_bytes = L.muon_grad_plan_workspace_size(self.handle)
 
     def norm(self, grads: Sequence[Optional[torch.Tensor]], max_norm: float = math.inf,
@@ -208,16 +204,15 @@ class GradNormPlan(_TensorList):
         finite. A gradient that is None counts as zero. The workspace belongs to the call."""
         ptrs = self._pointers(grads)
         n = len(self._numels)
-        with self._on(stream) as handle:
+        with self._on(stream):
             out = torch.empty(2 + (n if per_tensor else 0), dtype=torch.float32, device=self.device)
             ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             base = out.data_ptr()
             L.muon_grad_norm(self.handle, ptrs, n, max_norm, base,
                              base + 8 if per_tensor and n else None, ws.data_ptr() or None,
-                             self.ws_bytes, handle)
-        if per_tensor:
-            return out[0], out[1], out[2:]
-        return out[0], out[1]
+                             self.ws_bytes, self._stream())
+        norm, scale = out[:2].unbind()
+        return (norm, scale, out[2:]) if per_tensor else (norm, scale)
 
     def scale_(self, grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -225,8 +220,8 @@ class GradNormPlan(_TensorList):
         is 1 nothing is read or written."""
         ptrs = self._pointers(grads)
         self._check_scalar("scale", scale)
-        with self._on(stream) as handle:
-            L.muon_grad_scale(self.handle, ptrs, len(self._numels), scale.data_ptr(), handle)
+        with self._on(stream):
+            L.muon_grad_scale(self.handle, ptrs, len(ptrs), scale.data_ptr(), self._stream())
 
     def close(self):
         if getattr(self, "handle", None):
@@ -337,21 +332,31 @@ class AdamW(torch.optim.Optimizer):
                 st["master"].copy_(p)
 
     def _plan(self, gi, group, ps: List[torch.Tensor], grads):
-        states = [self.state[p] for p in ps]
-        key = [(p.data_ptr(), p.numel(), p.dtype, g.dtype, st["exp_avg"].data_ptr())
-               for p, g, st in zip(ps, grads, states)]
-        key.append(group["wd_mul"])
+        """The group's plan and the states of ``ps``. A plan is kept while the parameters, their
+        addresses, the gradients' dtypes and the decay's multiplier stay."""
         cached = self._plans.get(gi)
-        if cached is None or cached[0] != key:
-            small = "exp_avg_scale" in states[0]
-            plan = AdamWPlan([p.detach() for p in ps], [s["exp_avg"] for s in states],
-                             [s["exp_avg_sq"] for s in states], [g.dtype for g in grads],
-                             [s.get("master") for s in states],
-                             [s["exp_avg_scale"] for s in states] if small else None,
-                             [s["exp_avg_sq_scale"] for s in states] if small else None,
-                             [group["wd_mul"]] * len(ps))
-            cached = self._plans[gi] = (key, plan)
-        return cached[1]
+        if cached is not None:
+            plan, of, wd_mul, states, numels, pdt, gdt, at = cached
+            if (len(of) == len(ps) and all(map(operator.is_, of, ps)) and wd_mul == group["wd_mul"]
+                    and gdt == [g.dtype for g in grads]):
+                now = L.tensor_addresses(ps, numels, pdt, plan.device.index)
+                if not isinstance(now, int) and bytes(now) == at:
+                    return plan, states
+        states = [self.state[p] for p in ps]
+        gdt = [g.dtype for g in grads]
+        small = "exp_avg_scale" in states[0]
+        plan = AdamWPlan([p.detach() for p in ps], [s["exp_avg"] for s in states],
+                         [s["exp_avg_sq"] for s in states], gdt,
+                         [s.get("master") for s in states],
+                         [s["exp_avg_scale"] for s in states] if small else None,
+                         [s["exp_avg_sq_scale"] for s in states] if small else None,
+                         [group["wd_mul"]] * len(ps))
+        n = len(ps)
+        numels = (ctypes.c_int64 * n)(*[p.numel() for p in ps])
+        pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in ps])
+        at = bytes((ctypes.c_void_p * n)(*[p.data_ptr() for p in ps]))
+        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, gdt, at)
+        return plan, states
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -379,8 +384,8 @@ class AdamW(torch.optim.Optimizer):
                 cached = self._plans["norm"] = (key, GradNormPlan(every))
             self.last_grad_norm, scale = cached[1].norm(every, self.max_grad_norm)
         for gi, group, ps, grads in todo:
-            plan = self._plan(gi, group, ps, grads)
-            at = [self.state[p]["step"] + 1 for p in ps]
+            plan, states = self._plan(gi, group, ps, grads)
+            at = [st["step"] + 1 for st in states]
             for t in sorted(set(at)):
                 cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],
                                         group["weight_decay"], t,
@@ -389,6 +394,6 @@ class AdamW(torch.optim.Optimizer):
                 mine = grads if len(set(at)) == 1 else [g if k == t else None
                                                         for g, k in zip(grads, at)]
                 plan.step(mine, cfg, scale)
-            for p, t in zip(ps, at):
-                self.state[p]["step"] = t
+            for st, t in zip(states, at):
+                st["step"] = t
         return loss

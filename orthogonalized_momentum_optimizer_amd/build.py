@@ -2,7 +2,7 @@
 
     python -m orthogonalized_momentum_optimizer_amd.build
 
-Every source under csrc/ is compiled with hipcc for gfx950 only and linked into
+(and _tensor_args.so, the binding's check of tensor lists, with the C++ compiler). Every HIP source under csrc/ is compiled with hipcc for gfx950 only and linked into
 orthogonalized_momentum_optimizer_amd/libmuon.so, except mfma_loop.hip, a measurement kernel
 for bench.py that goes into libmuon_mfma_loop.so. Objects go to _build/ at the repository
 root. The library links against the HIP runtime by its soname, so inside a process that has
@@ -22,6 +22,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
+# the binding's check of tensor lists: host code, against PyTorch's headers
+ARGS_SOURCE = "tensor_args.cpp"
+ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
 # measurement only, a library of its own (bench.py's matrix-core issue bound)
 PROBE_LIB = os.path.join(PKG, "libmuon_mfma_loop.so")
 PROBE_SOURCES = ["mfma_loop.hip"]
@@ -60,6 +63,24 @@ def _run(cmd):
     return err
 
 
+def build_args() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("clang++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found: it is required to build _tensor_args.so")
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          *[x for p in include_paths() for x in ("-isystem", p)],
+          "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, ARGS_SOURCE),
+          "-o", ARGS_LIB + ".tmp", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          f"-Wl,-rpath,{torch_lib}"])
+    os.replace(ARGS_LIB + ".tmp", ARGS_LIB)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
@@ -73,7 +94,9 @@ def build(verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(4, len(SOURCES) + len(PROBE_SOURCES))) as ex:
+        args = ex.submit(build_args)
         objs = list(ex.map(one, SOURCES + PROBE_SOURCES))
+        args.result()
     for lib, part in ((LIB, objs[:len(SOURCES)]), (PROBE_LIB, objs[len(SOURCES):])):
         tmp = lib + ".tmp"
         _run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,--no-undefined", "-o", tmp,

@@ -12,38 +12,34 @@
 #include "adamw.h"
 #include "tensor_list.h"
 
-struct muon_adamw_plan {
-  std::vector<muon_adamw_tensor> tensors;
-  std::vector<muon::Range> ranges;   // the plan's buffers, ascending (all written)
-  std::vector<int> of[3][2];         // tensors of each (parameter mode, gradient dtype)
-  muon_adamw_state state = MUON_ADAMW_F32;
-};
-
 namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;                     // elements per block
-constexpr int kMaxItems = 48;                    // tensors per launch (passed by value)
+constexpr int kMaxItems = 480;                   // tensors per launch: their gradients' addresses
+                                                 // travel by value, the rest is in the table
 constexpr int64_t kMaxBlocks = kMaxTensorElems / kChunk;  // per launch
 
 // Parameter modes: a bf16 parameter, an fp32 one, a bf16 one with an fp32 master copy.
 enum { kBf16 = 0, kF32 = 1, kMaster = 2 };
 
+// One tensor in the plan's device table: what does not change from step to step.
 struct Item {
   void* p;
   float* w;                                      // master
-  const void* g;
   void* m;
   void* v;
   uint8_t* ms;                                   // scales of the 8-bit states
   uint8_t* vs;
   int64_t numel;
-  float lam;                                     // weight_decay * wd_mul
+  float wd_mul;
+  int first;                                     // its first block in its launch
 };
+static_assert(sizeof(Item) == 64, "one line of the scalar cache");
 
 struct Step {
-  float lr, beta1, beta2, eps;
+  float lr, beta1, beta2, eps, weight_decay;
   float inv_bc1;                                 // 1 / (1 - beta1^t)
   float inv_sqrt_bc2;                            // 1 / sqrt(1 - beta2^t)
   const float* grad_scale;
@@ -53,10 +49,17 @@ struct Step {
 };
 
 struct AdamwLaunch {
-  Item item[kMaxItems];
-  int first[64];                                 // first block of each; unused: INT_MAX
+  const Item* item;
+  const int* first;                              // the items' first blocks, packed
+  int count;
   Step s;
+  const void* g[kMaxItems];
 };
+static_assert(sizeof(AdamwLaunch) <= 4096, "kernel arguments");
+
+__device__ __forceinline__ int tensor_of(const AdamwLaunch& L, int b) {
+  return find_tensor([&](int i) { return L.first[i]; }, L.count, b);
+}
 
 // The gradient scale; false when the step is to be skipped.
 __device__ __forceinline__ bool read_scale(const Step& S, float& scale) {
@@ -89,13 +92,14 @@ __global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L
   constexpr int kVec = 8, kUnroll = kChunk / (kThreads * kVec);
   constexpr int PD = PM == kBf16 ? 0 : 1;        // what p is read from
   const int b = blockIdx.x;
-  const int q = find_tensor(L.first, b);
-  const Item& I = L.item[q];
+  const int q = tensor_of(L, b);
+  const void* const G = L.g[q];
   float scale;
-  if (!read_scale(L.s, scale)) return;
-  const float lam = I.lam;
+  if (!G || !read_scale(L.s, scale)) return;
+  const Item I = L.item[q];
+  const float lam = L.s.weight_decay * I.wd_mul;
   const int64_t n = I.numel;
-  const int64_t base = int64_t(b - L.first[q]) * kChunk;
+  const int64_t base = int64_t(b - I.first) * kChunk;
   void* const P = PM == kMaster ? I.w : I.p;
   float* const M = static_cast<float*>(I.m);
   float* const V = static_cast<float*>(I.v);
@@ -107,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t i = base + int64_t(u * kThreads + t) * kVec;
       load_vec<PD>(P, i, p[u]);
-      load_vec<GD>(I.g, i, g[u]);
+      load_vec<GD>(G, i, g[u]);
       load_vec<1>(M, i, m[u]);
       load_vec<1>(V, i, v[u]);
     }
@@ -126,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L
   // the last chunk of a tensor, element by element
   for (int64_t i = base + t; i < n; i += kThreads) {
     float p = load_one<PD>(P, i), m = M[i], v = V[i];
-    step_f32(L.s, scale, lam, p, load_one<GD>(I.g, i), m, v);
+    step_f32(L.s, scale, lam, p, load_one<GD>(G, i), m, v);
     store_one<PD>(P, i, p);
     if (PM == kMaster) store_one<0>(I.p, i, p);
     M[i] = m;
@@ -236,7 +240,8 @@ __device__ __forceinline__ void moments(const Step& S, float g, float& m, float&
 }
 
 template <int PM, int GD, bool FULL>
-__device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float scale, int64_t i) {
+__device__ __forceinline__ void step_8bit(const Item& I, const void* G, const Step& S, float scale,
+                                          int64_t i) {
   constexpr int PD = PM == kBf16 ? 0 : 1;
   const int64_t n = I.numel;
   const int cnt = FULL ? kLane : int(min<int64_t>(max<int64_t>(n - i, 0), kLane));
@@ -244,6 +249,7 @@ __device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float sc
   uint8_t* const M = static_cast<uint8_t*>(I.m);
   uint8_t* const V = static_cast<uint8_t*>(I.v);
   const int64_t blk = i / MUON_ADAMW_BLOCK;
+  const float lam = S.weight_decay * I.wd_mul;
 
   float p[kLane], g[kLane], m[kLane], r[kLane];
   u32x4 mc = {0, 0, 0, 0}, rc = {0, 0, 0, 0};
@@ -254,7 +260,7 @@ __device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float sc
   }
   if (cnt == kLane) {
     load_vec<PD>(P, i, p);
-    load_vec<GD>(I.g, i, g);
+    load_vec<GD>(G, i, g);
     mc = *reinterpret_cast<const u32x4*>(M + i);
     rc = *reinterpret_cast<const u32x4*>(V + i);
   } else {
@@ -263,7 +269,7 @@ __device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float sc
       p[e] = g[e] = 0.f;
       if (e < cnt) {
         p[e] = load_one<PD>(P, i + e);
-        g[e] = load_one<GD>(I.g, i + e);
+        g[e] = load_one<GD>(G, i + e);
         mc[e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
         rc[e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
       }
@@ -293,7 +299,7 @@ __device__ __forceinline__ void step_8bit(const Item& I, const Step& S, float sc
     for (int e = 0; e < kLane; ++e) r[e] = root(r[e]);
   }
 #pragma unroll
-  for (int e = 0; e < kLane; ++e) p[e] = updated(S, I.lam, p[e], m[e], r[e]);
+  for (int e = 0; e < kLane; ++e) p[e] = updated(S, lam, p[e], m[e], r[e]);
   mb = scale_byte(row_max(mtop));
   // the largest r is the largest v's root; an infinite v is held as the largest finite one
   rb = scale_byte(sqrtf(fminf(row_max(vtop), 3.402823466e38f)));
@@ -335,17 +341,58 @@ template <int PM, int GD>
 __global__ __launch_bounds__(kThreads) void adamw_8bit_kernel(const AdamwLaunch L) {
   static_assert(kChunk == kThreads * kLane, "one vector per lane");
   const int b = blockIdx.x;
-  const int q = find_tensor(L.first, b);
-  const Item& I = L.item[q];
+  const int q = tensor_of(L, b);
+  const void* const G = L.g[q];
   float scale;
-  if (!read_scale(L.s, scale)) return;
-  const int64_t base = int64_t(b - L.first[q]) * kChunk;
+  if (!G || !read_scale(L.s, scale)) return;
+  const Item I = L.item[q];
+  const int64_t base = int64_t(b - I.first) * kChunk;
   const int64_t i = base + int64_t(threadIdx.x) * kLane;
-  if (base + kChunk <= I.numel) step_8bit<PM, GD, true>(I, L.s, scale, i);
-  else step_8bit<PM, GD, false>(I, L.s, scale, i);
+  if (base + kChunk <= I.numel) step_8bit<PM, GD, true>(I, G, L.s, scale, i);
+  else step_8bit<PM, GD, false>(I, G, L.s, scale, i);
+}
+
+// ---- the table -------------------------------------------------------------------------------
+
+constexpr int kUpload = 48;                      // items per launch (by value: a plan's upload may
+                                                 // be captured, and needs no pinned memory)
+struct Upload {
+  Item item[kUpload];
+  Item* to;
+  int* first;
+  int count;
+};
+
+__global__ __launch_bounds__(64) void adamw_upload_kernel(const Upload U) {
+  const int t = threadIdx.x;
+  if (t >= U.count) return;
+  U.to[t] = U.item[t];
+  U.first[t] = U.item[t].first;
 }
 
 // ---- host ------------------------------------------------------------------------------------
+
+struct Launch {
+  int pm, gd;                                    // its kernel
+  int lo, count;                                 // its items
+  int64_t blocks;
+};
+
+}  // namespace
+}  // namespace muon
+
+struct muon_adamw_plan {
+  std::vector<muon_adamw_tensor> tensors;
+  std::vector<muon::Range> ranges;               // the plan's buffers, ascending
+  std::vector<muon::Item> items;                 // those with elements, by kernel
+  std::vector<int> index;                        // the tensor of each item
+  std::vector<muon::Launch> launches;
+  muon_adamw_state state = MUON_ADAMW_F32;
+  muon::Item* table = nullptr;                   // device: items, then their first blocks
+};
+
+namespace muon {
+namespace {
 
 typedef void (*AdamwKernel)(AdamwLaunch);
 
@@ -463,16 +510,69 @@ int muon_adamw_plan_create(muon_adamw_plan** out, const muon_adamw_tensor* tenso
       return fail(MUON_ERR_INVALID_ARG, "unknown state %d", (int)state);
     muon_adamw_plan made;
     made.state = state;
+    std::vector<int> of[3][2];
     for (int64_t i = 0; i < n; ++i) {
       const muon_adamw_tensor& T = tensors[i];
       if (int st = check_tensor(T, i, state, made.ranges)) return st;
       if (T.numel == 0) continue;
       const int pm = T.master ? kMaster : T.param_dtype == MUON_DT_F32 ? kF32 : kBf16;
-      made.of[pm][T.grad_dtype == MUON_DT_F32].push_back((int)i);
+      of[pm][T.grad_dtype == MUON_DT_F32].push_back((int)i);
     }
     if (int st = check_overlaps(made.ranges)) return st;   // sorts them
     made.tensors.assign(tensors, tensors + n);
+    for (int pm = 0; pm < 3; ++pm)
+      for (int gd = 0; gd < 2; ++gd) {
+        Launch l = {pm, gd, (int)made.items.size(), 0, 0};
+        for (int i : of[pm][gd]) {
+          const muon_adamw_tensor& T = tensors[i];
+          const int64_t nb = (T.numel + kChunk - 1) / kChunk;
+          if (l.count == kMaxItems || l.blocks + nb > kMaxBlocks) {
+            made.launches.push_back(l);
+            l = {pm, gd, (int)made.items.size(), 0, 0};
+          }
+          made.items.push_back({T.param, T.master, T.exp_avg, T.exp_avg_sq, T.exp_avg_scale,
+                                T.exp_avg_sq_scale, T.numel, T.wd_mul, (int)l.blocks});
+          made.index.push_back(i);
+          ++l.count;
+          l.blocks += nb;
+        }
+        if (l.count) made.launches.push_back(l);
+      }
     *out = new muon_adamw_plan(std::move(made));
+    return MUON_OK;
+  });
+}
+
+size_t muon_adamw_plan_table_size(const muon_adamw_plan* plan) {
+  return plan ? plan->items.size() * (sizeof(Item) + sizeof(int)) : 0;
+}
+
+int muon_adamw_plan_upload(muon_adamw_plan* plan, void* table, size_t table_bytes,
+                           hipStream_t stream) {
+  return c_entry([&]() -> int {
+    if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+    const size_t need = muon_adamw_plan_table_size(plan);
+    if (need == 0) return MUON_OK;
+    if (!table || !is_aligned16(table) || table_bytes < need)
+      return fail(MUON_ERR_WORKSPACE, "a table of %zu bytes, 16-byte aligned, is needed", need);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(table);
+    if (meets(plan->ranges, lo, lo + need))
+      return fail(MUON_ERR_INVALID_ARG, "the table overlaps a buffer of the plan");
+    const size_t n = plan->items.size();
+    Item* const to = static_cast<Item*>(table);
+    Upload U;
+    for (size_t at = 0; at < n; at += kUpload) {
+      U.count = (int)std::min<size_t>(kUpload, n - at);
+      std::copy_n(plan->items.begin() + at, U.count, U.item);
+      U.to = to + at;
+      U.first = reinterpret_cast<int*>(to + n) + at;
+      hipLaunchKernelGGL(adamw_upload_kernel, dim3(1), dim3(64), 0, stream, U);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess)
+        return fail(MUON_ERR_HIP, "launch of the AdamW table's upload failed: %s",
+                    hipGetErrorString(e));
+    }
+    plan->table = to;
     return MUON_OK;
   });
 }
@@ -512,6 +612,7 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
     L.s.beta1 = cfg->beta1;
     L.s.beta2 = cfg->beta2;
     L.s.eps = cfg->eps;
+    L.s.weight_decay = cfg->weight_decay;
     const double t = (double)cfg->step;
     L.s.inv_bc1 = (float)(1.0 / (1.0 - std::pow((double)cfg->beta1, t)));
     L.s.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow((double)cfg->beta2, t)));
@@ -519,44 +620,24 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
     L.s.skip_nonfinite = cfg->skip_nonfinite;
     L.s.stochastic = cfg->stochastic;
     L.s.key = key_of(cfg->seed, cfg->step);
-    for (int pm = 0; pm < 3; ++pm)
-      for (int gd = 0; gd < 2; ++gd) {
-        const AdamwKernel k = kernel_of(plan->state, pm, gd);
-        int count = 0;
-        int64_t blocks = 0;
-        auto flush = [&]() -> int {
-          if (count == 0) return MUON_OK;
-          for (int c = count; c < 64; ++c) L.first[c] = INT_MAX;
-          hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(kThreads), 0, stream, L);
-          const hipError_t e = hipGetLastError();
-          count = 0;
-          blocks = 0;
-          if (e != hipSuccess)
-            return fail(MUON_ERR_HIP, "launch of the AdamW kernel failed: %s",
-                        hipGetErrorString(e));
-          return MUON_OK;
-        };
-        for (int i : plan->of[pm][gd]) {
-          const muon_adamw_tensor& T = plan->tensors[i];
-          if (!grads[i]) continue;
-          const int64_t nb = (T.numel + kChunk - 1) / kChunk;
-          if (count == kMaxItems || blocks + nb > kMaxBlocks)
-            if (int st = flush()) return st;
-          Item& I = L.item[count];
-          I.p = T.param;
-          I.w = T.master;
-          I.g = grads[i];
-          I.m = T.exp_avg;
-          I.v = T.exp_avg_sq;
-          I.ms = T.exp_avg_scale;
-          I.vs = T.exp_avg_sq_scale;
-          I.numel = T.numel;
-          I.lam = cfg->weight_decay * T.wd_mul;
-          L.first[count++] = (int)blocks;
-          blocks += nb;
-        }
-        if (int st = flush()) return st;
+    for (const Launch& l : plan->launches) {
+      bool any = false;
+      for (int c = 0; c < l.count; ++c) {
+        L.g[c] = grads[plan->index[l.lo + c]];
+        any = any || L.g[c];
       }
+      if (!any) continue;
+      if (!plan->table)
+        return fail(MUON_ERR_WORKSPACE, "muon_adamw_plan_upload has not been called on the plan");
+      L.item = plan->table + l.lo;
+      L.first = reinterpret_cast<const int*>(plan->table + plan->items.size()) + l.lo;
+      L.count = l.count;
+      hipLaunchKernelGGL(kernel_of(plan->state, l.pm, l.gd), dim3((unsigned)l.blocks),
+                         dim3(kThreads), 0, stream, L);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess)
+        return fail(MUON_ERR_HIP, "launch of the AdamW kernel failed: %s", hipGetErrorString(e));
+    }
     return MUON_OK;
   });
 }

@@ -19,7 +19,6 @@ struct muon_grad_plan {
   std::vector<muon_dtype> dtype;
   std::vector<int> part0;       // first part of each tensor; [n] = all parts
   int64_t part_elems = 0;
-  std::vector<int> of[2];       // tensors of each dtype, in order
 };
 
 namespace muon {
@@ -27,21 +26,27 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;
-constexpr int kMaxItems = 64;                    // tensors per launch
 constexpr int64_t kMinPart = 16384;
+constexpr int64_t kMaxPart = int64_t(1) << 30;
 constexpr int64_t kMaxParts = 16384;             // beyond one per tensor
 constexpr int kFinishThreads = 1024;
+constexpr int kNormItems = 240;                  // tensors per launch (by value)
+
+struct NormItem {
+  uint64_t g;                                    // address; bit 0: fp32
+  int first;                                     // its first block = its first part
+  uint32_t tail;                                 // elements of its last part
+};
 
 struct NormLaunch {
-  const void* g[kMaxItems];
-  int64_t numel[kMaxItems];
-  int first[kMaxItems];                          // first block of each tensor in this launch
-  int part0[kMaxItems];                          // its first part
-  int id[kMaxItems];
-  double* partial;
+  NormItem item[kNormItems];
+  double* partial;                               // of the launch's first part
   int* tensor_part;                              // out: first part of each tensor
-  int64_t part_elems;
+  int part0;
+  int count, blocks;
+  int part_elems;
 };
+static_assert(sizeof(NormLaunch) <= 4096, "kernel arguments");
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -63,77 +68,89 @@ __device__ __forceinline__ double block_sum(double x) {
   return x;
 }
 
+// Sum of squares of n elements at g (16-byte aligned), this thread's share.
 template <int GD>
+__device__ __forceinline__ double squares(const void* g, int n) {
+  double acc = 0.0;
+  int i = threadIdx.x * kVec;
+  for (; i + kVec <= n; i += kThreads * kVec) {
+    float x[kVec];
+    load_vec<GD>(g, i, x);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc = fma(double(x[e]), double(x[e]), acc);
+  }
+  for (; i < n; ++i) {                           // the thread whose vector the end cuts
+    const double x = load_one<GD>(g, i);
+    acc = fma(x, x, acc);
+  }
+  return acc;
+}
+
 __global__ __launch_bounds__(kThreads) void grad_norm_parts_kernel(const NormLaunch L) {
   const int b = blockIdx.x;
-  const int q = find_tensor(L.first, b);
-  const void* const G = L.g[q];
-  const int k = b - L.first[q];
+  const int q = find_tensor([&](int i) { return L.item[i].first; }, L.count, b);
+  const NormItem I = L.item[q];
+  const int k = b - I.first;
+  const bool last = b + 1 == (q + 1 < L.count ? L.item[q + 1].first : L.blocks);
+  const int n = last ? int(I.tail) : L.part_elems;
   const int64_t lo = int64_t(k) * L.part_elems;
-  const int64_t hi = min(lo + L.part_elems, L.numel[q]);
   double acc = 0.0;
-  if (G) {
-    int64_t i = lo + int64_t(threadIdx.x) * kVec;
-    for (; i + kVec <= hi; i += kThreads * kVec) {
-      float x[kVec];
-      load_vec<GD>(G, i, x);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) acc = fma(double(x[e]), double(x[e]), acc);
-    }
-    for (; i < hi; ++i) {                        // the thread whose vector the end cuts
-      const double x = load_one<GD>(G, i);
-      acc = fma(x, x, acc);
-    }
-  }
+  if (I.g > 1)
+    acc = I.g & 1 ? squares<1>(reinterpret_cast<const float*>(I.g - 1) + lo, n)
+                  : squares<0>(reinterpret_cast<const uint16_t*>(I.g) + lo, n);
   const double sum = block_sum<kThreads>(acc);
   if (threadIdx.x == 0) {
-    L.partial[L.part0[q] + k] = sum;
-    if (k == 0) L.tensor_part[L.id[q]] = L.part0[q];
+    L.partial[b] = sum;
+    if (k == 0) L.tensor_part[q] = L.part0 + b;
   }
 }
 
+// Block 0: the norm and the scale. Blocks beyond it: a tensor's norm for each wave.
 __global__ __launch_bounds__(kFinishThreads) void grad_norm_finish_kernel(
     const double* __restrict__ partial, const int* __restrict__ tensor_part, int tensors,
     int parts, float max_norm, float* out, float* norms) {
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kFinishThreads) acc += partial[i];
-  const double sum = block_sum<kFinishThreads>(acc);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(sum);
-    const bool finite = norm <= 1.7976931348623157e308;   // false for NaN too
-    out[0] = float(norm);
-    out[1] = !finite ? __uint_as_float(0x7fc00000u)
-                     : norm > double(max_norm) ? float(double(max_norm) / norm) : 1.f;
+  if (blockIdx.x == 0) {
+    double acc = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kFinishThreads) acc += partial[i];
+    const double sum = block_sum<kFinishThreads>(acc);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(sum);
+      const bool finite = norm <= 1.7976931348623157e308;   // false for NaN too
+      out[0] = float(norm);
+      out[1] = !finite ? __uint_as_float(0x7fc00000u)
+                       : norm > double(max_norm) ? float(double(max_norm) / norm) : 1.f;
+    }
+    return;
   }
-  if (!norms) return;
   const int lane = threadIdx.x & 63;
-  for (int t = threadIdx.x >> 6; t < tensors; t += kFinishThreads / 64) {
-    const int lo = tensor_part[t], hi = t + 1 < tensors ? tensor_part[t + 1] : parts;
-    double x = 0.0;
-    for (int i = lo + lane; i < hi; i += 64) x += partial[i];
-    x = wave_sum(x);
-    if (lane == 0) norms[t] = float(sqrt(x));
-  }
+  const int t = (blockIdx.x - 1) * (kFinishThreads / 64) + (threadIdx.x >> 6);
+  if (t >= tensors) return;
+  const int lo = tensor_part[t], hi = t + 1 < tensors ? tensor_part[t + 1] : parts;
+  double x = 0.0;
+  for (int i = lo + lane; i < hi; i += 64) x += partial[i];
+  x = wave_sum(x);
+  if (lane == 0) norms[t] = float(sqrt(x));
 }
 
 constexpr int kScaleChunk = kThreads * kVec * 2;
 
-struct ScaleLaunch {
-  void* g[kMaxItems];
-  int64_t numel[kMaxItems];
-  int first[kMaxItems];
-  const float* scale;
+constexpr int kScaleItems = 160;                 // tensors per launch (by value)
+
+struct ScaleItem {
+  uint64_t g;                                    // address; bit 0: fp32
+  int64_t numel;
+  int first;
 };
 
+struct ScaleLaunch {
+  ScaleItem item[kScaleItems];
+  const float* scale;
+  int count;
+};
+static_assert(sizeof(ScaleLaunch) <= 4096, "kernel arguments");
+
 template <int GD>
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ScaleLaunch L) {
-  const float s = *L.scale;
-  if (s == 1.f) return;
-  const int b = blockIdx.x;
-  const int q = find_tensor(L.first, b);
-  void* const G = L.g[q];
-  const int64_t n = L.numel[q];
-  const int64_t base = int64_t(b - L.first[q]) * kScaleChunk;
+__device__ __forceinline__ void scale_chunk(void* G, int64_t base, int64_t n, float s) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int64_t i = base + int64_t(u * kThreads + threadIdx.x) * kVec;
@@ -147,6 +164,16 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ScaleLaunch 
       for (int64_t j = i; j < n; ++j) store_one<GD>(G, j, load_one<GD>(G, j) * s);
     }
   }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ScaleLaunch L) {
+  const float s = *L.scale;
+  if (s == 1.f) return;
+  const int b = blockIdx.x;
+  const ScaleItem I = L.item[find_tensor([&](int i) { return L.item[i].first; }, L.count, b)];
+  const int64_t base = int64_t(b - I.first) * kScaleChunk;
+  if (I.g & 1) scale_chunk<1>(reinterpret_cast<void*>(I.g - 1), base, I.numel, s);
+  else scale_chunk<0>(reinterpret_cast<void*>(I.g), base, I.numel, s);
 }
 
 int check_grads(const muon_grad_plan* plan, const void* const* grads, int64_t n,
@@ -214,12 +241,12 @@ int muon_grad_plan_create(muon_grad_plan** out, const int64_t* numel, const muon
     made.numel.assign(numel, numel + n);
     made.dtype.assign(dtype, dtype + n);
     made.part_elems = kMinPart;
-    while (total / (double)made.part_elems > (double)kMaxParts) made.part_elems *= 2;
+    while (made.part_elems < kMaxPart && total / (double)made.part_elems > (double)kMaxParts)
+      made.part_elems *= 2;
     int64_t parts = 0;
     for (int64_t i = 0; i < n; ++i) {
       made.part0.push_back((int)parts);
       parts += std::max<int64_t>(1, (numel[i] + made.part_elems - 1) / made.part_elems);
-      made.of[dtype[i] == MUON_DT_F32].push_back((int)i);
     }
     made.part0.push_back((int)parts);
     *out = new muon_grad_plan(std::move(made));
@@ -251,34 +278,32 @@ int muon_grad_norm(const muon_grad_plan* plan, const void* const* grads, int64_t
     if (need > 0) add_range(rs, workspace, need, true);
     if (int st = check_overlaps(rs)) return st;
 
+    double* const partial = static_cast<double*>(workspace);
+    int* const tensor_part =
+        n > 0 ? reinterpret_cast<int*>(static_cast<char*>(workspace) + partial_bytes(plan)) : nullptr;
     NormLaunch L;
-    L.partial = static_cast<double*>(workspace);
-    L.tensor_part = n > 0 ? reinterpret_cast<int*>(static_cast<char*>(workspace) + partial_bytes(plan))
-                          : nullptr;
-    L.part_elems = plan->part_elems;
-    for (int dt = 0; dt < 2; ++dt) {
-      const std::vector<int>& of = plan->of[dt];
-      for (size_t at = 0; at < of.size(); at += kMaxItems) {
-        const int count = (int)std::min<size_t>(kMaxItems, of.size() - at);
-        int blocks = 0;
-        for (int c = 0; c < kMaxItems; ++c) {
-          L.first[c] = INT_MAX;
-          if (c >= count) continue;
-          const int i = of[at + c];
-          L.g[c] = grads[i];
-          L.numel[c] = plan->numel[i];
-          L.first[c] = blocks;
-          L.part0[c] = plan->part0[i];
-          L.id[c] = i;
-          blocks += plan->part0[i + 1] - plan->part0[i];
-        }
-        hipLaunchKernelGGL(dt ? grad_norm_parts_kernel<1> : grad_norm_parts_kernel<0>,
-                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, L);
-        if (int st = launched("gradient norm")) return st;
+    L.part_elems = (int)plan->part_elems;
+    for (int64_t at = 0; at < n; at += kNormItems) {
+      L.count = (int)std::min<int64_t>(kNormItems, n - at);
+      L.part0 = plan->part0[at];
+      L.blocks = plan->part0[at + L.count] - L.part0;
+      L.partial = partial + L.part0;
+      L.tensor_part = tensor_part + at;
+      for (int c = 0; c < L.count; ++c) {
+        const int64_t i = at + c;
+        const int first = plan->part0[i] - L.part0;
+        const int parts = plan->part0[i + 1] - plan->part0[i];
+        L.item[c] = {reinterpret_cast<uint64_t>(grads[i]) | uint64_t(plan->dtype[i] == MUON_DT_F32),
+                     first, uint32_t(plan->numel[i] - (parts - 1) * plan->part_elems)};
       }
+      hipLaunchKernelGGL(grad_norm_parts_kernel, dim3((unsigned)L.blocks), dim3(kThreads), 0,
+                         stream, L);
+      if (int st = launched("gradient norm")) return st;
     }
-    hipLaunchKernelGGL(grad_norm_finish_kernel, dim3(1), dim3(kFinishThreads), 0, stream,
-                       L.partial, L.tensor_part, (int)n, plan->part0.back(), max_norm, out, norms);
+    const int waves = kFinishThreads / 64;
+    const unsigned blocks = norms ? unsigned(1 + (n + waves - 1) / waves) : 1u;
+    hipLaunchKernelGGL(grad_norm_finish_kernel, dim3(blocks), dim3(kFinishThreads), 0, stream,
+                       partial, tensor_part, (int)n, plan->part0.back(), max_norm, out, norms);
     return launched("gradient norm");
   });
 }
@@ -294,31 +319,26 @@ int muon_grad_scale(const muon_grad_plan* plan, void* const* grads, int64_t n,
     constexpr int64_t kMaxBlocks = kMaxTensorElems / kScaleChunk;   // per launch
     ScaleLaunch L;
     L.scale = scale;
-    for (int dt = 0; dt < 2; ++dt) {
-      int count = 0;
-      int64_t blocks = 0;
-      auto flush = [&]() -> int {
-        if (count == 0) return MUON_OK;
-        for (int c = count; c < kMaxItems; ++c) L.first[c] = INT_MAX;
-        hipLaunchKernelGGL(dt ? grad_scale_kernel<1> : grad_scale_kernel<0>,
-                           dim3((unsigned)blocks), dim3(kThreads), 0, stream, L);
-        count = 0;
-        blocks = 0;
-        return launched("gradient scale");
-      };
-      for (int i : plan->of[dt]) {
-        if (!grads[i]) continue;
-        const int64_t nb = (plan->numel[i] + kScaleChunk - 1) / kScaleChunk;
-        if (nb == 0) continue;
-        if (count == kMaxItems || blocks + nb > kMaxBlocks)
-          if (int st = flush()) return st;
-        L.g[count] = grads[i];
-        L.numel[count] = plan->numel[i];
-        L.first[count++] = (int)blocks;
-        blocks += nb;
-      }
-      if (int st = flush()) return st;
+    L.count = 0;
+    int64_t blocks = 0;
+    auto flush = [&]() -> int {
+      if (L.count == 0) return MUON_OK;
+      hipLaunchKernelGGL(grad_scale_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, L);
+      L.count = 0;
+      blocks = 0;
+      return launched("gradient scale");
+    };
+    for (int64_t i = 0; i < n; ++i) {
+      const int64_t nb = (plan->numel[i] + kScaleChunk - 1) / kScaleChunk;
+      if (!grads[i] || nb == 0) continue;
+      if (L.count == kScaleItems || blocks + nb > kMaxBlocks)
+        if (int st = flush()) return st;
+      L.item[L.count++] = {reinterpret_cast<uint64_t>(grads[i]) |
+                               uint64_t(plan->dtype[i] == MUON_DT_F32),
+                           plan->numel[i], (int)blocks};
+      blocks += nb;
     }
+    if (int st = flush()) return st;
     return MUON_OK;
   });
 }

@@ -85,11 +85,19 @@ __device__ __forceinline__ void store_one(void* base, int64_t i, float x) {
   else static_cast<float*>(base)[i] = x;
 }
 
-// The tensor of block b: the last entry of first[0..63] (ascending, unused ones INT_MAX) that
-// is at most b. One load and one ballot, whatever the number of entries.
-__device__ __forceinline__ int find_tensor(const int* first, int b) {
-  const int f = first[threadIdx.x & 63];
-  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(f <= b)) - 1);
+// The tensor of block b: the last of first(0) .. first(count - 1) (ascending, first(0) = 0) that is
+// at most b, for count <= 512. Up to 64 entries: a load by every lane and a ballot; more: the same
+// over every eighth entry, then over the eight from there.
+template <typename F>
+__device__ __forceinline__ int find_tensor(F&& first, int count, int b) {
+  const int lane = threadIdx.x & 63;
+  int base = 0, step = count <= 64 ? 1 : 8;
+  int f = lane * step < count ? first(lane * step) : 0x7fffffff;
+  if (step == 8) {
+    base = 8 * (__popcll(__ballot(f <= b)) - 1);
+    f = lane < 8 && base + lane < count ? first(base + lane) : 0x7fffffff;
+  }
+  return __builtin_amdgcn_readfirstlane(base + __popcll(__ballot(f <= b)) - 1);
 }
 
 inline size_t dtype_bytes(muon_dtype d) { return d == MUON_DT_BF16 ? 2 : 4; }

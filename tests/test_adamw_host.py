@@ -145,6 +145,32 @@ def test_step_rejects_gradients(grad):
     L.muon_adamw_plan_destroy(plan)
 
 
+def test_table():
+    lib = L.lib()
+    assert lib.muon_adamw_plan_table_size(None) == 0
+    assert status_of(L.muon_adamw_plan_upload, None, BASE, 0, 0)[0] == INV
+    empty = L.muon_adamw_plan_create(None, 0, 0)
+    assert L.muon_adamw_plan_table_size(empty) == 0
+    L.muon_adamw_plan_upload(empty, None, 0, 0)                    # nothing to fill: no HIP call
+    L.muon_adamw_plan_destroy(empty)
+    plan = create(entries())
+    size = L.muon_adamw_plan_table_size(plan)
+    assert 0 < size <= 256                                         # two tensors have elements
+    for table, given, status in ((None, size, WS), (BASE + 8, size, WS), (BASE + (64 << 20), size - 1, WS),
+                                 (BASE, size, INV), (BASE + (2 << 20) - 16, size, INV)):
+        assert status_of(L.muon_adamw_plan_upload, plan, table, given, 0)[0] == status
+    L.muon_adamw_plan_destroy(plan)
+
+
+@no_gpu_only
+def test_step_needs_the_table():
+    plan = create(entries())
+    grads = L.make_pointers([BASE + (64 << 20), None, None])
+    status, msg = status_of(L.muon_adamw_step, plan, grads, 3, L.muon_adamw_config_default(), 0)
+    assert status == WS and "upload" in msg
+    L.muon_adamw_plan_destroy(plan)
+
+
 # ---- gradient norm ---------------------------------------------------------------------------
 
 def test_grad_plan_rejects():
@@ -223,6 +249,21 @@ def cpu_args(n=300, small=False):
                     exp_avg_scales=[z(b, dtype=torch.uint8).view(torch.float8_e8m0fnu)],
                     exp_avg_sq_scales=[z(b, dtype=torch.uint8).view(torch.float8_e8m0fnu)])
     return dict(params=[z(n)], exp_avgs=[z(n)], exp_avg_sqs=[z(n)], grad_dtypes=[torch.float32])
+
+
+def test_tensor_addresses_on_the_host():
+    """The native check refuses what is not a CUDA tensor of the layout (the accepted cases are
+    the GPU tests'), and buffers of another length."""
+    numels, dtypes = (ctypes.c_int64 * 3)(4, 4, 4), (ctypes.c_int32 * 3)(1, 1, 1)
+    out = L.tensor_addresses([None] * 3, numels, dtypes, 0)
+    assert list(out) == [None] * 3
+    for bad in (torch.zeros(4), torch.zeros(4, device="meta"), "text", 5, torch.zeros(4).to_sparse()):
+        assert L.tensor_addresses([None, bad, None], numels, dtypes, 0) == 1
+        assert L.tensor_addresses((bad, None, None), numels, dtypes, 0) == 0
+    with pytest.raises(ValueError):
+        L.tensor_addresses([None] * 2, numels, dtypes, 0)
+    with pytest.raises(TypeError):
+        L.tensor_addresses(7, numels, dtypes, 0)
 
 
 @pytest.mark.parametrize("small,change,error", [
