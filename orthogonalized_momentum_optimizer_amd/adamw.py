@@ -20,6 +20,9 @@ from . import _lib as L
 from .optim import dtype_code
 
 _NOTHING = contextlib.nullcontext()
+# the current stream's handle without a Stream object around it (2 us of a 10 us step)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def make_adamw_config(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
@@ -88,7 +91,7 @@ class _TensorList:
         return _NOTHING
 
     def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _raw_stream(self.device.index)
 
 
 class AdamWPlan(_TensorList):
@@ -204,15 +207,16 @@ class GradNormPlan(_TensorList):
         finite. A gradient that is None counts as zero. The workspace belongs to the call."""
         ptrs = self._pointers(grads)
         n = len(self._numels)
+        each = n if per_tensor else 0
+        ws = (2 + each + 3) // 4 * 4                  # 16-byte aligned, behind the results
         with self._on(stream):
-            out = torch.empty(2 + (n if per_tensor else 0), dtype=torch.float32, device=self.device)
-            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            out = torch.empty(ws + (self.ws_bytes + 3) // 4, dtype=torch.float32, device=self.device)
             base = out.data_ptr()
-            L.muon_grad_norm(self.handle, ptrs, n, max_norm, base,
-                             base + 8 if per_tensor and n else None, ws.data_ptr() or None,
-                             self.ws_bytes, self._stream())
-        norm, scale = out[:2].unbind()
-        return (norm, scale, out[2:]) if per_tensor else (norm, scale)
+            L.muon_grad_norm(self.handle, ptrs, n, max_norm, base, base + 8 if each else None,
+                             base + 4 * ws if self.ws_bytes else None, self.ws_bytes, self._stream())
+        if per_tensor:
+            return out[0], out[1], out[2:2 + n]
+        return out[0], out[1]
 
     def scale_(self, grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:

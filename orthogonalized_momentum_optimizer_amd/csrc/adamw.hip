@@ -15,16 +15,36 @@
 namespace muon {
 namespace {
 
+// Both kernels are bound by HBM, and how fast it goes depends on how they ask for it. Measured on
+// GPT-2-124M's tables (154 M elements, bf16, fp32 states, 3.40 GB), one choice changed at a time:
+//   8 elements per thread, cached                                    632 us   5.4 TB/s
+//   4 elements per thread, so that each access of a wave is one
+//     contiguous run of whole lines (1 KB of an fp32 stream)         622 us
+//   blocks of one wave                                               598 us
+//   at most 16 waves per compute unit and not 32                     574 us   5.9 TB/s
+//   nontemporal loads and stores                                     506 us   6.7 TB/s
+// (a copy of 4 GB reaches 4.9 to 5.4 TB/s). Fewer bytes in flight keep the streams' rows together;
+// with 13 waves the time is up again (539 us). Nontemporal accesses pay only together, and only
+// where they are whole lines: with 8 elements per thread they cost 10%.
+constexpr int kThreadsF32 = 64;
+constexpr int kVec = 4;
+constexpr int kChunkF32 = kThreadsF32 * kVec;
+// Shared memory that such a block asks for and does not use: 16 blocks fit a compute unit, not 32.
+constexpr int kHoldF32 = 10000;
+// 8-bit states
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;                     // elements per block
+constexpr int kOwn = kChunk / kThreads;          // elements per thread
+
 constexpr int kMaxItems = 480;                   // tensors per launch: their gradients' addresses
                                                  // travel by value, the rest is in the table
-constexpr int64_t kMaxBlocks = kMaxTensorElems / kChunk;  // per launch
+constexpr int64_t kPiece = int64_t(1) << 32;     // elements of a tensor in one item
+constexpr int64_t kMaxBlocks = kPiece / kChunkF32;  // per launch: under 2^32 threads
 
 // Parameter modes: a bf16 parameter, an fp32 one, a bf16 one with an fp32 master copy.
 enum { kBf16 = 0, kF32 = 1, kMaster = 2 };
 
-// One tensor in the plan's device table: what does not change from step to step.
+// One tensor, or piece of one, in the plan's device table: what does not change from step to step.
 struct Item {
   void* p;
   float* w;                                      // master
@@ -57,8 +77,30 @@ struct AdamwLaunch {
 };
 static_assert(sizeof(AdamwLaunch) <= 4096, "kernel arguments");
 
-__device__ __forceinline__ int tensor_of(const AdamwLaunch& L, int b) {
-  return find_tensor([&](int i) { return L.first[i]; }, L.count, b);
+// The table, which no kernel writes while steps run, through the scalar cache: its lines stay
+// there, where vector loads of it would queue with the streams of the tensors.
+template <typename T>
+using Constant = const __attribute__((address_space(4))) T*;
+
+// The tensor of block b, by bisection (8 scalar loads for 196 tensors).
+__device__ __forceinline__ int bisect(const AdamwLaunch& L, int b) {
+  const Constant<int> first = (Constant<int>)(uintptr_t)L.first;
+  int lo = 0, hi = L.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Blocks go from the last tensor to the first: a gradient norm, which goes the other way, has left
+// the last gradients in the memory-side cache (GPT-2-124M with it: 423 -> 411 us).
+__device__ __forceinline__ int block_of_launch() { return gridDim.x - 1 - blockIdx.x; }
+
+__device__ __forceinline__ Item item_of(const AdamwLaunch& L, int q) {
+  const Constant<Item> t = (Constant<Item>)(uintptr_t)L.item + q;
+  return {t->p, t->w, t->m, t->v, t->ms, t->vs, t->numel, t->wd_mul, t->first};
 }
 
 // The gradient scale; false when the step is to be skipped.
@@ -88,47 +130,38 @@ __device__ __forceinline__ void step_f32(const Step& S, float scale, float lam, 
 }
 
 template <int PM, int GD>
-__global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L) {
-  constexpr int kVec = 8, kUnroll = kChunk / (kThreads * kVec);
+__global__ __launch_bounds__(kThreadsF32) void adamw_f32_kernel(const AdamwLaunch L) {
   constexpr int PD = PM == kBf16 ? 0 : 1;        // what p is read from
-  const int b = blockIdx.x;
-  const int q = tensor_of(L, b);
+  const int b = block_of_launch();
+  const int q = bisect(L, b);
   const void* const G = L.g[q];
   float scale;
   if (!G || !read_scale(L.s, scale)) return;
-  const Item I = L.item[q];
+  const Item I = item_of(L, q);
   const float lam = L.s.weight_decay * I.wd_mul;
   const int64_t n = I.numel;
-  const int64_t base = int64_t(b - I.first) * kChunk;
+  const int64_t base = int64_t(b - I.first) * kChunkF32;
   void* const P = PM == kMaster ? I.w : I.p;
   float* const M = static_cast<float*>(I.m);
   float* const V = static_cast<float*>(I.v);
-  const int t = threadIdx.x;
 
-  if (base + kChunk <= n) {
-    float p[kUnroll][kVec], g[kUnroll][kVec], m[kUnroll][kVec], v[kUnroll][kVec];
+  if (base + kChunkF32 <= n) {
+    const int64_t i = base + int64_t(threadIdx.x) * kVec;
+    float p[kVec], g[kVec], m[kVec], v[kVec];
+    load_vec<PD, true>(P, i, p);
+    load_vec<GD, true>(G, i, g);
+    load_vec<1, true>(M, i, m);
+    load_vec<1, true>(V, i, v);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = base + int64_t(u * kThreads + t) * kVec;
-      load_vec<PD>(P, i, p[u]);
-      load_vec<GD>(G, i, g[u]);
-      load_vec<1>(M, i, m[u]);
-      load_vec<1>(V, i, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = base + int64_t(u * kThreads + t) * kVec;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) step_f32(L.s, scale, lam, p[u][e], g[u][e], m[u][e], v[u][e]);
-      store_vec<PD>(P, i, p[u]);
-      if (PM == kMaster) store_vec<0>(I.p, i, p[u]);
-      store_vec<1>(M, i, m[u]);
-      store_vec<1>(V, i, v[u]);
-    }
+    for (int e = 0; e < kVec; ++e) step_f32(L.s, scale, lam, p[e], g[e], m[e], v[e]);
+    store_vec<PD, true>(P, i, p);
+    if (PM == kMaster) store_vec<0, true>(I.p, i, p);
+    store_vec<1, true>(M, i, m);
+    store_vec<1, true>(V, i, v);
     return;
   }
   // the last chunk of a tensor, element by element
-  for (int64_t i = base + t; i < n; i += kThreads) {
+  for (int64_t i = base + threadIdx.x; i < n; i += kThreadsF32) {
     float p = load_one<PD>(P, i), m = M[i], v = V[i];
     step_f32(L.s, scale, lam, p, load_one<GD>(G, i), m, v);
     store_one<PD>(P, i, p);
@@ -140,23 +173,27 @@ __global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const AdamwLaunch L
 
 // ---- 8-bit states ----------------------------------------------------------------------------
 //
-// A block of 256 elements is 16 lanes x 16 elements: one row of the wavefront's data-parallel
-// primitives, so that the largest |x| of a block takes four rotations within the row and the
-// codes of a lane are one 16-byte access.
-
-constexpr int kLane = 16;                        // elements per lane
+// A block of 256 elements is 32 lanes x 8 elements where all its streams are bf16 and codes, and 64
+// lanes x 4 where one is fp32: each access of a wave is one contiguous run, of whole lines. A
+// thread has kOwn elements, in groups 64 lanes apart.
 
 template <int CTRL>
 __device__ __forceinline__ float row_rotate(float x) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
 }
 
-// The largest of x over the lane's row of 16, in every lane. NaN only where all are.
-__device__ __forceinline__ float row_max(float x) {
-  x = fmaxf(x, row_rotate<0x128>(x));
+// The largest of x >= 0 over the lanes of a block, in every lane.
+template <int LANE>
+__device__ __forceinline__ float block_max(float x) {
+  x = fmaxf(x, row_rotate<0x128>(x));            // over the row of 16 lanes
   x = fmaxf(x, row_rotate<0x124>(x));
   x = fmaxf(x, row_rotate<0x122>(x));
-  return fmaxf(x, row_rotate<0x121>(x));
+  x = fmaxf(x, row_rotate<0x121>(x));
+  if (LANE == 8)                                 // and the row beside it
+    return fmaxf(x, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401f)));
+  const int y = __float_as_int(x);               // and the other three (floats >= 0 order as integers)
+  return __int_as_float(max(max(__builtin_amdgcn_readlane(y, 0), __builtin_amdgcn_readlane(y, 16)),
+                            max(__builtin_amdgcn_readlane(y, 32), __builtin_amdgcn_readlane(y, 48))));
 }
 
 // The smallest scale byte b with top <= T * 2^(b - 127): top = 2^(E - 127) * f has b = E - 8,
@@ -175,13 +212,24 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// 16 codes <-> floats, by the hardware's scaled conversions: exact one way, to nearest even or
+// A register whose every bit the next conversions write.
+__device__ __forceinline__ int unset() {
+  int w;
+  asm("" : "=v"(w));
+  return w;
+}
+
+template <int LANE>                              // a lane's codes of one group
+using Codes = uint32_t __attribute__((ext_vector_type(LANE / 4)));
+
+// A lane's codes <-> floats, by the hardware's scaled conversions: exact one way, to nearest even or
 // stochastically the other (up with the probability of what is cut off: the upper 20 of the 32
 // random bits are added below the format's last place). Measured over all codes and scales and
 // over random values, subnormals of the format included: bit by bit what adamw.h defines.
-__device__ __forceinline__ void decode(const u32x4 c, float scale, float (&x)[kLane]) {
+template <int LANE>
+__device__ __forceinline__ void decode(const Codes<LANE> c, float scale, float* x) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < LANE / 4; ++k) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, false);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, true);
     x[4 * k] = a[0];
@@ -190,11 +238,12 @@ __device__ __forceinline__ void decode(const u32x4 c, float scale, float (&x)[kL
     x[4 * k + 3] = b[1];
   }
 }
-__device__ __forceinline__ u32x4 encode(const float (&x)[kLane], float scale) {
-  u32x4 c;
+template <int LANE>
+__device__ __forceinline__ Codes<LANE> encode(const float* x, float scale) {
+  Codes<LANE> c;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    i16x2 w = {0, 0};
+  for (int k = 0; k < LANE / 4; ++k) {
+    i16x2 w = __builtin_bit_cast(i16x2, unset());
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k], x[4 * k + 1], scale, false);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k + 2], x[4 * k + 3], scale, true);
     c[k] = __builtin_bit_cast(uint32_t, w);
@@ -202,13 +251,14 @@ __device__ __forceinline__ u32x4 encode(const float (&x)[kLane], float scale) {
   return c;
 }
 // Elements 2j and 2j + 1 take the halves of h(j ^ key): 16 random bits, then half of one.
-__device__ __forceinline__ u32x4 encode_stochastic(const float (&x)[kLane], float scale,
-                                                   uint32_t pair, uint32_t key) {
-  u32x4 c;
+template <int LANE>
+__device__ __forceinline__ Codes<LANE> encode_stochastic(const float* x, float scale, uint32_t pair,
+                                                         uint32_t key) {
+  Codes<LANE> c;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < LANE / 4; ++k) {
     const uint32_t h0 = mix32((pair + 2 * k) ^ key), h1 = mix32((pair + 2 * k + 1) ^ key);
-    int w = 0;
+    int w = unset();
     w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k], h0 << 16 | 0x8000u, scale, 0);
     w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k + 1], (h0 & 0xffff0000u) | 0x8000u, scale, 1);
     w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k + 2], h1 << 16 | 0x8000u, scale, 2);
@@ -239,117 +289,149 @@ __device__ __forceinline__ void moments(const Step& S, float g, float& m, float&
   v = c + d;
 }
 
-template <int PM, int GD, bool FULL>
+// The chunk from element `base` on; FULL: it ends inside the tensor.
+template <int PM, int GD, int LANE, bool FULL>
 __device__ __forceinline__ void step_8bit(const Item& I, const void* G, const Step& S, float scale,
-                                          int64_t i) {
-  constexpr int PD = PM == kBf16 ? 0 : 1;
-  const int64_t n = I.numel;
-  const int cnt = FULL ? kLane : int(min<int64_t>(max<int64_t>(n - i, 0), kLane));
+                                          int64_t base) {
+  constexpr int PD = PM == kBf16 ? 0 : 1, GROUPS = kOwn / LANE;
+  const float lam = S.weight_decay * I.wd_mul;
   void* const P = PM == kMaster ? I.w : I.p;
   uint8_t* const M = static_cast<uint8_t*>(I.m);
   uint8_t* const V = static_cast<uint8_t*>(I.v);
-  const int64_t blk = i / MUON_ADAMW_BLOCK;
-  const float lam = S.weight_decay * I.wd_mul;
+  const int64_t own = base + int64_t(threadIdx.x / 64) * (64 * kOwn) + (threadIdx.x & 63) * LANE;
+  auto element = [&](int u) { return own + u * 64 * LANE; };
+  auto inside = [&](int u) {                     // of the group's elements
+    return FULL ? LANE : int(min<int64_t>(max<int64_t>(I.numel - element(u), 0), LANE));
+  };
 
-  float p[kLane], g[kLane], m[kLane], r[kLane];
-  u32x4 mc = {0, 0, 0, 0}, rc = {0, 0, 0, 0};
-  int mb = 0, rb = 0;
-  if (cnt > 0) {
-    mb = I.ms[blk];
-    rb = I.vs[blk];
-  }
-  if (cnt == kLane) {
-    load_vec<PD>(P, i, p);
-    load_vec<GD>(G, i, g);
-    mc = *reinterpret_cast<const u32x4*>(M + i);
-    rc = *reinterpret_cast<const u32x4*>(V + i);
-  } else {
+  float p[GROUPS][LANE], g[GROUPS][LANE], m[kOwn], r[kOwn];
+  Codes<LANE> mc[GROUPS], rc[GROUPS];
+  int mb[GROUPS], rb[GROUPS];
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) {
-      p[e] = g[e] = 0.f;
-      if (e < cnt) {
-        p[e] = load_one<PD>(P, i + e);
-        g[e] = load_one<GD>(G, i + e);
-        mc[e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
-        rc[e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
+  for (int u = 0; u < GROUPS; ++u) {
+    const int64_t i = element(u);
+    const int cnt = inside(u);
+    mb[u] = rb[u] = 0;
+    if (cnt > 0) {
+      mb[u] = I.ms[i / MUON_ADAMW_BLOCK];
+      rb[u] = I.vs[i / MUON_ADAMW_BLOCK];
+    }
+    if (cnt == LANE) {
+      load_vec<PD, true>(P, i, p[u]);
+      load_vec<GD, true>(G, i, g[u]);
+      mc[u] = load_at<true>(reinterpret_cast<const Codes<LANE>*>(M + i));
+      rc[u] = load_at<true>(reinterpret_cast<const Codes<LANE>*>(V + i));
+    } else {
+      mc[u] = rc[u] = Codes<LANE>(0);
+#pragma unroll
+      for (int e = 0; e < LANE; ++e) {
+        p[u][e] = g[u][e] = 0.f;
+        if (e < cnt) {
+          p[u][e] = load_one<PD>(P, i + e);
+          g[u][e] = load_one<GD>(G, i + e);
+          mc[u][e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
+          rc[u][e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
+        }
       }
     }
   }
-  decode(mc, scale_of(mb), m);
-  decode(rc, scale_of(rb), r);
 
-  float mtop = 0.f, vtop = 0.f;
+  float mtop[GROUPS], vtop[GROUPS];
   uint32_t vlow = ~0u;                           // the smallest v over 0, less one unit
 #pragma unroll
-  for (int e = 0; e < kLane; ++e) {
-    float v = r[e] * r[e];
-    moments(S, g[e] * scale, m[e], v);
-    r[e] = v;
-    mtop = fmaxf(mtop, fabsf(m[e]));
-    vtop = fmaxf(vtop, v);
-    vlow = min(vlow, __float_as_uint(v) - 1u);
+  for (int u = 0; u < GROUPS; ++u) {
+    float* const mu = m + u * LANE;
+    float* const ru = r + u * LANE;
+    decode<LANE>(mc[u], scale_of(mb[u]), mu);
+    decode<LANE>(rc[u], scale_of(rb[u]), ru);
+    mtop[u] = vtop[u] = 0.f;
+#pragma unroll
+    for (int e = 0; e < LANE; ++e) {
+      float v = ru[e] * ru[e];
+      moments(S, g[u][e] * scale, mu[e], v);
+      asm("" : "+v"(mu[e]));                     // kept, not computed again behind the branch
+      ru[e] = v;
+      mtop[u] = fmaxf(mtop[u], fabsf(mu[e]));
+      vtop[u] = fmaxf(vtop[u], v);
+      vlow = min(vlow, __float_as_uint(v) - 1u);
+    }
   }
   // rare, and the whole wave's: a v that root() does not take
-  const bool wide = __any(vlow < 0x0d000000u - 1u || vtop > 3.402823466e38f);
-  if (wide) {
+  bool wide = vlow < 0x0d000000u - 1u;
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) r[e] = sqrtf(r[e]);
+  for (int u = 0; u < GROUPS; ++u) wide = wide || vtop[u] > 3.402823466e38f;
+  float rtop[GROUPS];                            // of the block: its largest v's root
+#pragma unroll
+  for (int u = 0; u < GROUPS; ++u) rtop[u] = block_max<LANE>(vtop[u]);
+  if (__any(wide)) {
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) r[e] = sqrtf(r[e]);
+#pragma unroll
+    for (int u = 0; u < GROUPS; ++u)             // an infinite v is held as the largest finite one
+      rtop[u] = sqrtf(fminf(rtop[u], 3.402823466e38f));
   } else {
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) r[e] = root(r[e]);
-  }
+    for (int e = 0; e < kOwn; ++e) r[e] = root(r[e]);
 #pragma unroll
-  for (int e = 0; e < kLane; ++e) p[e] = updated(S, lam, p[e], m[e], r[e]);
-  mb = scale_byte(row_max(mtop));
-  // the largest r is the largest v's root; an infinite v is held as the largest finite one
-  rb = scale_byte(sqrtf(fminf(row_max(vtop), 3.402823466e38f)));
-  const float ms = scale_of(mb), rs = scale_of(rb);
-  const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, 0x1.fffffep63f);
-#pragma unroll
-  for (int e = 0; e < kLane; ++e)                // NaN and 0 as they are
-    r[e] = r[e] > 0.f ? __builtin_amdgcn_fmed3f(r[e], low, high) : r[e];
-  mc = encode(m, ms);
-  if (S.stochastic) {
-    const uint64_t pair = uint64_t(i) >> 1;
-    rc = encode_stochastic(r, rs, uint32_t(pair), S.key ^ uint32_t(pair >> 32) * 0xEB26D985u);
-  } else {
-    rc = encode(r, rs);
+    for (int u = 0; u < GROUPS; ++u) rtop[u] = root(rtop[u]);
   }
 
-  if (cnt == kLane) {
-    store_vec<PD>(P, i, p);
-    if (PM == kMaster) store_vec<0>(I.p, i, p);
-    *reinterpret_cast<u32x4*>(M + i) = mc;
-    *reinterpret_cast<u32x4*>(V + i) = rc;
-  } else {
 #pragma unroll
-    for (int e = 0; e < kLane; ++e)
-      if (e < cnt) {
-        store_one<PD>(P, i + e, p[e]);
-        if (PM == kMaster) store_one<0>(I.p, i + e, p[e]);
-        M[i + e] = uint8_t(mc[e >> 2] >> (8 * (e & 3)));
-        V[i + e] = uint8_t(rc[e >> 2] >> (8 * (e & 3)));
-      }
-  }
-  if ((threadIdx.x & 15) == 0 && cnt > 0) {
-    I.ms[blk] = uint8_t(mb);
-    I.vs[blk] = uint8_t(rb);
+  for (int u = 0; u < GROUPS; ++u) {
+    const int64_t i = element(u);
+    const int cnt = inside(u);
+    float* const mu = m + u * LANE;
+    float* const ru = r + u * LANE;
+#pragma unroll
+    for (int e = 0; e < LANE; ++e) p[u][e] = updated(S, lam, p[u][e], mu[e], ru[e]);
+    mb[u] = scale_byte(block_max<LANE>(mtop[u]));
+    rb[u] = scale_byte(rtop[u]);
+    const float rs = scale_of(rb[u]);
+    const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, 0x1.fffffep63f);
+#pragma unroll
+    for (int e = 0; e < LANE; ++e)              // NaN and 0 as they are
+      ru[e] = ru[e] > 0.f ? __builtin_amdgcn_fmed3f(ru[e], low, high) : ru[e];
+    mc[u] = encode<LANE>(mu, scale_of(mb[u]));
+    if (S.stochastic) {
+      const uint64_t pair = uint64_t(i) >> 1;
+      rc[u] = encode_stochastic<LANE>(ru, rs, uint32_t(pair), S.key ^ uint32_t(pair >> 32) * 0xEB26D985u);
+    } else {
+      rc[u] = encode<LANE>(ru, rs);
+    }
+    if (cnt == LANE) {
+      store_vec<PD, true>(P, i, p[u]);
+      if (PM == kMaster) store_vec<0, true>(I.p, i, p[u]);
+      store_at<true>(reinterpret_cast<Codes<LANE>*>(M + i), mc[u]);
+      store_at<true>(reinterpret_cast<Codes<LANE>*>(V + i), rc[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < LANE; ++e)
+        if (e < cnt) {
+          store_one<PD>(P, i + e, p[u][e]);
+          if (PM == kMaster) store_one<0>(I.p, i + e, p[u][e]);
+          M[i + e] = uint8_t(mc[u][e >> 2] >> (8 * (e & 3)));
+          V[i + e] = uint8_t(rc[u][e >> 2] >> (8 * (e & 3)));
+        }
+    }
+    if (threadIdx.x % (MUON_ADAMW_BLOCK / LANE) == 0 && cnt > 0) {
+      I.ms[i / MUON_ADAMW_BLOCK] = uint8_t(mb[u]);
+      I.vs[i / MUON_ADAMW_BLOCK] = uint8_t(rb[u]);
+    }
   }
 }
 
 template <int PM, int GD>
 __global__ __launch_bounds__(kThreads) void adamw_8bit_kernel(const AdamwLaunch L) {
-  static_assert(kChunk == kThreads * kLane, "one vector per lane");
-  const int b = blockIdx.x;
-  const int q = tensor_of(L, b);
+  constexpr int LANE = PM == kBf16 && GD == 0 ? 8 : 4;
+  const int b = block_of_launch();
+  const int q = find_tensor([&](int i) { return L.first[i]; }, L.count, b);
   const void* const G = L.g[q];
   float scale;
   if (!G || !read_scale(L.s, scale)) return;
-  const Item I = L.item[q];
+  const Item I = item_of(L, q);
   const int64_t base = int64_t(b - I.first) * kChunk;
-  const int64_t i = base + int64_t(threadIdx.x) * kLane;
-  if (base + kChunk <= I.numel) step_8bit<PM, GD, true>(I, G, L.s, scale, i);
-  else step_8bit<PM, GD, false>(I, G, L.s, scale, i);
+  if (base + kChunk <= I.numel) step_8bit<PM, GD, LANE, true>(I, G, L.s, scale, base);
+  else step_8bit<PM, GD, LANE, false>(I, G, L.s, scale, base);
 }
 
 // ---- the table -------------------------------------------------------------------------------
@@ -386,6 +468,7 @@ struct muon_adamw_plan {
   std::vector<muon::Range> ranges;               // the plan's buffers, ascending
   std::vector<muon::Item> items;                 // those with elements, by kernel
   std::vector<int> index;                        // the tensor of each item
+  std::vector<size_t> grad_offset;               // bytes, of the item's piece in its gradient
   std::vector<muon::Launch> launches;
   muon_adamw_state state = MUON_ADAMW_F32;
   muon::Item* table = nullptr;                   // device: items, then their first blocks
@@ -465,12 +548,24 @@ int check_config(const muon_adamw_config* cfg) {
   return MUON_OK;
 }
 
-// Whether [lo, hi) meets one of the plan's buffers.
-bool meets(const std::vector<Range>& rs, uintptr_t lo, uintptr_t hi) {
-  auto it = std::upper_bound(rs.begin(), rs.end(), lo,
-                             [](uintptr_t x, const Range& r) { return x < r.hi; });
-  return it != rs.end() && it->lo < hi;
-}
+// Whether ranges meet one of the plan's buffers. The gap that the last one lay in is kept:
+// gradients of one allocation take one search.
+class Buffers {
+ public:
+  explicit Buffers(const std::vector<Range>& rs) : rs_(rs) {}
+  bool meet(uintptr_t lo, uintptr_t hi) {
+    if (lo >= gap_lo_ && hi <= gap_hi_) return false;
+    const auto it = std::upper_bound(rs_.begin(), rs_.end(), lo,
+                                     [](uintptr_t x, const Range& r) { return x < r.hi; });
+    gap_lo_ = it == rs_.begin() ? 0 : (it - 1)->hi;
+    gap_hi_ = it == rs_.end() ? ~uintptr_t(0) : it->lo;
+    return hi > gap_hi_ || lo < gap_lo_;
+  }
+
+ private:
+  const std::vector<Range>& rs_;
+  uintptr_t gap_lo_ = 1, gap_hi_ = 0;
+};
 
 uint32_t key_of(uint64_t seed, int64_t step) {
   uint64_t z = seed + (uint64_t)step * 0x1493FA689CA113ADull;
@@ -520,21 +615,32 @@ int muon_adamw_plan_create(muon_adamw_plan** out, const muon_adamw_tensor* tenso
     }
     if (int st = check_overlaps(made.ranges)) return st;   // sorts them
     made.tensors.assign(tensors, tensors + n);
+    // (the 8-bit kernel needs an element's index in its tensor, and fits a whole one in a launch)
+    const int64_t chunk = state == MUON_ADAMW_8BIT ? kChunk : kChunkF32;
+    const int64_t piece = state == MUON_ADAMW_8BIT ? kMaxTensorElems : kPiece;
     for (int pm = 0; pm < 3; ++pm)
       for (int gd = 0; gd < 2; ++gd) {
         Launch l = {pm, gd, (int)made.items.size(), 0, 0};
         for (int i : of[pm][gd]) {
           const muon_adamw_tensor& T = tensors[i];
-          const int64_t nb = (T.numel + kChunk - 1) / kChunk;
-          if (l.count == kMaxItems || l.blocks + nb > kMaxBlocks) {
-            made.launches.push_back(l);
-            l = {pm, gd, (int)made.items.size(), 0, 0};
+          const int64_t pb = dtype_bytes(T.param_dtype), sb = state == MUON_ADAMW_8BIT ? 1 : 4;
+          for (int64_t off = 0; off < T.numel; off += piece) {
+            const int64_t len = std::min(piece, T.numel - off);
+            const int64_t nb = (len + chunk - 1) / chunk;
+            if (l.count == kMaxItems || l.blocks + nb > kMaxBlocks) {
+              made.launches.push_back(l);
+              l = {pm, gd, (int)made.items.size(), 0, 0};
+            }
+            made.items.push_back({static_cast<char*>(T.param) + off * pb,
+                                  T.master ? T.master + off : nullptr,
+                                  static_cast<char*>(T.exp_avg) + off * sb,
+                                  static_cast<char*>(T.exp_avg_sq) + off * sb, T.exp_avg_scale,
+                                  T.exp_avg_sq_scale, len, T.wd_mul, (int)l.blocks});
+            made.index.push_back(i);
+            made.grad_offset.push_back((size_t)off * dtype_bytes(T.grad_dtype));
+            ++l.count;
+            l.blocks += nb;
           }
-          made.items.push_back({T.param, T.master, T.exp_avg, T.exp_avg_sq, T.exp_avg_scale,
-                                T.exp_avg_sq_scale, T.numel, T.wd_mul, (int)l.blocks});
-          made.index.push_back(i);
-          ++l.count;
-          l.blocks += nb;
         }
         if (l.count) made.launches.push_back(l);
       }
@@ -556,7 +662,7 @@ int muon_adamw_plan_upload(muon_adamw_plan* plan, void* table, size_t table_byte
     if (!table || !is_aligned16(table) || table_bytes < need)
       return fail(MUON_ERR_WORKSPACE, "a table of %zu bytes, 16-byte aligned, is needed", need);
     const uintptr_t lo = reinterpret_cast<uintptr_t>(table);
-    if (meets(plan->ranges, lo, lo + need))
+    if (Buffers(plan->ranges).meet(lo, lo + need))
       return fail(MUON_ERR_INVALID_ARG, "the table overlaps a buffer of the plan");
     const size_t n = plan->items.size();
     Item* const to = static_cast<Item*>(table);
@@ -588,6 +694,7 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
                   plan->tensors.size());
     if (int st = check_config(cfg)) return st;
     if (n > 0 && !grads) return fail(MUON_ERR_INVALID_ARG, "grads is NULL");
+    Buffers buffers(plan->ranges);
     for (int64_t i = 0; i < n; ++i) {
       const muon_adamw_tensor& T = plan->tensors[i];
       if (!std::isfinite(cfg->weight_decay * T.wd_mul))
@@ -597,13 +704,13 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
       if (!is_aligned16(grads[i]))
         return fail(MUON_ERR_INVALID_ARG, "gradient %lld must be 16-byte aligned", (long long)i);
       const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
-      if (meets(plan->ranges, lo, lo + (size_t)T.numel * dtype_bytes(T.grad_dtype)))
+      if (buffers.meet(lo, lo + (size_t)T.numel * dtype_bytes(T.grad_dtype)))
         return fail(MUON_ERR_INVALID_ARG, "gradient %lld overlaps a buffer of the plan",
                     (long long)i);
     }
     if (cfg->grad_scale) {
       const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
-      if (meets(plan->ranges, lo, lo + sizeof(float)))
+      if (buffers.meet(lo, lo + sizeof(float)))
         return fail(MUON_ERR_INVALID_ARG, "grad_scale overlaps a buffer of the plan");
     }
 
@@ -623,8 +730,9 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
     for (const Launch& l : plan->launches) {
       bool any = false;
       for (int c = 0; c < l.count; ++c) {
-        L.g[c] = grads[plan->index[l.lo + c]];
-        any = any || L.g[c];
+        const void* const g = grads[plan->index[l.lo + c]];
+        L.g[c] = g ? static_cast<const char*>(g) + plan->grad_offset[l.lo + c] : nullptr;
+        any = any || g;
       }
       if (!any) continue;
       if (!plan->table)
@@ -632,8 +740,9 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
       L.item = plan->table + l.lo;
       L.first = reinterpret_cast<const int*>(plan->table + plan->items.size()) + l.lo;
       L.count = l.count;
+      const bool f32 = plan->state == MUON_ADAMW_F32;
       hipLaunchKernelGGL(kernel_of(plan->state, l.pm, l.gd), dim3((unsigned)l.blocks),
-                         dim3(kThreads), 0, stream, L);
+                         dim3(f32 ? kThreadsF32 : kThreads), f32 ? kHoldF32 : 0, stream, L);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess)
         return fail(MUON_ERR_HIP, "launch of the AdamW kernel failed: %s", hipGetErrorString(e));

@@ -19,6 +19,7 @@ struct muon_grad_plan {
   std::vector<muon_dtype> dtype;
   std::vector<int> part0;       // first part of each tensor; [n] = all parts
   int64_t part_elems = 0;
+  int keep_part = 0;            // parts from here on are left in the memory-side cache
 };
 
 namespace muon {
@@ -26,9 +27,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;
+constexpr int kUnroll = 4;                       // loads of a thread in flight
 constexpr int64_t kMinPart = 16384;
 constexpr int64_t kMaxPart = int64_t(1) << 30;
 constexpr int64_t kMaxParts = 16384;             // beyond one per tensor
+constexpr int64_t kCacheBytes = int64_t(1) << 28;  // the memory-side cache: 256 MB
 constexpr int kFinishThreads = 1024;
 constexpr int kNormItems = 240;                  // tensors per launch (by value)
 
@@ -44,6 +47,7 @@ struct NormLaunch {
   int* tensor_part;                              // out: first part of each tensor
   int part0;
   int count, blocks;
+  int keep_part;
   int part_elems;
 };
 static_assert(sizeof(NormLaunch) <= 4096, "kernel arguments");
@@ -68,16 +72,27 @@ __device__ __forceinline__ double block_sum(double x) {
   return x;
 }
 
-// Sum of squares of n elements at g (16-byte aligned), this thread's share.
-template <int GD>
+// Sum of squares of n elements at g (16-byte aligned), this thread's share. Each access of a wave
+// is one contiguous kilobyte. NT: nontemporal.
+template <int GD, bool NT>
 __device__ __forceinline__ double squares(const void* g, int n) {
+  constexpr int N = GD == 0 ? 8 : 4;             // elements of a 16-byte access
   double acc = 0.0;
-  int i = threadIdx.x * kVec;
-  for (; i + kVec <= n; i += kThreads * kVec) {
-    float x[kVec];
-    load_vec<GD>(g, i, x);
+  int i = threadIdx.x * N;
+  for (; i + (kUnroll - 1) * kThreads * N + N <= n; i += kUnroll * kThreads * N) {
+    float x[kUnroll][N];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) acc = fma(double(x[e]), double(x[e]), acc);
+    for (int u = 0; u < kUnroll; ++u) load_vec<GD, NT>(g, i + u * kThreads * N, x[u]);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc = fma(double(x[u][e]), double(x[u][e]), acc);
+  }
+  for (; i + N <= n; i += kThreads * N) {
+    float x[N];
+    load_vec<GD, NT>(g, i, x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc = fma(double(x[e]), double(x[e]), acc);
   }
   for (; i < n; ++i) {                           // the thread whose vector the end cuts
     const double x = load_one<GD>(g, i);
@@ -95,9 +110,12 @@ __global__ __launch_bounds__(kThreads) void grad_norm_parts_kernel(const NormLau
   const int n = last ? int(I.tail) : L.part_elems;
   const int64_t lo = int64_t(k) * L.part_elems;
   double acc = 0.0;
-  if (I.g > 1)
-    acc = I.g & 1 ? squares<1>(reinterpret_cast<const float*>(I.g - 1) + lo, n)
-                  : squares<0>(reinterpret_cast<const uint16_t*>(I.g) + lo, n);
+  if (I.g > 1) {
+    const float* const f = reinterpret_cast<const float*>(I.g - 1) + lo;
+    const uint16_t* const h = reinterpret_cast<const uint16_t*>(I.g) + lo;
+    if (L.part0 + b >= L.keep_part) acc = I.g & 1 ? squares<1, false>(f, n) : squares<0, false>(h, n);
+    else acc = I.g & 1 ? squares<1, true>(f, n) : squares<0, true>(h, n);
+  }
   const double sum = block_sum<kThreads>(acc);
   if (threadIdx.x == 0) {
     L.partial[b] = sum;
@@ -156,10 +174,10 @@ __device__ __forceinline__ void scale_chunk(void* G, int64_t base, int64_t n, fl
     const int64_t i = base + int64_t(u * kThreads + threadIdx.x) * kVec;
     if (i + kVec <= n) {
       float x[kVec];
-      load_vec<GD>(G, i, x);
+      load_vec<GD, false>(G, i, x);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) x[e] *= s;
-      store_vec<GD>(G, i, x);
+      store_vec<GD, false>(G, i, x);
     } else {
       for (int64_t j = i; j < n; ++j) store_one<GD>(G, j, load_one<GD>(G, j) * s);
     }
@@ -176,26 +194,25 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ScaleLaunch 
   else scale_chunk<0>(reinterpret_cast<void*>(I.g), base, I.numel, s);
 }
 
-int check_grads(const muon_grad_plan* plan, const void* const* grads, int64_t n,
-                bool written, std::vector<Range>& rs) {
+int check_grads(const muon_grad_plan* plan, const void* const* grads, int64_t n) {
   if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
   if (n != (int64_t)plan->numel.size())
     return fail(MUON_ERR_INVALID_ARG, "n = %lld but the plan has %zu gradients", (long long)n,
                 plan->numel.size());
   if (n > 0 && !grads) return fail(MUON_ERR_INVALID_ARG, "grads is NULL");
-  for (int64_t i = 0; i < n; ++i) {
-    if (!grads[i] || plan->numel[i] == 0) continue;
-    if (!is_aligned16(grads[i]))
+  for (int64_t i = 0; i < n; ++i)
+    if (!is_aligned16(grads[i]) && plan->numel[i] > 0)
       return fail(MUON_ERR_INVALID_ARG, "gradient %lld must be 16-byte aligned", (long long)i);
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
-    rs.push_back({lo, lo + (size_t)plan->numel[i] * dtype_bytes(plan->dtype[i]), written});
-  }
   return MUON_OK;
 }
 
-void add_range(std::vector<Range>& rs, const void* p, size_t bytes, bool written) {
+Range range_of(const void* p, size_t bytes, bool written) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  rs.push_back({lo, lo + bytes, written});
+  return {lo, lo + bytes, written};
+}
+
+Range grad_range(const muon_grad_plan* plan, const void* const* grads, int64_t i, bool written) {
+  return range_of(grads[i], grads[i] ? plan->numel[i] * dtype_bytes(plan->dtype[i]) : 0, written);
 }
 
 size_t partial_bytes(const muon_grad_plan* plan) {
@@ -249,6 +266,15 @@ int muon_grad_plan_create(muon_grad_plan** out, const int64_t* numel, const muon
       parts += std::max<int64_t>(1, (numel[i] + made.part_elems - 1) / made.part_elems);
     }
     made.part0.push_back((int)parts);
+    // the last gradients' parts that fit the memory-side cache
+    int64_t bytes = 0;
+    made.keep_part = (int)parts;
+    for (int64_t i = n - 1; i >= 0 && bytes < kCacheBytes; --i) {
+      const int64_t size = (int64_t)dtype_bytes(dtype[i]), part = made.part_elems * size;
+      const int64_t fit = std::min(numel[i] * size, kCacheBytes - bytes) / part + 1;
+      made.keep_part = std::max(made.part0[i], made.part0[i + 1] - (int)fit);
+      bytes += numel[i] * size;
+    }
     *out = new muon_grad_plan(std::move(made));
     return MUON_OK;
   });
@@ -265,24 +291,35 @@ int muon_grad_norm(const muon_grad_plan* plan, const void* const* grads, int64_t
                    float max_norm, float* out, float* norms, void* workspace,
                    size_t workspace_bytes, hipStream_t stream) {
   return c_entry([&]() -> int {
-    std::vector<Range> rs;
-    if (int st = check_grads(plan, grads, n, false, rs)) return st;
+    if (int st = check_grads(plan, grads, n)) return st;
     if (!(max_norm >= 0.f))
       return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no clipping)");
     if (!out) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
     const size_t need = muon_grad_plan_workspace_size(plan);
     if (need > 0 && (!workspace || !is_aligned16(workspace) || workspace_bytes < need))
       return fail(MUON_ERR_WORKSPACE, "a workspace of %zu bytes, 16-byte aligned, is needed", need);
-    add_range(rs, out, 2 * sizeof(float), true);
-    if (norms && n > 0) add_range(rs, norms, n * sizeof(float), true);
-    if (need > 0) add_range(rs, workspace, need, true);
-    if (int st = check_overlaps(rs)) return st;
+    // three written buffers against each other and the gradients (which may overlap one another)
+    const Range w[3] = {range_of(out, 2 * sizeof(float), true),
+                        range_of(norms, norms ? n * sizeof(float) : 0, true),
+                        range_of(workspace, need, true)};
+    auto meet = [](const Range& a, const Range& b) {
+      return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
+    };
+    bool clash = meet(w[0], w[1]) || meet(w[0], w[2]) || meet(w[1], w[2]);
+    for (int64_t i = 0; i < n && !clash; ++i) {
+      const Range g = grad_range(plan, grads, i, false);
+      clash = meet(g, w[0]) || meet(g, w[1]) || meet(g, w[2]);
+    }
+    if (clash)
+      return fail(MUON_ERR_INVALID_ARG, "out, norms and the workspace must not overlap one "
+                  "another or a gradient");
 
     double* const partial = static_cast<double*>(workspace);
     int* const tensor_part =
         n > 0 ? reinterpret_cast<int*>(static_cast<char*>(workspace) + partial_bytes(plan)) : nullptr;
     NormLaunch L;
     L.part_elems = (int)plan->part_elems;
+    L.keep_part = plan->keep_part;
     for (int64_t at = 0; at < n; at += kNormItems) {
       L.count = (int)std::min<int64_t>(kNormItems, n - at);
       L.part0 = plan->part0[at];
@@ -311,10 +348,13 @@ int muon_grad_norm(const muon_grad_plan* plan, const void* const* grads, int64_t
 int muon_grad_scale(const muon_grad_plan* plan, void* const* grads, int64_t n,
                     const float* scale, hipStream_t stream) {
   return c_entry([&]() -> int {
-    std::vector<Range> rs;
-    if (int st = check_grads(plan, grads, n, true, rs)) return st;
+    if (int st = check_grads(plan, grads, n)) return st;
     if (!scale) return fail(MUON_ERR_INVALID_ARG, "scale is NULL");
-    add_range(rs, scale, sizeof(float), false);
+    std::vector<Range> rs;
+    rs.reserve(n + 1);
+    for (int64_t i = 0; i < n; ++i)
+      if (grads[i] && plan->numel[i] > 0) rs.push_back(grad_range(plan, grads, i, true));
+    rs.push_back(range_of(scale, sizeof(float), false));
     if (int st = check_overlaps(rs)) return st;
     constexpr int64_t kMaxBlocks = kMaxTensorElems / kScaleChunk;   // per launch
     ScaleLaunch L;

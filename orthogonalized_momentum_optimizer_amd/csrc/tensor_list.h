@@ -15,11 +15,11 @@ namespace muon {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// A tensor's blocks of 4096 elements then fit one launch (under 2^32 threads).
 constexpr int64_t kMaxTensorElems = int64_t(1) << 35;
 
 // Two floats -> two bfloat16 in one dword (lo = first), round to nearest even.
@@ -28,48 +28,54 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// N (a multiple of 8) consecutive elements of a bf16 (DT 0) or fp32 (DT 1) buffer, 16-byte
-// aligned: 16-byte accesses.
-template <int DT, int N>
+template <bool NT, typename T>
+__device__ __forceinline__ T load_at(const T* p) {
+  return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void store_at(T* p, T x) {
+  if (NT) __builtin_nontemporal_store(x, p);
+  else *p = x;
+}
+
+// N (4 or 8) consecutive elements of a bf16 (DT 0) or fp32 (DT 1) buffer, aligned to N elements or
+// 16 bytes: accesses of 16 bytes (of 8 for 4 bf16). NT: nontemporal.
+template <int DT, bool NT, int N>
 __device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&x)[N]) {
-  static_assert(N % 8 == 0, "whole 16-byte accesses");
+  static_assert(N == 4 || N == 8, "elements of an access or two");
   if (DT == 0) {
-    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
+    typedef uint32_t W __attribute__((ext_vector_type(N / 2)));
+    const W w = load_at<NT>(reinterpret_cast<const W*>(static_cast<const uint16_t*>(base) + i));
 #pragma unroll
-    for (int a = 0; a < N / 8; ++a) {
-      const u32x4 w = q[a];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[8 * a + 2 * k] = __uint_as_float(w[k] << 16);
-        x[8 * a + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
+    for (int k = 0; k < N / 2; ++k) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   } else {
     const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
 #pragma unroll
     for (int a = 0; a < N / 4; ++a) {
-      const f32x4 w = q[a];
+      const f32x4 w = load_at<NT>(q + a);
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[4 * a + k] = w[k];
     }
   }
 }
 
-template <int DT, int N>
+template <int DT, bool NT, int N>
 __device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&x)[N]) {
-  static_assert(N % 8 == 0, "whole 16-byte accesses");
+  static_assert(N == 4 || N == 8, "elements of an access or two");
   if (DT == 0) {
-    u32x4* q = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + i);
+    typedef uint32_t W __attribute__((ext_vector_type(N / 2)));
+    W w;
 #pragma unroll
-    for (int a = 0; a < N / 8; ++a)
-      q[a] = u32x4{pack_bf16x2(x[8 * a], x[8 * a + 1]), pack_bf16x2(x[8 * a + 2], x[8 * a + 3]),
-                   pack_bf16x2(x[8 * a + 4], x[8 * a + 5]),
-                   pack_bf16x2(x[8 * a + 6], x[8 * a + 7])};
+    for (int k = 0; k < N / 2; ++k) w[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+    store_at<NT>(reinterpret_cast<W*>(static_cast<uint16_t*>(base) + i), w);
   } else {
     f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + i);
 #pragma unroll
     for (int a = 0; a < N / 4; ++a)
-      q[a] = f32x4{x[4 * a], x[4 * a + 1], x[4 * a + 2], x[4 * a + 3]};
+      store_at<NT>(q + a, f32x4{x[4 * a], x[4 * a + 1], x[4 * a + 2], x[4 * a + 3]});
   }
 }
 

@@ -337,6 +337,35 @@ def test_offsets_beyond_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_fp32_states_of_more_than_one_piece():
+    """One bf16 tensor of 2^32 + 5000 elements with fp32 states (51 GB), cut into two pieces of the
+    launch: elements around 2^31, the cut and the ends step as the formula says, no other moves."""
+    n = 2 ** 32 + 5000
+    print(f"[adamw] {n} elements, fp32 states", flush=True)
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device=dev()) for _ in "pg")
+    m, v = (torch.zeros(n, device=dev()) for _ in "mv")
+    plan = om.AdamWPlan([p], [m], [v], [torch.bfloat16])
+    cfg = om.make_adamw_config(1e-2, (0.9, 0.99), 1e-8, 0.0, 3)
+    spans = [(a - 600, a + 600) for a in (2 ** 31, 2 ** 32)] + [(0, 1000), (n - 1160, n)]
+    r = np.random.default_rng(1)
+    for a, b in spans:
+        g[a:b] = on(r.normal(0, 1, b - a), torch.bfloat16)
+    plan.step([g], cfg)
+    torch.cuda.synchronize()
+    for a, b in spans:
+        gs = f64(g[a:b])
+        want, wm, wv = oa.adamw_step(np.zeros(b - a), gs, np.zeros(b - a), np.zeros(b - a), 3,
+                                     cfg.lr, cfg.beta1, cfg.beta2, cfg.eps)
+        assert np.all(np.abs(f64(m[a:b]) - wm) <= 4 * E32 * np.abs(wm))
+        assert np.all(np.abs(f64(v[a:b]) - wv) <= 6 * E32 * wv)
+        assert np.all(np.abs(f64(p[a:b]) - want) <= (2.0 ** -8 + 20 * E32) * np.abs(want))
+    total = sum(b - a for a, b in spans)
+    assert total - 20 <= int((p != 0).sum()) <= total
+    assert int((m != 0).sum()) <= total
+    del p, g, m, v, plan
+    torch.cuda.empty_cache()
+
+
 # ---- gradient norm ---------------------------------------------------------------------------
 
 def norm_bound(x):
