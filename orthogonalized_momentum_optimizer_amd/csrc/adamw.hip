@@ -31,9 +31,12 @@ constexpr int kVec = 4;
 constexpr int kChunkF32 = kThreadsF32 * kVec;
 // Shared memory that such a block asks for and does not use: 16 blocks fit a compute unit, not 32.
 constexpr int kHoldF32 = 10000;
-// 8-bit states
+// 8-bit states: GPT-2-124M's tables 274 us cached and with 16 neighbouring elements per lane, 242
+// with whole lines and nontemporal accesses (6.4 TB/s); blocks of 64, 128 and 512 threads 0 to 4%
+// slower. Here 5 blocks per compute unit measured 1% better than the 6 that fit.
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;                     // elements per block
+constexpr int kHold = 30000;
 constexpr int kOwn = kChunk / kThreads;          // elements per thread
 
 constexpr int kMaxItems = 480;                   // tensors per launch: their gradients' addresses
@@ -82,7 +85,7 @@ static_assert(sizeof(AdamwLaunch) <= 4096, "kernel arguments");
 template <typename T>
 using Constant = const __attribute__((address_space(4))) T*;
 
-// The tensor of block b, by bisection (8 scalar loads for 196 tensors).
+// The tensor of block b by bisection, log2(count) scalar loads one behind the other.
 __device__ __forceinline__ int bisect(const AdamwLaunch& L, int b) {
   const Constant<int> first = (Constant<int>)(uintptr_t)L.first;
   int lo = 0, hi = L.count;
@@ -94,8 +97,14 @@ __device__ __forceinline__ int bisect(const AdamwLaunch& L, int b) {
   return lo;
 }
 
+// The same by one or two vector loads.
+__device__ __forceinline__ int lookup(const AdamwLaunch& L, int b) {
+  return find_tensor([&](int i) { return L.first[i]; }, L.count, b);
+}
+
 // Blocks go from the last tensor to the first: a gradient norm, which goes the other way, has left
-// the last gradients in the memory-side cache (GPT-2-124M with it: 423 -> 411 us).
+// the last gradients in the memory-side cache (GPT-2-124M, 8-bit, with its norm: 346 us forwards, 336
+// backwards).
 __device__ __forceinline__ int block_of_launch() { return gridDim.x - 1 - blockIdx.x; }
 
 __device__ __forceinline__ Item item_of(const AdamwLaunch& L, int q) {
@@ -133,7 +142,8 @@ template <int PM, int GD>
 __global__ __launch_bounds__(kThreadsF32) void adamw_f32_kernel(const AdamwLaunch L) {
   constexpr int PD = PM == kBf16 ? 0 : 1;        // what p is read from
   const int b = block_of_launch();
-  const int q = bisect(L, b);
+  // 5 tensors: 510 us by bisection, 527 by vector loads; 196 tensors: 580 and 567
+  const int q = L.count <= 16 ? bisect(L, b) : lookup(L, b);
   const void* const G = L.g[q];
   float scale;
   if (!G || !read_scale(L.s, scale)) return;
@@ -173,27 +183,28 @@ __global__ __launch_bounds__(kThreadsF32) void adamw_f32_kernel(const AdamwLaunc
 
 // ---- 8-bit states ----------------------------------------------------------------------------
 //
-// A block of 256 elements is 32 lanes x 8 elements where all its streams are bf16 and codes, and 64
-// lanes x 4 where one is fp32: each access of a wave is one contiguous run, of whole lines. A
-// thread has kOwn elements, in groups 64 lanes apart.
+// A block of 256 elements lies over LANES lanes, each of which has pieces of PIECE elements of it,
+// LANES * PIECE apart. Every access of a wave is then made of whole 128-byte lines, and the
+// largest |x| of a block is found among few lanes:
+//   all streams bf16 or codes   16 lanes x 2 pieces of 8 (bf16 256 bytes, codes 128 in a run)
+//   one of them fp32            32 lanes x 2 pieces of 4 (fp32 512, bf16 256, codes 128)
+// A wave has 64 * kOwn consecutive elements, four blocks.
 
 template <int CTRL>
 __device__ __forceinline__ float row_rotate(float x) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
 }
 
-// The largest of x >= 0 over the lanes of a block, in every lane.
-template <int LANE>
+// The largest of x over the lanes of a block, in every lane.
+template <int LANES>
 __device__ __forceinline__ float block_max(float x) {
   x = fmaxf(x, row_rotate<0x128>(x));            // over the row of 16 lanes
   x = fmaxf(x, row_rotate<0x124>(x));
   x = fmaxf(x, row_rotate<0x122>(x));
   x = fmaxf(x, row_rotate<0x121>(x));
-  if (LANE == 8)                                 // and the row beside it
-    return fmaxf(x, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401f)));
-  const int y = __float_as_int(x);               // and the other three (floats >= 0 order as integers)
-  return __int_as_float(max(max(__builtin_amdgcn_readlane(y, 0), __builtin_amdgcn_readlane(y, 16)),
-                            max(__builtin_amdgcn_readlane(y, 32), __builtin_amdgcn_readlane(y, 48))));
+  if (LANES == 32)                               // and the row beside it
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401f)));
+  return x;
 }
 
 // The smallest scale byte b with top <= T * 2^(b - 127): top = 2^(E - 127) * f has b = E - 8,
@@ -219,17 +230,17 @@ __device__ __forceinline__ int unset() {
   return w;
 }
 
-template <int LANE>                              // a lane's codes of one group
-using Codes = uint32_t __attribute__((ext_vector_type(LANE / 4)));
+template <int PIECE>                             // a piece's codes
+using Codes = uint32_t __attribute__((ext_vector_type(PIECE / 4)));
 
-// A lane's codes <-> floats, by the hardware's scaled conversions: exact one way, to nearest even or
+// A piece's codes <-> floats, by the hardware's scaled conversions: exact one way, to nearest even or
 // stochastically the other (up with the probability of what is cut off: the upper 20 of the 32
 // random bits are added below the format's last place). Measured over all codes and scales and
 // over random values, subnormals of the format included: bit by bit what adamw.h defines.
-template <int LANE>
-__device__ __forceinline__ void decode(const Codes<LANE> c, float scale, float* x) {
+template <int PIECE>
+__device__ __forceinline__ void decode(const Codes<PIECE> c, float scale, float* x) {
 #pragma unroll
-  for (int k = 0; k < LANE / 4; ++k) {
+  for (int k = 0; k < PIECE / 4; ++k) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, false);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[k], scale, true);
     x[4 * k] = a[0];
@@ -238,11 +249,11 @@ __device__ __forceinline__ void decode(const Codes<LANE> c, float scale, float* 
     x[4 * k + 3] = b[1];
   }
 }
-template <int LANE>
-__device__ __forceinline__ Codes<LANE> encode(const float* x, float scale) {
-  Codes<LANE> c;
+template <int PIECE>
+__device__ __forceinline__ Codes<PIECE> encode(const float* x, float scale) {
+  Codes<PIECE> c;
 #pragma unroll
-  for (int k = 0; k < LANE / 4; ++k) {
+  for (int k = 0; k < PIECE / 4; ++k) {
     i16x2 w = __builtin_bit_cast(i16x2, unset());
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k], x[4 * k + 1], scale, false);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[4 * k + 2], x[4 * k + 3], scale, true);
@@ -251,12 +262,12 @@ __device__ __forceinline__ Codes<LANE> encode(const float* x, float scale) {
   return c;
 }
 // Elements 2j and 2j + 1 take the halves of h(j ^ key): 16 random bits, then half of one.
-template <int LANE>
-__device__ __forceinline__ Codes<LANE> encode_stochastic(const float* x, float scale, uint32_t pair,
+template <int PIECE>
+__device__ __forceinline__ Codes<PIECE> encode_stochastic(const float* x, float scale, uint32_t pair,
                                                          uint32_t key) {
-  Codes<LANE> c;
+  Codes<PIECE> c;
 #pragma unroll
-  for (int k = 0; k < LANE / 4; ++k) {
+  for (int k = 0; k < PIECE / 4; ++k) {
     const uint32_t h0 = mix32((pair + 2 * k) ^ key), h1 = mix32((pair + 2 * k + 1) ^ key);
     int w = unset();
     w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[4 * k], h0 << 16 | 0x8000u, scale, 0);
@@ -290,148 +301,173 @@ __device__ __forceinline__ void moments(const Step& S, float g, float& m, float&
 }
 
 // The chunk from element `base` on; FULL: it ends inside the tensor.
-template <int PM, int GD, int LANE, bool FULL>
-__device__ __forceinline__ void step_8bit(const Item& I, const void* G, const Step& S, float scale,
-                                          int64_t base) {
-  constexpr int PD = PM == kBf16 ? 0 : 1, GROUPS = kOwn / LANE;
+template <int PM, int GD, bool FULL>
+__device__ __forceinline__ void step_8bit(const Item& I, const void* grad, const Step& S,
+                                          float scale, int64_t base) {
+  constexpr int PD = PM == kBf16 ? 0 : 1;
+  constexpr bool NARROW = PM == kBf16 && GD == 0;
+  constexpr int LANES = NARROW ? 16 : 32, PIECE = NARROW ? 8 : 4;
+  constexpr int PER = MUON_ADAMW_BLOCK / (LANES * PIECE);    // pieces of a lane in a block
+  constexpr int PIECES = kOwn / PIECE, BLOCKS = PIECES / PER;
   const float lam = S.weight_decay * I.wd_mul;
-  void* const P = PM == kMaster ? I.w : I.p;
-  uint8_t* const M = static_cast<uint8_t*>(I.m);
-  uint8_t* const V = static_cast<uint8_t*>(I.v);
-  const int64_t own = base + int64_t(threadIdx.x / 64) * (64 * kOwn) + (threadIdx.x & 63) * LANE;
-  auto element = [&](int u) { return own + u * 64 * LANE; };
-  auto inside = [&](int u) {                     // of the group's elements
-    return FULL ? LANE : int(min<int64_t>(max<int64_t>(I.numel - element(u), 0), LANE));
+  // the chunk's own addresses, and elements and blocks counted from there in 32 bits
+  char* const P = static_cast<char*>(PM == kMaster ? I.w : I.p) + base * (PD ? 4 : 2);
+  uint16_t* const H = static_cast<uint16_t*>(I.p) + base;    // the parameter beside a master
+  const char* const G = static_cast<const char*>(grad) + base * (GD ? 4 : 2);
+  uint8_t* const M = static_cast<uint8_t*>(I.m) + base;
+  uint8_t* const V = static_cast<uint8_t*>(I.v) + base;
+  uint8_t* const MS = I.ms + base / MUON_ADAMW_BLOCK;
+  uint8_t* const VS = I.vs + base / MUON_ADAMW_BLOCK;
+  const uint32_t left = FULL ? kChunk : uint32_t(I.numel - base);
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t first = threadIdx.x / 64 * (64 * kOwn) + lane / LANES * MUON_ADAMW_BLOCK;
+  auto block = [&](int k) { return first / MUON_ADAMW_BLOCK + k * (64 / LANES); };
+  auto element = [&](int x) {                    // the first of piece x
+    return first + x / PER * (64 / LANES * MUON_ADAMW_BLOCK) + x % PER * (LANES * PIECE) +
+           lane % LANES * PIECE;
+  };
+  auto inside = [&](int x) {                     // of the piece's elements
+    return FULL ? PIECE : int(min(left - min(left, element(x)), uint32_t(PIECE)));
   };
 
-  float p[GROUPS][LANE], g[GROUPS][LANE], m[kOwn], r[kOwn];
-  Codes<LANE> mc[GROUPS], rc[GROUPS];
-  int mb[GROUPS], rb[GROUPS];
+  float p[PIECES][PIECE], g[PIECES][PIECE], m[kOwn], r[kOwn];
+  Codes<PIECE> mc[PIECES], rc[PIECES];
+  int mb[BLOCKS], rb[BLOCKS];
 #pragma unroll
-  for (int u = 0; u < GROUPS; ++u) {
-    const int64_t i = element(u);
-    const int cnt = inside(u);
-    mb[u] = rb[u] = 0;
-    if (cnt > 0) {
-      mb[u] = I.ms[i / MUON_ADAMW_BLOCK];
-      rb[u] = I.vs[i / MUON_ADAMW_BLOCK];
+  for (int k = 0; k < BLOCKS; ++k) {
+    mb[k] = rb[k] = 0;
+    if (FULL || block(k) * MUON_ADAMW_BLOCK < left) {
+      mb[k] = MS[block(k)];
+      rb[k] = VS[block(k)];
     }
-    if (cnt == LANE) {
-      load_vec<PD, true>(P, i, p[u]);
-      load_vec<GD, true>(G, i, g[u]);
-      mc[u] = load_at<true>(reinterpret_cast<const Codes<LANE>*>(M + i));
-      rc[u] = load_at<true>(reinterpret_cast<const Codes<LANE>*>(V + i));
-    } else {
-      mc[u] = rc[u] = Codes<LANE>(0);
+  }
 #pragma unroll
-      for (int e = 0; e < LANE; ++e) {
-        p[u][e] = g[u][e] = 0.f;
+  for (int x = 0; x < PIECES; ++x) {
+    const uint32_t i = element(x);
+    const int cnt = inside(x);
+    if (cnt == PIECE) {
+      load_vec<PD, true>(P, i, p[x]);
+      load_vec<GD, true>(G, i, g[x]);
+      mc[x] = load_at<true>(reinterpret_cast<const Codes<PIECE>*>(M + i));
+      rc[x] = load_at<true>(reinterpret_cast<const Codes<PIECE>*>(V + i));
+    } else {
+      mc[x] = rc[x] = Codes<PIECE>(0);
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) {
+        p[x][e] = g[x][e] = 0.f;
         if (e < cnt) {
-          p[u][e] = load_one<PD>(P, i + e);
-          g[u][e] = load_one<GD>(G, i + e);
-          mc[u][e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
-          rc[u][e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
+          p[x][e] = load_one<PD>(P, i + e);
+          g[x][e] = load_one<GD>(G, i + e);
+          mc[x][e >> 2] |= uint32_t(M[i + e]) << (8 * (e & 3));
+          rc[x][e >> 2] |= uint32_t(V[i + e]) << (8 * (e & 3));
         }
       }
     }
   }
 
-  float mtop[GROUPS], vtop[GROUPS];
+  float mtop[BLOCKS], vtop[BLOCKS];
   uint32_t vlow = ~0u;                           // the smallest v over 0, less one unit
 #pragma unroll
-  for (int u = 0; u < GROUPS; ++u) {
-    float* const mu = m + u * LANE;
-    float* const ru = r + u * LANE;
-    decode<LANE>(mc[u], scale_of(mb[u]), mu);
-    decode<LANE>(rc[u], scale_of(rb[u]), ru);
-    mtop[u] = vtop[u] = 0.f;
+  for (int k = 0; k < BLOCKS; ++k) mtop[k] = vtop[k] = 0.f;
 #pragma unroll
-    for (int e = 0; e < LANE; ++e) {
-      float v = ru[e] * ru[e];
-      moments(S, g[u][e] * scale, mu[e], v);
-      asm("" : "+v"(mu[e]));                     // kept, not computed again behind the branch
-      ru[e] = v;
-      mtop[u] = fmaxf(mtop[u], fabsf(mu[e]));
-      vtop[u] = fmaxf(vtop[u], v);
+  for (int x = 0; x < PIECES; ++x) {
+    const int k = x / PER;
+    float* const mx = m + x * PIECE;
+    float* const rx = r + x * PIECE;
+    decode<PIECE>(mc[x], scale_of(mb[k]), mx);
+    decode<PIECE>(rc[x], scale_of(rb[k]), rx);
+#pragma unroll
+    for (int e = 0; e < PIECE; ++e) {
+      float v = rx[e] * rx[e];
+      moments(S, g[x][e] * scale, mx[e], v);
+      asm("" : "+v"(mx[e]));                     // kept, not computed again behind the branch
+      rx[e] = v;
+      mtop[k] = fmaxf(mtop[k], fabsf(mx[e]));
+      vtop[k] = fmaxf(vtop[k], v);
       vlow = min(vlow, __float_as_uint(v) - 1u);
     }
   }
   // rare, and the whole wave's: a v that root() does not take
   bool wide = vlow < 0x0d000000u - 1u;
 #pragma unroll
-  for (int u = 0; u < GROUPS; ++u) wide = wide || vtop[u] > 3.402823466e38f;
-  float rtop[GROUPS];                            // of the block: its largest v's root
+  for (int k = 0; k < BLOCKS; ++k) wide = wide || vtop[k] > 3.402823466e38f;
+  float rtop[BLOCKS];                            // of the block: its largest v's root
 #pragma unroll
-  for (int u = 0; u < GROUPS; ++u) rtop[u] = block_max<LANE>(vtop[u]);
+  for (int k = 0; k < BLOCKS; ++k) rtop[k] = block_max<LANES>(vtop[k]);
   if (__any(wide)) {
 #pragma unroll
     for (int e = 0; e < kOwn; ++e) r[e] = sqrtf(r[e]);
 #pragma unroll
-    for (int u = 0; u < GROUPS; ++u)             // an infinite v is held as the largest finite one
-      rtop[u] = sqrtf(fminf(rtop[u], 3.402823466e38f));
+    for (int k = 0; k < BLOCKS; ++k)             // an infinite v is held as the largest finite one
+      rtop[k] = sqrtf(fminf(rtop[k], 3.402823466e38f));
   } else {
 #pragma unroll
     for (int e = 0; e < kOwn; ++e) r[e] = root(r[e]);
 #pragma unroll
-    for (int u = 0; u < GROUPS; ++u) rtop[u] = root(rtop[u]);
+    for (int k = 0; k < BLOCKS; ++k) rtop[k] = root(rtop[k]);
   }
 
 #pragma unroll
-  for (int u = 0; u < GROUPS; ++u) {
-    const int64_t i = element(u);
-    const int cnt = inside(u);
-    float* const mu = m + u * LANE;
-    float* const ru = r + u * LANE;
-#pragma unroll
-    for (int e = 0; e < LANE; ++e) p[u][e] = updated(S, lam, p[u][e], mu[e], ru[e]);
-    mb[u] = scale_byte(block_max<LANE>(mtop[u]));
-    rb[u] = scale_byte(rtop[u]);
-    const float rs = scale_of(rb[u]);
+  for (int k = 0; k < BLOCKS; ++k) {
+    mb[k] = scale_byte(block_max<LANES>(mtop[k]));
+    rb[k] = scale_byte(rtop[k]);
+    const float rs = scale_of(rb[k]);
     const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, 0x1.fffffep63f);
 #pragma unroll
-    for (int e = 0; e < LANE; ++e)              // NaN and 0 as they are
-      ru[e] = ru[e] > 0.f ? __builtin_amdgcn_fmed3f(ru[e], low, high) : ru[e];
-    mc[u] = encode<LANE>(mu, scale_of(mb[u]));
-    if (S.stochastic) {
-      const uint64_t pair = uint64_t(i) >> 1;
-      rc[u] = encode_stochastic<LANE>(ru, rs, uint32_t(pair), S.key ^ uint32_t(pair >> 32) * 0xEB26D985u);
-    } else {
-      rc[u] = encode<LANE>(ru, rs);
-    }
-    if (cnt == LANE) {
-      store_vec<PD, true>(P, i, p[u]);
-      if (PM == kMaster) store_vec<0, true>(I.p, i, p[u]);
-      store_at<true>(reinterpret_cast<Codes<LANE>*>(M + i), mc[u]);
-      store_at<true>(reinterpret_cast<Codes<LANE>*>(V + i), rc[u]);
-    } else {
+    for (int x = k * PER; x < (k + 1) * PER; ++x) {
+      const uint32_t i = element(x);
+      const int cnt = inside(x);
+      float* const mx = m + x * PIECE;
+      float* const rx = r + x * PIECE;
 #pragma unroll
-      for (int e = 0; e < LANE; ++e)
-        if (e < cnt) {
-          store_one<PD>(P, i + e, p[u][e]);
-          if (PM == kMaster) store_one<0>(I.p, i + e, p[u][e]);
-          M[i + e] = uint8_t(mc[u][e >> 2] >> (8 * (e & 3)));
-          V[i + e] = uint8_t(rc[u][e >> 2] >> (8 * (e & 3)));
-        }
+      for (int e = 0; e < PIECE; ++e) {
+        p[x][e] = updated(S, lam, p[x][e], mx[e], rx[e]);
+        // NaN and 0 as they are
+        rx[e] = rx[e] > 0.f ? __builtin_amdgcn_fmed3f(rx[e], low, high) : rx[e];
+      }
+      mc[x] = encode<PIECE>(mx, scale_of(mb[k]));
+      if (S.stochastic) {
+        // a chunk's pairs do not cross a multiple of 2^32
+        const uint32_t pair = uint32_t(uint64_t(base) >> 1) + i / 2;
+        rc[x] = encode_stochastic<PIECE>(rx, rs, pair,
+                                         S.key ^ uint32_t(uint64_t(base) >> 33) * 0xEB26D985u);
+      } else {
+        rc[x] = encode<PIECE>(rx, rs);
+      }
+      if (cnt == PIECE) {
+        store_vec<PD, true>(P, i, p[x]);
+        if (PM == kMaster) store_vec<0, true>(H, i, p[x]);
+        store_at<true>(reinterpret_cast<Codes<PIECE>*>(M + i), mc[x]);
+        store_at<true>(reinterpret_cast<Codes<PIECE>*>(V + i), rc[x]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e)
+          if (e < cnt) {
+            store_one<PD>(P, i + e, p[x][e]);
+            if (PM == kMaster) store_one<0>(H, i + e, p[x][e]);
+            M[i + e] = uint8_t(mc[x][e >> 2] >> (8 * (e & 3)));
+            V[i + e] = uint8_t(rc[x][e >> 2] >> (8 * (e & 3)));
+          }
+      }
     }
-    if (threadIdx.x % (MUON_ADAMW_BLOCK / LANE) == 0 && cnt > 0) {
-      I.ms[i / MUON_ADAMW_BLOCK] = uint8_t(mb[u]);
-      I.vs[i / MUON_ADAMW_BLOCK] = uint8_t(rb[u]);
+    if (lane % LANES == 0 && (FULL || block(k) * MUON_ADAMW_BLOCK < left)) {
+      MS[block(k)] = uint8_t(mb[k]);
+      VS[block(k)] = uint8_t(rb[k]);
     }
   }
 }
 
 template <int PM, int GD>
 __global__ __launch_bounds__(kThreads) void adamw_8bit_kernel(const AdamwLaunch L) {
-  constexpr int LANE = PM == kBf16 && GD == 0 ? 8 : 4;
   const int b = block_of_launch();
-  const int q = find_tensor([&](int i) { return L.first[i]; }, L.count, b);
+  const int q = lookup(L, b);                    // 8% faster than bisection here, 772 tensors
   const void* const G = L.g[q];
   float scale;
   if (!G || !read_scale(L.s, scale)) return;
   const Item I = item_of(L, q);
   const int64_t base = int64_t(b - I.first) * kChunk;
-  if (base + kChunk <= I.numel) step_8bit<PM, GD, LANE, true>(I, G, L.s, scale, base);
-  else step_8bit<PM, GD, LANE, false>(I, G, L.s, scale, base);
+  if (base + kChunk <= I.numel) step_8bit<PM, GD, true>(I, G, L.s, scale, base);
+  else step_8bit<PM, GD, false>(I, G, L.s, scale, base);
 }
 
 // ---- the table -------------------------------------------------------------------------------
@@ -742,7 +778,7 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
       L.count = l.count;
       const bool f32 = plan->state == MUON_ADAMW_F32;
       hipLaunchKernelGGL(kernel_of(plan->state, l.pm, l.gd), dim3((unsigned)l.blocks),
-                         dim3(f32 ? kThreadsF32 : kThreads), f32 ? kHoldF32 : 0, stream, L);
+                         dim3(f32 ? kThreadsF32 : kThreads), f32 ? kHoldF32 : kHold, stream, L);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess)
         return fail(MUON_ERR_HIP, "launch of the AdamW kernel failed: %s", hipGetErrorString(e));

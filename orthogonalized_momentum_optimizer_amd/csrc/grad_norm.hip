@@ -28,7 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVec = 8;
 constexpr int kUnroll = 4;                       // loads of a thread in flight
-constexpr int64_t kMinPart = 16384;
+constexpr int64_t kMinPart = 32768;
 constexpr int64_t kMaxPart = int64_t(1) << 30;
 constexpr int64_t kMaxParts = 16384;             // beyond one per tensor
 constexpr int64_t kCacheBytes = int64_t(1) << 28;  // the memory-side cache: 256 MB
