@@ -49,7 +49,8 @@
  * enqueued. A step allocates nothing, and a plan is not changed by a step: steps on one plan
  * may be called from several host threads, but the buffers they update are the plan's, so that
  * the steps themselves must be ordered on the device. A captured step replays with the cfg it
- * was captured with, step index and seed included.
+ * was captured with, step index and seed included; the plan's buffers and its table must stay
+ * allocated as long as the graph is replayed.
  */
 #ifndef MUON_ADAMW_H
 #define MUON_ADAMW_H

@@ -75,6 +75,12 @@ class _TensorList:
                              f"on {self.device} expected")
         raise TypeError(f"gradient {out}: a dtype other than the plan's ({g.dtype})")
 
+    def fits(self, grads: Sequence[torch.Tensor]) -> bool:
+        """Whether the gradients have the plan's sizes, dtypes and device, and are contiguous."""
+        return (len(grads) == len(self._numels) and
+                not isinstance(L.tensor_addresses(grads, self._numels, self._dtypes,
+                                                  self.device.index), int))
+
     def _check_scalar(self, name, x):
         if x.numel() != 1 or x.dtype != torch.float32 or x.device != self.device:
             raise ValueError(f"{name} must be one float32 on {self.device}")
@@ -337,20 +343,26 @@ class AdamW(torch.optim.Optimizer):
 
     def _plan(self, gi, group, ps: List[torch.Tensor], grads):
         """The group's plan and the states of ``ps``. A plan is kept while the parameters, their
-        addresses, the gradients' dtypes and the decay's multiplier stay."""
+        addresses, the gradients' layout and the decay's multiplier stay."""
         cached = self._plans.get(gi)
         if cached is not None:
-            plan, of, wd_mul, states, numels, pdt, gdt, at = cached
+            plan, of, wd_mul, states, numels, pdt, at = cached
             if (len(of) == len(ps) and all(map(operator.is_, of, ps)) and wd_mul == group["wd_mul"]
-                    and gdt == [g.dtype for g in grads]):
+                    and plan.fits(grads)):
                 now = L.tensor_addresses(ps, numels, pdt, plan.device.index)
                 if not isinstance(now, int) and bytes(now) == at:
                     return plan, states
+        for p, g in zip(ps, grads):
+            if not p.is_contiguous() or not g.is_contiguous():
+                raise ValueError("AdamW needs contiguous parameters and gradients")
+            if "step" not in self.state[p]:
+                self._init_state(p, group)
         states = [self.state[p] for p in ps]
-        gdt = [g.dtype for g in grads]
         small = "exp_avg_scale" in states[0]
+        if any(("exp_avg_scale" in st) != small for st in states):
+            raise ValueError("a group's states must all have the same state_bits")
         plan = AdamWPlan([p.detach() for p in ps], [s["exp_avg"] for s in states],
-                         [s["exp_avg_sq"] for s in states], gdt,
+                         [s["exp_avg_sq"] for s in states], [g.dtype for g in grads],
                          [s.get("master") for s in states],
                          [s["exp_avg_scale"] for s in states] if small else None,
                          [s["exp_avg_sq_scale"] for s in states] if small else None,
@@ -359,7 +371,7 @@ class AdamW(torch.optim.Optimizer):
         numels = (ctypes.c_int64 * n)(*[p.numel() for p in ps])
         pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in ps])
         at = bytes((ctypes.c_void_p * n)(*[p.data_ptr() for p in ps]))
-        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, gdt, at)
+        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, at)
         return plan, states
 
     @torch.no_grad()
@@ -370,25 +382,21 @@ class AdamW(torch.optim.Optimizer):
                 loss = closure()
         todo = []
         for gi, group in enumerate(self.param_groups):
-            ps = [p for p in group["params"] if p.grad is not None]
-            grads = [p.grad for p in ps]
-            for p, g in zip(ps, grads):
-                if not p.is_contiguous() or not g.is_contiguous():
-                    raise ValueError("AdamW needs contiguous parameters and gradients")
-                if "step" not in self.state[p]:
-                    self._init_state(p, group)
+            grads = [p.grad for p in group["params"]]
+            ps = group["params"]
+            if any(g is None for g in grads):
+                ps = [p for p, g in zip(ps, grads) if g is not None]
+                grads = [g for g in grads if g is not None]
             if ps:
-                todo.append((gi, group, ps, grads))
+                todo.append((group, *self._plan(gi, group, ps, grads), grads))
         scale = None
         if self.max_grad_norm is not None and todo:
-            every = [g for _, _, _, grads in todo for g in grads]
-            key = [(g.numel(), g.dtype, g.get_device()) for g in every]
-            cached = self._plans.get("norm")
-            if cached is None or cached[0] != key:
-                cached = self._plans["norm"] = (key, GradNormPlan(every))
-            self.last_grad_norm, scale = cached[1].norm(every, self.max_grad_norm)
-        for gi, group, ps, grads in todo:
-            plan, states = self._plan(gi, group, ps, grads)
+            every = [g for *_, grads in todo for g in grads]
+            plan = self._plans.get("norm")
+            if plan is None or not plan.fits(every):
+                plan = self._plans["norm"] = GradNormPlan(every)
+            self.last_grad_norm, scale = plan.norm(every, self.max_grad_norm)
+        for group, plan, states, grads in todo:
             at = [st["step"] + 1 for st in states]
             for t in sorted(set(at)):
                 cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],

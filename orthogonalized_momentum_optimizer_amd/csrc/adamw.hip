@@ -41,8 +41,10 @@ constexpr int kOwn = kChunk / kThreads;          // elements per thread
 
 constexpr int kMaxItems = 480;                   // tensors per launch: their gradients' addresses
                                                  // travel by value, the rest is in the table
-constexpr int64_t kPiece = int64_t(1) << 32;     // elements of a tensor in one item
-constexpr int64_t kMaxBlocks = kPiece / kChunkF32;  // per launch: under 2^32 threads
+constexpr int64_t kPiece = int64_t(1) << 31;     // elements of a tensor in one item, fp32 states
+constexpr int64_t kMaxBlocks = int64_t(1) << 23; // per launch: under 2^32 threads
+static_assert(kPiece / kChunkF32 <= kMaxBlocks && kMaxTensorElems / kChunk <= kMaxBlocks,
+              "an item fits a launch");
 
 // Parameter modes: a bf16 parameter, an fp32 one, a bf16 one with an fp32 master copy.
 enum { kBf16 = 0, kF32 = 1, kMaster = 2 };
@@ -281,8 +283,9 @@ __device__ __forceinline__ Codes<PIECE> encode_stochastic(const float* x, float 
 
 // sqrt(v) rounded to nearest, for v = 0 and 2^-101 <= v < 2^128: one step of Newton's method from
 // the reciprocal root, whose residual v - s^2 is exact there. Compared with the compiler's sqrt
-// over every significand at even and odd exponents: equal (its own sequence, which also takes
-// the rest of the range, is twice as long, and the kernel is bound by instructions).
+// over every significand at even and odd exponents: equal. (Its own sequence, which also takes
+// the rest of the range, is twice as long; with it, a full division and conversions in steps the
+// kernel was bound by instructions: 294 us for the tables.)
 __device__ __forceinline__ float root(float v) {
   const float q = __builtin_amdgcn_rsqf(v + 0x1p-126f);       // v itself, but for 0
   const float s = v * q;
@@ -472,8 +475,7 @@ __global__ __launch_bounds__(kThreads) void adamw_8bit_kernel(const AdamwLaunch 
 
 // ---- the table -------------------------------------------------------------------------------
 
-constexpr int kUpload = 48;                      // items per launch (by value: a plan's upload may
-                                                 // be captured, and needs no pinned memory)
+constexpr int kUpload = 48;                      // items per launch (by value: no pinned memory)
 struct Upload {
   Item item[kUpload];
   Item* to;

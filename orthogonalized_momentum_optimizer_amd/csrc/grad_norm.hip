@@ -305,6 +305,8 @@ int muon_grad_norm(const muon_grad_plan* plan, const void* const* grads, int64_t
     if (!(max_norm >= 0.f))
       return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no clipping)");
     if (!out) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
+    if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(norms)) & 3)
+      return fail(MUON_ERR_INVALID_ARG, "out and norms must be 4-byte aligned");
     const size_t need = muon_grad_plan_workspace_size(plan);
     if (need > 0 && (!workspace || !is_aligned16(workspace) || workspace_bytes < need))
       return fail(MUON_ERR_WORKSPACE, "a workspace of %zu bytes, 16-byte aligned, is needed", need);
@@ -359,7 +361,8 @@ int muon_grad_scale(const muon_grad_plan* plan, void* const* grads, int64_t n,
                     const float* scale, hipStream_t stream) {
   return c_entry([&]() -> int {
     if (int st = check_grads(plan, grads, n)) return st;
-    if (!scale) return fail(MUON_ERR_INVALID_ARG, "scale is NULL");
+    if (!scale || (reinterpret_cast<uintptr_t>(scale) & 3))
+      return fail(MUON_ERR_INVALID_ARG, "scale must be non-NULL and 4-byte aligned");
     std::vector<Range> rs;
     rs.reserve(n + 1);
     for (int64_t i = 0; i < n; ++i)

@@ -219,6 +219,7 @@ def norm_call(mutate=lambda a: None):
     (dict(max_norm=math.nan), INV), (dict(out=None), INV), (dict(workspace=None), WS),
     (dict(workspace=BASE + (4 << 20) + 8), WS), (dict(workspace_bytes=3), WS),
     (dict(out=BASE + 1992), INV), (dict(norms=BASE + (2 << 20) + 4), INV),
+    (dict(out=BASE + (2 << 20) + 2), INV), (dict(norms=BASE + (3 << 20) + 1), INV),
     (dict(workspace=BASE + (3 << 20)), INV), (dict(grads=[BASE + 2, None, None]), INV)], ids=str)
 def test_grad_norm_rejects(change, status):
     got, msg = norm_call(lambda a: a.update(change))
@@ -231,7 +232,7 @@ def test_grad_scale_rejects():
     P = L.make_pointers
     for grads, n, scale in (([BASE, BASE + 1984], 2, BASE + 4096), ([BASE, BASE], 2, BASE + 4096),
                             ([BASE, None], 2, None), ([BASE, None], 1, BASE + 4096),
-                            ([BASE + 4, None], 2, BASE + 4096), ([BASE, None], 2, BASE + 1996)):
+                            ([BASE + 4, None], 2, BASE + 4096), ([BASE, None], 2, BASE + 4097), ([BASE, None], 2, BASE + 1996)):
         assert status_of(L.muon_grad_scale, plan, P(grads), n, scale, 0)[0] == INV
     L.muon_grad_scale(plan, P([None, None]), 2, BASE, 0)     # nothing to do: no HIP call
     L.muon_grad_plan_destroy(plan)

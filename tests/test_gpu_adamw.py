@@ -233,6 +233,11 @@ def test_special_values(small):
         for t in (1, 2):
             s.step_and_check(om.make_adamw_config(1e-2, (0.9, 0.99), 0.0, 0.0, t, seed=1),
                              s.grads(std), label=f"std {std} step {t}")
+    for std in (1e-30, 1e-36, 1e-41):              # v is zero, m and its scale at the bottom of fp32
+        s = Set([n], "f32", "f32", False, small, seed=3)
+        for t in (1, 2):
+            s.step_and_check(om.make_adamw_config(1e-2, (0.9, 0.99), 1e-8, 0.0, t, seed=1),
+                             s.grads(std), label=f"std {std} step {t}")
     s = Set([n], "f32", "f32", False, small, seed=4)                      # a late step
     s.step_and_check(om.make_adamw_config(1e-2, step=10 ** 9, seed=2 ** 63), s.grads())
     s = Set([n], "f32", "f32", False, small, seed=5)                      # no averaging at all
@@ -338,8 +343,8 @@ def test_offsets_beyond_32_bits():
 
 
 def test_fp32_states_of_more_than_one_piece():
-    """One bf16 tensor of 2^32 + 5000 elements with fp32 states (51 GB), cut into two pieces of the
-    launch: elements around 2^31, the cut and the ends step as the formula says, no other moves."""
+    """One bf16 tensor of 2^32 + 5000 elements with fp32 states (51 GB), cut into three pieces:
+    elements around the cuts at 2^31 and 2^32 and the ends step as the formula says, no other moves."""
     n = 2 ** 32 + 5000
     print(f"[adamw] {n} elements, fp32 states", flush=True)
     p, g = (torch.zeros(n, dtype=torch.bfloat16, device=dev()) for _ in "pg")
