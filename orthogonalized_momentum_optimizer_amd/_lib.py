@@ -141,10 +141,8 @@ _lib = None
 _args = None
 
 
-def tensor_addresses(tensors, numels, dtypes, device: int):
-    """The addresses of a list of tensors (None: 0) as a ctypes array, or the index of the first
-    one that is not a contiguous tensor of its ``numels`` and ``dtypes`` entry on ``device``.
-    ``numels``, ``dtypes``: ctypes arrays of int64 and of muon_dtype as int32."""
+def args():
+    """The native part of the binding (csrc/tensor_args.cpp); raises if it has not been built."""
     global _args
     if _args is None:
         try:
@@ -152,9 +150,21 @@ def tensor_addresses(tensors, numels, dtypes, device: int):
         except ImportError as e:
             raise RuntimeError("_tensor_args.so is missing: build it with `python -m "
                                "orthogonalized_momentum_optimizer_amd.build`") from e
+    return _args
+
+
+def tensor_addresses(tensors, numels, dtypes, device: int):
+    """The addresses of a list of tensors (None: 0) as a ctypes array, or the index of the first
+    one that is not a contiguous tensor of its ``numels`` and ``dtypes`` entry on ``device``.
+    ``numels``, ``dtypes``: ctypes arrays of int64 and of muon_dtype as int32."""
     out = (ctypes.c_void_p * len(numels))()
-    bad = _args.addresses(tensors, numels, dtypes, device, out)
+    bad = args().addresses(tensors, numels, dtypes, device, out)
     return out if bad < 0 else bad
+
+
+def address_of(function) -> int:
+    """The address of a function of the library."""
+    return ctypes.cast(function, ctypes.c_void_p).value
 
 
 def lib() -> ctypes.CDLL:
@@ -237,13 +247,17 @@ def status_string(status: int) -> str:
     return lib().muon_status_string(int(status)).decode()
 
 
+def raise_status(status: int) -> None:
+    raise MuonError(status, muon_last_error())
+
+
 def muon_last_error() -> str:
     return lib().muon_last_error().decode()
 
 
 def _check(status: int) -> None:
     if status != MUON_OK:
-        raise MuonError(status, muon_last_error())
+        raise_status(status)
 
 
 def muon_status_string(status: int) -> str:

@@ -20,6 +20,7 @@ from . import _lib as L
 from .optim import dtype_code
 
 _NOTHING = contextlib.nullcontext()
+_SCALE_AT = L.muon_adamw_config.grad_scale.offset
 # the current stream's handle without a Stream object around it (2 us of a 10 us step)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -57,33 +58,30 @@ class _TensorList:
         self._numels = (ctypes.c_int64 * n)(*numels)
         self._dtypes = (ctypes.c_int32 * n)(*[dtype_code(d) for d in dtypes])
 
-    def _pointers(self, grads: Sequence[Optional[torch.Tensor]]):
-        """The gradients' addresses, after checking them against the plan."""
-        n = len(self._numels)
+    def _list(self, grads: Sequence[Optional[torch.Tensor]]):
         if not isinstance(grads, (list, tuple)):
             grads = list(grads)
-        if len(grads) != n:
-            raise ValueError(f"expected {n} gradients, got {len(grads)}")
-        out = L.tensor_addresses(grads, self._numels, self._dtypes, self.device.index)
-        if not isinstance(out, int):
-            return out
-        g = grads[out]
+        if len(grads) != len(self._numels):
+            raise ValueError(f"expected {len(self._numels)} gradients, got {len(grads)}")
+        return grads
+
+    def _refuse(self, grads, code: int):
+        """Raises for what a native call returned: a gradient's index, or a status below 0."""
+        if code < 0:
+            L.raise_status(code)
+        g = grads[code]
         if not isinstance(g, torch.Tensor):
-            raise TypeError(f"gradient {out}: a tensor or None expected")
-        if g.numel() != self._numels[out] or not g.is_contiguous() or g.device != self.device:
-            raise ValueError(f"gradient {out}: a contiguous tensor of {self._numels[out]} elements "
-                             f"on {self.device} expected")
-        raise TypeError(f"gradient {out}: a dtype other than the plan's ({g.dtype})")
+            raise TypeError(f"gradient {code}: a tensor or None expected")
+        if g.numel() != self._numels[code] or not g.is_contiguous() or g.device != self.device:
+            raise ValueError(f"gradient {code}: a contiguous tensor of {self._numels[code]} "
+                             f"elements on {self.device} expected")
+        raise TypeError(f"gradient {code}: a dtype other than the plan's ({g.dtype})")
 
     def fits(self, grads: Sequence[torch.Tensor]) -> bool:
         """Whether the gradients have the plan's sizes, dtypes and device, and are contiguous."""
         return (len(grads) == len(self._numels) and
                 not isinstance(L.tensor_addresses(grads, self._numels, self._dtypes,
                                                   self.device.index), int))
-
-    def _check_scalar(self, name, x):
-        if x.numel() != 1 or x.dtype != torch.float32 or x.device != self.device:
-            raise ValueError(f"{name} must be one float32 on {self.device}")
 
     def _on(self, stream):
         """A context with the plan's device as the current one and ``stream`` (or the current
@@ -159,6 +157,7 @@ class AdamWPlan(_TensorList):
         self.state_bits = 8 if small else 32
         self.handle = L.muon_adamw_plan_create(L.make_adamw_tensors(entries) if n else None, n,
                                                L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
+        self._step = L.address_of(L.lib().muon_adamw_step)
         self._held = held
         size = L.muon_adamw_plan_table_size(self.handle)
         if size:
@@ -175,13 +174,12 @@ class AdamWPlan(_TensorList):
              stream: Optional[torch.cuda.Stream] = None) -> None:
         """One step. A gradient may be None: its parameter is left out. ``grad_scale``: one
         float32 on the device that every gradient is multiplied by (``GradNormPlan.norm``'s)."""
-        ptrs = self._pointers(grads)
-        if grad_scale is not None:
-            self._check_scalar("grad_scale", grad_scale)
-            cfg = L.muon_adamw_config.from_buffer_copy(cfg)
-            cfg.grad_scale = grad_scale.data_ptr()
+        grads = self._list(grads)
         with self._on(stream):
-            L.muon_adamw_step(self.handle, ptrs, len(ptrs), cfg, self._stream())
+            code = L.args().adamw_step(self._step, self.handle or 0, grads, self._numels, self._dtypes,
+                                       self.device.index, cfg, grad_scale, _SCALE_AT, self._stream())
+        if code is not None:
+            self._refuse(grads, code)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -205,31 +203,32 @@ class GradNormPlan(_TensorList):
         self._set_list(_one_device(grads), [g.numel() for g in grads], [g.dtype for g in grads])
         self.handle = L.muon_grad_plan_create(list(self._numels), list(self._dtypes))
         self.ws_bytes = L.muon_grad_plan_workspace_size(self.handle)
+        self._norm = L.address_of(L.lib().muon_grad_norm)
 
     def norm(self, grads: Sequence[Optional[torch.Tensor]], max_norm: float = math.inf,
              per_tensor: bool = False, stream: Optional[torch.cuda.Stream] = None):
         """(norm, scale), or with ``per_tensor`` (norm, scale, norms): float32 on the device,
         new tensors each call. scale = min(1, max_norm / norm), NaN for a norm that is not
         finite. A gradient that is None counts as zero. The workspace belongs to the call."""
-        ptrs = self._pointers(grads)
-        n = len(self._numels)
-        each = n if per_tensor else 0
-        ws = (2 + each + 3) // 4 * 4                  # 16-byte aligned, behind the results
+        grads = self._list(grads)
         with self._on(stream):
-            out = torch.empty(ws + (self.ws_bytes + 3) // 4, dtype=torch.float32, device=self.device)
-            base = out.data_ptr()
-            L.muon_grad_norm(self.handle, ptrs, n, max_norm, base, base + 8 if each else None,
-                             base + 4 * ws if self.ws_bytes else None, self.ws_bytes, self._stream())
-        if per_tensor:
-            return out[0], out[1], out[2:2 + n]
-        return out[0], out[1]
+            out = L.args().grad_norm(self._norm, self.handle or 0, grads, self._numels, self._dtypes,
+                                     self.device.index, max_norm, per_tensor, self.ws_bytes,
+                                     self._stream())
+        if isinstance(out, int):
+            self._refuse(grads, out)
+        return out
 
     def scale_(self, grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:
         """Multiplies every gradient by ``scale`` (one float32 on the device) in place; where it
         is 1 nothing is read or written."""
-        ptrs = self._pointers(grads)
-        self._check_scalar("scale", scale)
+        grads = self._list(grads)
+        if scale.numel() != 1 or scale.dtype != torch.float32 or scale.device != self.device:
+            raise ValueError(f"scale must be one float32 on {self.device}")
+        ptrs = L.tensor_addresses(grads, self._numels, self._dtypes, self.device.index)
+        if isinstance(ptrs, int):
+            self._refuse(grads, ptrs)
         with self._on(stream):
             L.muon_grad_scale(self.handle, ptrs, len(ptrs), scale.data_ptr(), self._stream())
 
