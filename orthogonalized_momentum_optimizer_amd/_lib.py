@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 import torch  # noqa: F401  (loads the HIP runtime the library must share)
@@ -156,7 +157,8 @@ def args():
 def tensor_addresses(tensors, numels, dtypes, device: int):
     """The addresses of a list of tensors (None: 0) as a ctypes array, or the index of the first
     one that is not a contiguous tensor of its ``numels`` and ``dtypes`` entry on ``device``.
-    ``numels``, ``dtypes``: ctypes arrays of int64 and of muon_dtype as int32."""
+    ``numels``, ``dtypes``: ctypes arrays of int64 and of muon_dtype as int32 (2: float8_e4m3fn,
+    3: float8_e8m0fnu)."""
     out = (ctypes.c_void_p * len(numels))()
     bad = args().addresses(tensors, numels, dtypes, device, out)
     return out if bad < 0 else bad
@@ -376,6 +378,15 @@ def make_adamw_tensors(entries) -> ctypes.Array:
     for i, e in enumerate(entries):
         arr[i] = muon_adamw_tensor(*e)
     return arr
+
+
+def pack_adamw_tensors(columns) -> ctypes.Array:
+    """The same from whole columns of those fields (None: a NULL pointer)."""
+    rows = list(zip(*columns))
+    pack = struct.Struct("@6Pqiif0q").pack
+    raw = b"".join(pack(*[x or 0 for x in r[:6]], *r[6:]) for r in rows)
+    return (muon_adamw_tensor * max(len(rows), 1)).from_buffer_copy(
+        raw or bytes(ctypes.sizeof(muon_adamw_tensor)))
 
 
 def make_pointers(pointers: Sequence) -> ctypes.Array:

@@ -126,36 +126,24 @@ class AdamWPlan(_TensorList):
         lists = (exp_avgs, exp_avg_sqs, grad_dtypes, masters, scales_m, scales_r, wd_muls)
         if any(len(x) != n for x in lists):
             raise ValueError("one state, gradient dtype, master, scale and wd_mul per parameter")
-        state_dtype = torch.float8_e4m3fn if small else torch.float32
-        held, entries = [], []
-        for i in range(n):
-            p, w, m, v, ms, vs = (params[i], masters[i], exp_avgs[i], exp_avg_sqs[i], scales_m[i],
-                                  scales_r[i])
-            mine = [t for t in (p, w, m, v, ms, vs) if t is not None]
-            for t in (p, w, m, v):
-                if t is not None and t.numel() != p.numel():
-                    raise ValueError(f"parameter {i}: tensors of {p.numel()} elements expected")
-            if any(not t.is_contiguous() for t in mine):
-                raise ValueError(f"parameter {i}: contiguous tensors expected")
-            if m.dtype != state_dtype or v.dtype != state_dtype:
-                raise TypeError(f"parameter {i}: states must be {state_dtype} "
-                                f"{'beside' if small else 'without'} scales")
-            if w is not None and w.dtype != torch.float32:
-                raise TypeError(f"parameter {i}: the master copy must be float32")
-            for t in (ms, vs):
-                if t is None:
-                    continue
-                if t.dtype != torch.float8_e8m0fnu:
-                    raise TypeError(f"parameter {i}: scales must be float8_e8m0fnu")
-                if t.numel() != -(-p.numel() // L.MUON_ADAMW_BLOCK):
-                    raise ValueError(f"parameter {i}: one scale per {L.MUON_ADAMW_BLOCK} elements")
-            held += mine
-            ptr = [t.data_ptr() if t is not None else None for t in (p, w, m, v, ms, vs)]
-            entries.append((*ptr, p.numel(), dtype_code(p.dtype), dtype_code(grad_dtypes[i]),
-                            wd_muls[i]))
-        self._set_list(_one_device(held), [p.numel() for p in params], grad_dtypes)
+        tensors = (params, masters, exp_avgs, exp_avg_sqs, scales_m, scales_r)
+        grad_codes = [dtype_code(d) for d in grad_dtypes]
+        codes = [dtype_code(p.dtype) for p in params]
+        self._set_list(params[0].device if n else _one_device(()), [p.numel() for p in params],
+                       grad_dtypes)
+        blocks = [-(-k // L.MUON_ADAMW_BLOCK) for k in self._numels] if small else [0] * n
+        ints = lambda xs: (ctypes.c_int32 * n)(*xs)  # noqa: E731
+        sizes = [self._numels] * 4 + [(ctypes.c_int64 * n)(*blocks)] * 2
+        state = ints([2 if small else 1] * n)
+        dtypes = [ints(codes), ints([1] * n), state, state] + [ints([3] * n)] * 2
+        index = self.device.index if self.device.type == "cuda" else -1
+        at = [L.tensor_addresses(*x, index) for x in zip(tensors, sizes, dtypes)]
+        if any(isinstance(x, int) for x in at):
+            self._refuse_tensors(*tensors, torch.float8_e4m3fn if small else torch.float32)
+        held = [t for ts in tensors for t in ts if t is not None]
         self.state_bits = 8 if small else 32
-        self.handle = L.muon_adamw_plan_create(L.make_adamw_tensors(entries) if n else None, n,
+        packed = L.pack_adamw_tensors((*at, self._numels, codes, grad_codes, wd_muls))
+        self.handle = L.muon_adamw_plan_create(packed if n else None, n,
                                                L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
         self._step = L.address_of(L.lib().muon_adamw_step)
         self._held = held
@@ -168,6 +156,34 @@ class AdamWPlan(_TensorList):
                 self._table = torch.empty(size, dtype=torch.uint8, device=self.device)
                 L.muon_adamw_plan_upload(self.handle, self._table.data_ptr(), size, self._stream())
                 torch.cuda.current_stream(self.device).synchronize()   # steps on any stream
+
+    @staticmethod
+    def _refuse_tensors(params, masters, exp_avgs, exp_avg_sqs, scales_m, scales_r, state_dtype):
+        """Raises for the tensor that does not fit."""
+        every = []
+        for i, (p, w, m, v, ms, vs) in enumerate(zip(params, masters, exp_avgs, exp_avg_sqs,
+                                                     scales_m, scales_r)):
+            mine = [t for t in (p, w, m, v, ms, vs) if t is not None]
+            if not all(isinstance(t, torch.Tensor) for t in mine):
+                raise TypeError(f"parameter {i}: tensors expected")
+            for t in (p, w, m, v):
+                if t is not None and t.numel() != p.numel():
+                    raise ValueError(f"parameter {i}: tensors of {p.numel()} elements expected")
+            if any(not t.is_contiguous() for t in mine):
+                raise ValueError(f"parameter {i}: contiguous tensors expected")
+            if any(t is not None and t.dtype != state_dtype for t in (m, v)):
+                raise TypeError(f"parameter {i}: states must be {state_dtype}: float8_e4m3fn beside "
+                                "scales, float32 without")
+            if w is not None and w.dtype != torch.float32:
+                raise TypeError(f"parameter {i}: the master copy must be float32")
+            for t in (ms, vs):
+                if t is not None and t.dtype != torch.float8_e8m0fnu:
+                    raise TypeError(f"parameter {i}: scales must be float8_e8m0fnu")
+                if t is not None and t.numel() != -(-p.numel() // L.MUON_ADAMW_BLOCK):
+                    raise ValueError(f"parameter {i}: one scale per {L.MUON_ADAMW_BLOCK} elements")
+            every += mine
+        _one_device(every)
+        raise ValueError("a tensor that a plan cannot hold")
 
     def step(self, grads: Sequence[Optional[torch.Tensor]], cfg: L.muon_adamw_config,
              grad_scale: Optional[torch.Tensor] = None,

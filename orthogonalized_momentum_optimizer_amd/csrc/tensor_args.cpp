@@ -16,11 +16,13 @@
 
 namespace {
 
-// muon_dtype of a tensor, -1 if the library has none for it
+// muon_dtype of a tensor, 2 for codes and 3 for scales of 8-bit states, -1 for any other
 int dtype_code(const at::Tensor& t) {
   switch (t.scalar_type()) {
     case at::kBFloat16: return 0;
     case at::kFloat: return 1;
+    case at::kFloat8_e4m3fn: return 2;
+    case at::kFloat8_e8m0fnu: return 3;
     default: return -1;
   }
 }
