@@ -290,8 +290,10 @@ class AdamW(torch.optim.Optimizer):
     were set from outside). ``wd_mul``: multiplier of ``weight_decay``. These and the
     hyper-parameters may differ by group. ``max_grad_norm``: clips the gradients' global norm
     over all groups, inside the step (the gradients themselves stay as they are);
-    ``skip_nonfinite`` then leaves a step out whose norm is not finite (its index still
-    counts). ``last_grad_norm`` is the norm of the last step, on the device."""
+    ``skip_nonfinite`` leaves a step out whose norm is not finite (its index still counts).
+    ``last_grad_norm`` is the norm of the last step that had either, on the device. A step under
+    graph capture replays with the index, and so the bias corrections and the random bits, that
+    it was captured with."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, wd_mul: float = 1.0, state_bits: int = 32,
@@ -323,13 +325,19 @@ class AdamW(torch.optim.Optimizer):
         self.last_grad_norm = None
 
     def load_state_dict(self, state_dict):
-        """As the base class's, except that states keep the dtypes they were saved with."""
+        """As the base class's, except that states keep the dtypes they were saved with. One of
+        ``torch.optim.AdamW`` will do: its moments are the 32-bit states."""
         super().load_state_dict(state_dict)
+        for group in self.param_groups:
+            for k, v in self.defaults.items():
+                group.setdefault(k, v)
         ids = [i for g in state_dict["param_groups"] for i in g["params"]]
         ps = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(ids, ps):
             for k, v in state_dict["state"].get(i, {}).items():
-                if isinstance(v, torch.Tensor):
+                if k == "step":
+                    self.state[p][k] = int(v)
+                elif isinstance(v, torch.Tensor):
                     self.state[p][k] = v.detach().clone().to(p.device)
         self._plans = {}
 
@@ -405,18 +413,19 @@ class AdamW(torch.optim.Optimizer):
             if ps:
                 todo.append((group, *self._plan(gi, group, ps, grads), grads))
         scale = None
-        if self.max_grad_norm is not None and todo:
+        if (self.max_grad_norm is not None or self.skip_nonfinite) and todo:
             every = [g for *_, grads in todo for g in grads]
             plan = self._plans.get("norm")
             if plan is None or not plan.fits(every):
                 plan = self._plans["norm"] = GradNormPlan(every)
-            self.last_grad_norm, scale = plan.norm(every, self.max_grad_norm)
+            self.last_grad_norm, scale = plan.norm(
+                every, math.inf if self.max_grad_norm is None else self.max_grad_norm)
         for group, plan, states, grads in todo:
             at = [st["step"] + 1 for st in states]
             for t in sorted(set(at)):
                 cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],
                                         group["weight_decay"], t,
-                                        self.skip_nonfinite and scale is not None,
+                                        self.skip_nonfinite,
                                         group["stochastic"], group["seed"])
                 mine = grads if len(set(at)) == 1 else [g if k == t else None
                                                         for g, k in zip(grads, at)]

@@ -339,6 +339,42 @@ def test_state_dict_keeps_the_states_dtypes():
     assert opt.state[p[1]]["exp_avg"].dtype == opt.state[p[0]]["master"].dtype == torch.float32
 
 
+def test_state_dict_of_torch_adamw_loads():
+    p = torch.nn.Parameter(torch.randn(7))
+    theirs = torch.optim.AdamW([p], lr=3e-4, weight_decay=0.2)
+    p.grad = torch.randn(7)
+    theirs.step()
+    theirs.step()
+    mine = om.AdamW([p])
+    mine.load_state_dict(theirs.state_dict())
+    g, st = mine.param_groups[0], mine.state[p]
+    assert g["lr"] == 3e-4 and g["weight_decay"] == 0.2 and g["state_bits"] == 32 and g["wd_mul"] == 1.0
+    assert st["step"] == 2 and type(st["step"]) is int
+    assert torch.equal(st["exp_avg"], theirs.state[p]["exp_avg"])
+
+
+def test_optimizer_copies_and_checkpoints():
+    import copy
+    import io
+    p = torch.nn.Parameter(torch.randn(300))
+    opt = om.AdamW([p], state_bits=8, max_grad_norm=2.0, skip_nonfinite=True)
+    opt._init_state(p, opt.param_groups[0])
+    opt.state[p]["exp_avg"].view(torch.uint8).fill_(0x31)
+    other = copy.deepcopy(opt)
+    q = other.param_groups[0]["params"][0]
+    assert other.max_grad_norm == 2.0 and other.skip_nonfinite and other._plans == {}
+    assert other.state[q]["exp_avg"].dtype == torch.float8_e4m3fn
+    other.step()                                  # no gradients: nothing to do
+    file = io.BytesIO()
+    torch.save(opt.state_dict(), file)
+    file.seek(0)
+    other.load_state_dict(torch.load(file, weights_only=True))
+    for k, v in opt.state[p].items():
+        if torch.is_tensor(v):
+            assert other.state[q][k].dtype == v.dtype
+            assert torch.equal(other.state[q][k].view(torch.uint8), v.view(torch.uint8))
+
+
 def test_c_program_uses_the_abi(tmp_path):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")

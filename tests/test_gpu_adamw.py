@@ -610,6 +610,20 @@ def test_skipped_steps_of_the_optimizer():
     assert bool((p.detach() < was).all())
 
 
+def test_skipping_without_clipping():
+    print("[adamw] skip without clipping", flush=True)
+    ps = [torch.nn.Parameter(torch.ones(700, device=dev())) for _ in range(2)]
+    opt = om.AdamW([{"params": ps[:1]}, {"params": ps[1:], "state_bits": 8}], skip_nonfinite=True)
+    for p in ps:
+        p.grad = torch.full((700,), 100.0, device=dev())
+    opt.step()
+    was = [p.detach().clone() for p in ps]
+    assert all(bool((p.detach() < 1).all()) for p in ps)           # a norm over 1 is not clipped
+    ps[1].grad[3] = math.nan                                       # in one group: neither moves
+    opt.step()
+    assert all(torch.equal(p.detach(), w) for p, w in zip(ps, was))
+
+
 def test_clipping_in_front_of_the_other_optimizers():
     """clip_grad_norm_ over all gradients, then Muon for the matrix and CautiousAdam for the
     rest: the same bits as those optimizers given the clipped gradients."""
