@@ -147,6 +147,7 @@ class AdamWPlan(_TensorList):
                                                L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
         self._step = L.address_of(L.lib().muon_adamw_step)
         self._held = held
+        self._table = self._made_on = None
         size = L.muon_adamw_plan_table_size(self.handle)
         if size:
             with self._on(None):
@@ -154,7 +155,8 @@ class AdamWPlan(_TensorList):
                     raise RuntimeError("create the plan before the capture (AdamW: take a step "
                                        "before it)")
                 self._table = torch.empty(size, dtype=torch.uint8, device=self.device)
-                L.muon_adamw_plan_upload(self.handle, self._table.data_ptr(), size, self._stream())
+                self._made_on = self._stream()
+                L.muon_adamw_plan_upload(self.handle, self._table.data_ptr(), size, self._made_on)
                 torch.cuda.current_stream(self.device).synchronize()   # steps on any stream
 
     @staticmethod
@@ -192,8 +194,11 @@ class AdamWPlan(_TensorList):
         float32 on the device that every gradient is multiplied by (``GradNormPlan.norm``'s)."""
         grads = self._list(grads)
         with self._on(stream):
+            on = self._stream()
+            if on != self._made_on and self._table is not None:
+                self._table.record_stream(torch.cuda.current_stream(self.device))
             code = L.args().adamw_step(self._step, self.handle or 0, grads, self._numels, self._dtypes,
-                                       self.device.index, cfg, grad_scale, _SCALE_AT, self._stream())
+                                       self.device.index, cfg, grad_scale, _SCALE_AT, on)
         if code is not None:
             self._refuse(grads, code)
 

@@ -132,7 +132,8 @@ class Set:
         with np.errstate(divide="ignore", invalid="ignore"):
             bound_u = np.abs(m) / (1 - b1 ** t) / den
             low = 1 / np.sqrt(np.maximum(1 - SUB / v, 0)) - 1          # infinite: nothing known
-            du = np.where(v > 0, (4 * E32 * mag_m + SUB) / (1 - b1 ** t) / den
+            low = np.where(v > 0, low, 0)
+            du = np.where(den > 0, (4 * E32 * mag_m + SUB) / (1 - b1 ** t) / den
                           + (16 * E32 + low) * bound_u, 0)
             tol = 2 * E32 * np.abs(p) + cfg.lr * (du + 4 * E32 * abs(lam) * np.abs(p0)) + 1e-30
         if self.w:
@@ -475,6 +476,20 @@ def test_on_another_stream(small):
         again = norms.norm(g, 0.5)
     side.synchronize()
     assert torch.equal(again[0], norm)
+    # a plan that is dropped while its step is still to run on the other stream
+    t = Set([300001], "bf16", "bf16", True, small, seed=2)
+    h, prev = t.grads(), [t.before(0)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(200):
+            norms.norm(g, 0.5)                       # keeps the stream busy
+    t.plan.step(h, cfg, stream=side)
+    t.plan.close()
+    t.plan = None
+    junk = [torch.full((4096,), 255, dtype=torch.uint8, device=dev()) for _ in range(64)]
+    side.synchronize()
+    t.check(0, prev[0], h[0], cfg, label="dropped plan")
+    del junk
 
 
 @pytest.mark.parametrize("small", [False, True], ids=["f32", "8bit"])
