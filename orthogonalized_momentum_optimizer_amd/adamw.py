@@ -75,6 +75,8 @@ class _TensorList:
         if g.numel() != self._numels[code] or not g.is_contiguous() or g.device != self.device:
             raise ValueError(f"gradient {code}: a contiguous tensor of {self._numels[code]} "
                              f"elements on {self.device} expected")
+        if dtype_code(g.dtype) == self._dtypes[code]:
+            raise ValueError(f"gradient {code}: a tensor whose memory holds its values expected")
         raise TypeError(f"gradient {code}: a dtype other than the plan's ({g.dtype})")
 
     def fits(self, grads: Sequence[torch.Tensor]) -> bool:

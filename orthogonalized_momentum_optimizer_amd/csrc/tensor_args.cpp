@@ -27,9 +27,10 @@ int dtype_code(const at::Tensor& t) {
   }
 }
 
+// (A lazily negated view's memory holds other values than the tensor.)
 bool fits(const at::Tensor& t, int64_t numel, int dtype, long device) {
   return t.is_cuda() && t.get_device() == device && t.numel() == numel &&
-         dtype_code(t) == dtype && t.is_contiguous();
+         dtype_code(t) == dtype && t.is_contiguous() && !t.is_neg();
 }
 
 // A held buffer argument.
@@ -72,7 +73,8 @@ struct List {
         const at::Tensor& t = THPVariable_Unpack(list[i]);
         if (!fits(t, numel[i], dtype[i], device)) return i;
         to[i] = reinterpret_cast<uint64_t>(t.const_data_ptr());
-      } catch (...) {                            // a tensor without storage
+        if (!to[i] && numel[i] > 0) return i;    // without storage: not one that is left out
+      } catch (...) {                            // the same
         return i;
       }
     }
@@ -122,11 +124,13 @@ PyObject* adamw_step(PyObject*, PyObject* args) {
     }
     std::memcpy(config, cfg.view.buf, size);
     if (scale != Py_None) {
-      if (!THPVariable_Check(scale) || !fits(THPVariable_Unpack(scale), 1, 1, list.device)) {
+      const void* at = nullptr;
+      if (THPVariable_Check(scale) && fits(THPVariable_Unpack(scale), 1, 1, list.device))
+        at = THPVariable_Unpack(scale).const_data_ptr();
+      if (!at) {
         PyErr_SetString(PyExc_ValueError, "grad_scale must be one float32 on the plan's device");
         return nullptr;
       }
-      const void* const at = THPVariable_Unpack(scale).const_data_ptr();
       std::memcpy(config + offset, &at, sizeof at);
     }
     typedef int (*Step)(const void*, const void*, int64_t, const void*, void*);

@@ -8,6 +8,7 @@ import subprocess
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 import orthogonalized_momentum_optimizer_amd as om
 from orthogonalized_momentum_optimizer_amd import _lib as L
@@ -265,6 +266,25 @@ def test_tensor_addresses_on_the_host():
         L.tensor_addresses([None] * 2, numels, dtypes, 0)
     with pytest.raises(TypeError):
         L.tensor_addresses(7, numels, dtypes, 0)
+
+
+def test_tensors_without_storage():
+    """A tensor of the right device and layout without storage (a subclass that wraps others, a
+    fake tensor) is refused, not taken for a gradient that is left out."""
+    numels, dtypes = (ctypes.c_int64 * 1)(8), (ctypes.c_int32 * 1)(1)
+    class Wrapper(torch.Tensor):
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise AssertionError("no operation is expected")
+
+    make = lambda n: torch.Tensor._make_wrapper_subclass(  # noqa: E731
+        Wrapper, (n,), dtype=torch.float32, device="cuda:0")
+    with FakeTensorMode():
+        fake = torch.empty(8, device="cuda:0")
+    for t in (make(8), fake):
+        assert t.is_cuda and t.is_contiguous()
+        assert L.tensor_addresses([t], numels, dtypes, 0) == 0
+    assert list(L.tensor_addresses([make(0)], (ctypes.c_int64 * 1)(0), dtypes, 0)) == [None]
 
 
 @pytest.mark.parametrize("small,change,error", [

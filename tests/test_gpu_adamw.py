@@ -674,6 +674,8 @@ def test_refusals_with_device_tensors():
         plan.step([p], cfg)                                               # the parameter itself
     with pytest.raises(om.MuonError):
         plan.step([torch.zeros(301, device=dev())[1:]], cfg)              # 4-byte aligned
+    with pytest.raises(ValueError, match="memory"):
+        plan.step([torch._neg_view(ok)], cfg)                             # its memory: other values
     for scale in (torch.ones(2, device=dev()), torch.ones(1), torch.ones(1, device=dev()).half()):
         with pytest.raises(ValueError):
             plan.step([ok], cfg, grad_scale=scale)
