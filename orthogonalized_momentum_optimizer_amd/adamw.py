@@ -154,8 +154,7 @@ class AdamWPlan(_TensorList):
         if size:
             with self._on(None):
                 if torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("create the plan before the capture (AdamW: take a step "
-                                       "before it)")
+                    raise RuntimeError("create the plan before the capture")
                 self._table = torch.empty(size, dtype=torch.uint8, device=self.device)
                 self._made_on = self._stream()
                 L.muon_adamw_plan_upload(self.handle, self._table.data_ptr(), size, self._made_on)
@@ -382,6 +381,11 @@ class AdamW(torch.optim.Optimizer):
                 now = L.tensor_addresses(ps, numels, pdt, plan.device.index)
                 if not isinstance(now, int) and bytes(now) == at:
                     return plan, states
+        if ps[0].is_cuda:
+            with torch.cuda.device(ps[0].device):
+                if torch.cuda.is_current_stream_capturing():   # before a state is made in the graph
+                    raise RuntimeError("AdamW: take a step with these parameters and gradients "
+                                       "before the capture")
         for p, g in zip(ps, grads):
             if not p.is_contiguous() or not g.is_contiguous():
                 raise ValueError("AdamW needs contiguous parameters and gradients")

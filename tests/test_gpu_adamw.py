@@ -609,6 +609,24 @@ def test_optimizer_without_clipping_matches_torch():
     assert float((a - b).detach().abs().max()) <= 10 * 1e-2 * 1e-5 + 20 * E32 * float(b.detach().abs().max())
 
 
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_first_step_under_capture_is_refused(state_bits):
+    """...before a state is made: its zeros would be the graph's work, not done yet."""
+    print(f"[adamw] first step captured, {state_bits} bits", flush=True)
+    p = torch.nn.Parameter(torch.ones(700, device=dev()))
+    p.grad = torch.ones(700, device=dev())
+    opt = om.AdamW([p], state_bits=state_bits, max_grad_norm=1.0)
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            opt.step()
+    assert not opt.state
+    opt.step()
+    other = torch.nn.Parameter(torch.ones(700, device=dev()))
+    other.grad = p.grad
+    om.AdamW([other], state_bits=state_bits, max_grad_norm=1.0).step()
+    assert torch.equal(p.detach(), other.detach()) and bool((p.detach() < 1).all())
+
+
 def test_skipped_steps_of_the_optimizer():
     print("[adamw] optimizer skip", flush=True)
     p = torch.nn.Parameter(torch.ones(1000, device=dev()))
