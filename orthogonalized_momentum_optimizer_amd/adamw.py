@@ -150,6 +150,7 @@ class AdamWPlan(_TensorList):
         self._step = L.address_of(L.lib().muon_adamw_step)
         self._held = held
         self._table = self._made_on = None
+        self.captured = False            # whether a graph may read the table
         size = L.muon_adamw_plan_table_size(self.handle)
         if size:
             with self._on(None):
@@ -198,6 +199,7 @@ class AdamWPlan(_TensorList):
             on = self._stream()
             if on != self._made_on and self._table is not None:
                 self._table.record_stream(torch.cuda.current_stream(self.device))
+            self.captured = self.captured or torch.cuda.is_current_stream_capturing()
             code = L.args().adamw_step(self._step, self.handle or 0, grads, self._numels, self._dtypes,
                                        self.device.index, cfg, grad_scale, _SCALE_AT, on)
         if code is not None:
@@ -309,6 +311,7 @@ class AdamW(torch.optim.Optimizer):
                         wd_mul=wd_mul, state_bits=state_bits, master_weights=master_weights,
                         stochastic=stochastic, seed=seed)
         self._plans = {}
+        self._captured = []              # plans no longer used here that a graph may replay
         self.max_grad_norm = max_grad_norm
         self.skip_nonfinite = skip_nonfinite
         self.last_grad_norm = None
@@ -326,8 +329,11 @@ class AdamW(torch.optim.Optimizer):
         return state
 
     def __setstate__(self, state):
-        super().__setstate__(state)
-        self._plans = {}
+        super().__setstate__(state)                  # load_state_dict calls this as well
+        self.__dict__.setdefault("_plans", {})
+        self.__dict__.setdefault("_captured", [])
+        for gi in list(self._plans):
+            self._drop_plan(gi)
         self.last_grad_norm = None
 
     def load_state_dict(self, state_dict):
@@ -345,7 +351,13 @@ class AdamW(torch.optim.Optimizer):
                     self.state[p][k] = int(v)
                 elif isinstance(v, torch.Tensor):
                     self.state[p][k] = v.detach().clone().to(p.device)
-        self._plans = {}
+
+    def _drop_plan(self, gi):
+        """Forgets a group's plan, unless a graph was captured with it: its table and the states
+        that it was made for then stay allocated as long as the optimizer."""
+        cached = self._plans.pop(gi, None)
+        if gi != "norm" and cached is not None and cached[0].captured:
+            self._captured.append(cached[0])
 
     def _init_state(self, p, group):
         st = self.state[p]
@@ -401,6 +413,7 @@ class AdamW(torch.optim.Optimizer):
                          [s["exp_avg_scale"] for s in states] if small else None,
                          [s["exp_avg_sq_scale"] for s in states] if small else None,
                          [group["wd_mul"]] * len(ps))
+        self._drop_plan(gi)
         n = len(ps)
         numels = (ctypes.c_int64 * n)(*[p.numel() for p in ps])
         pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in ps])

@@ -18,6 +18,7 @@ sqrt(1 + x), x = 3 2^-150 / v, hence u by at most 1 / sqrt(1 - x) - 1 of itself.
 8-bit states are compared byte by byte with the operation-by-operation fp32 evaluation
 (adamw_ref.py), which the CPU tests hold to the float64 definition.
 """
+import copy
 import math
 
 import numpy as np
@@ -625,6 +626,55 @@ def test_first_step_under_capture_is_refused(state_bits):
     other.grad = p.grad
     om.AdamW([other], state_bits=state_bits, max_grad_norm=1.0).step()
     assert torch.equal(p.detach(), other.detach()) and bool((p.detach() < 1).all())
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_graph_outlives_its_plan_in_the_optimizer(state_bits):
+    """A captured step replays after the optimizer has gone over to other gradients, and after a
+    state was loaded: the tables and states that it was captured with are still there."""
+    print(f"[adamw] graph and other gradients, {state_bits} bits", flush=True)
+    r = np.random.default_rng(16)
+    ps = [torch.nn.Parameter(on(r.normal(0, 1, n), torch.float32)) for n in (700, 5000)]
+    gs = [on(r.normal(0, 1, p.numel()), torch.float32) for p in ps]
+    opt = om.AdamW(ps, state_bits=state_bits, max_grad_norm=1.0)
+
+    def step(grads):
+        for p, g in zip(ps, grads):
+            p.grad = g
+        opt.step()
+
+    step(gs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(gs)
+    first = opt._plans[0][0]
+    assert first.captured
+    step([gs[0], None])                                        # another plan
+    assert opt._plans[0][0] is not first and not opt._plans[0][0].captured
+    assert opt._captured == [first] and first.handle and first._table is not None
+    held = [[t.clone() for t in st.values() if torch.is_tensor(t)] for st in opt.state.values()]
+    was = [p.detach().clone() for p in ps]
+    junk = [torch.full((256,), 255, dtype=torch.uint8, device=dev()) for _ in range(64)]
+    results = []
+    for _ in range(3):                                         # from the same start each time
+        with torch.no_grad():
+            for p, w, st, h in zip(ps, was, opt.state.values(), held):
+                p.copy_(w)
+                for t, x in zip([t for t in st.values() if torch.is_tensor(t)], h):
+                    t.view(torch.uint8).copy_(x.view(torch.uint8))
+        graph.replay()
+        torch.cuda.synchronize()
+        results.append([p.detach().clone() for p in ps])
+    for res in results:
+        assert all(torch.equal(a, b) and not torch.equal(a, w)
+                   for a, b, w in zip(res, results[0], was))
+    opt.load_state_dict(opt.state_dict())
+    assert first in opt._captured and not opt._plans
+    graph.replay()                                             # on the states before the load
+    torch.cuda.synchronize()
+    assert all(bool(torch.isfinite(p.detach()).all()) for p in ps)
+    assert copy.deepcopy(opt)._captured == []
+    del junk
 
 
 def test_skipped_steps_of_the_optimizer():
