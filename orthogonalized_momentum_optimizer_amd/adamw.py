@@ -20,6 +20,7 @@ from . import _lib as L
 from .optim import dtype_code
 
 _NOTHING = contextlib.nullcontext()
+_STATES = ("exp_avg", "exp_avg_sq", "master", "exp_avg_scale", "exp_avg_sq_scale")
 _SCALE_AT = L.muon_adamw_config.grad_scale.offset
 # the current stream's handle without a Stream object around it (2 us of a 10 us step)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -311,6 +312,7 @@ class AdamW(torch.optim.Optimizer):
                         wd_mul=wd_mul, state_bits=state_bits, master_weights=master_weights,
                         stochastic=stochastic, seed=seed)
         self._plans = {}
+        self._every = []                 # the parameters' states that the plans were checked with
         self._captured = []              # plans no longer used here that a graph may replay
         self.max_grad_norm = max_grad_norm
         self.skip_nonfinite = skip_nonfinite
@@ -332,6 +334,7 @@ class AdamW(torch.optim.Optimizer):
         super().__setstate__(state)                  # load_state_dict calls this as well
         self.__dict__.setdefault("_plans", {})
         self.__dict__.setdefault("_captured", [])
+        self._every = []
         for gi in list(self._plans):
             self._drop_plan(gi)
         self.last_grad_norm = None
@@ -382,14 +385,25 @@ class AdamW(torch.optim.Optimizer):
             if "master" in st:
                 st["master"].copy_(p)
 
+    def _follow_states(self):
+        """Drops the plans of groups whose states are other dicts by now. Looking a parameter up
+        takes 0.2 us, so that is done only where the dicts of all parameters have changed."""
+        every = self.state.values()
+        if len(every) == len(self._every) and all(map(operator.is_, every, self._every)):
+            return
+        for gi, cached in list(self._plans.items()):
+            if gi != "norm" and not all(self.state.get(p) is st for p, st in zip(cached[1], cached[3])):
+                self._drop_plan(gi)
+        self._every = list(self.state.values())
+
     def _plan(self, gi, group, ps: List[torch.Tensor], grads):
         """The group's plan and the states of ``ps``. A plan is kept while the parameters, their
-        addresses, the gradients' layout and the decay's multiplier stay."""
+        states, both's addresses, the gradients' layout and the decay's multiplier stay."""
         cached = self._plans.get(gi)
         if cached is not None:
-            plan, of, wd_mul, states, numels, pdt, at = cached
+            plan, of, wd_mul, states, numels, pdt, at, states_at = cached
             if (len(of) == len(ps) and all(map(operator.is_, of, ps)) and wd_mul == group["wd_mul"]
-                    and plan.fits(grads)):
+                    and L.args().entries_at(states, _STATES, states_at) and plan.fits(grads)):
                 now = L.tensor_addresses(ps, numels, pdt, plan.device.index)
                 if not isinstance(now, int) and bytes(now) == at:
                     return plan, states
@@ -418,7 +432,9 @@ class AdamW(torch.optim.Optimizer):
         numels = (ctypes.c_int64 * n)(*[p.numel() for p in ps])
         pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in ps])
         at = bytes((ctypes.c_void_p * n)(*[p.data_ptr() for p in ps]))
-        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, at)
+        states_at = (ctypes.c_uint64 * (n * len(_STATES)))(
+            *[st[k].data_ptr() if k in st else 0 for st in states for k in _STATES])
+        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, at, states_at)
         return plan, states
 
     @torch.no_grad()
@@ -427,6 +443,7 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        self._follow_states()
         todo = []
         for gi, group in enumerate(self.param_groups):
             grads = [p.grad for p in group["params"]]

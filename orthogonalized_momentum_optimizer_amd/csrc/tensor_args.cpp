@@ -99,6 +99,37 @@ PyObject* addresses(PyObject*, PyObject* args) {
   return PyLong_FromSsize_t(list.addresses(static_cast<uint64_t*>(out.view.buf)));
 }
 
+// entries_at(dicts, keys, addresses) -> whether the tensors under `keys` (a tuple) in each of a list
+// of dicts are at the addresses, dict by dict; 0: no such entry, or one without memory.
+PyObject* entries_at(PyObject*, PyObject* args) {
+  PyObject *dicts, *keys;
+  Buffer at;
+  if (!PyArg_ParseTuple(args, "O!O!y*", &PyList_Type, &dicts, &PyTuple_Type, &keys, &at.view))
+    return nullptr;
+  const Py_ssize_t n = PyList_GET_SIZE(dicts), k = PyTuple_GET_SIZE(keys);
+  if (at.view.len != n * k * 8) {
+    PyErr_SetString(PyExc_ValueError, "addresses and entries differ in length");
+    return nullptr;
+  }
+  const uint64_t* want = static_cast<const uint64_t*>(at.view.buf);
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* const dict = PyList_GET_ITEM(dicts, i);
+      if (!PyDict_Check(dict)) Py_RETURN_FALSE;
+      for (Py_ssize_t j = 0; j < k; ++j, ++want) {
+        PyObject* const t = PyDict_GetItemWithError(dict, PyTuple_GET_ITEM(keys, j));
+        if (!t && PyErr_Occurred()) return nullptr;
+        const uint64_t is = t && THPVariable_Check(t)
+            ? reinterpret_cast<uint64_t>(THPVariable_Unpack(t).const_data_ptr()) : 0;
+        if (is != *want) Py_RETURN_FALSE;
+      }
+    }
+  } catch (const std::exception&) {              // a tensor without storage
+    Py_RETURN_FALSE;
+  }
+  Py_RETURN_TRUE;
+}
+
 // adamw_step(function, plan, tensors, numels, dtypes, device, cfg, scale, offset, stream) -> None,
 // the index (>= 0) of a gradient that does not fit, or the library's status (< 0). scale: None, or
 // one float32 on the device, whose address goes into the copy of cfg at `offset`.
@@ -195,6 +226,7 @@ PyObject* grad_norm(PyObject*, PyObject* args) {
 
 PyMethodDef methods[] = {
     {"addresses", addresses, METH_VARARGS, "Addresses of the tensors of a plan's layout."},
+    {"entries_at", entries_at, METH_VARARGS, "Whether dicts hold tensors at these addresses."},
     {"adamw_step", adamw_step, METH_VARARGS, "muon_adamw_step over a list of gradients."},
     {"grad_norm", grad_norm, METH_VARARGS, "muon_grad_norm over a list of gradients."},
     {nullptr, nullptr, 0, nullptr}};

@@ -287,6 +287,29 @@ def test_tensors_without_storage():
     assert list(L.tensor_addresses([make(0)], (ctypes.c_int64 * 1)(0), dtypes, 0)) == [None]
 
 
+def test_entries_at():
+    at = L.args().entries_at
+    a, b, c = torch.zeros(4), torch.zeros(2), torch.zeros(0)
+    dicts, keys = [{"x": a, "n": 3}, {"x": b, "y": c}], ("x", "y")
+    want = (ctypes.c_uint64 * 4)(a.data_ptr(), 0, b.data_ptr(), 0)
+    assert at(dicts, keys, want) and at([], keys, (ctypes.c_uint64 * 0)())
+    for i, k, v in ((0, "x", a.clone()), (0, "y", b), (1, "x", a), (1, "x", None), (1, "y", a)):
+        other = [dict(d) for d in dicts]
+        other[i][k] = v
+        assert not at(other, keys, want)
+    assert at([{"x": a, "y": "text"}, {"x": b}], keys, want) and not at([{}, None], keys, want)
+    with FakeTensorMode():
+        fake = torch.empty(8)
+    assert not at([{"x": fake}], ("x",), (ctypes.c_uint64 * 1)(a.data_ptr()))
+    for args in ((dicts, keys, (ctypes.c_uint64 * 3)()), (dicts, keys[:1], want)):
+        with pytest.raises(ValueError):
+            at(*args)
+    with pytest.raises(TypeError):
+        at(tuple(dicts), keys, want)
+    with pytest.raises(TypeError):
+        at([{}], ([],), (ctypes.c_uint64 * 1)())                        # an unhashable key
+
+
 @pytest.mark.parametrize("small,change,error", [
     (False, {}, ValueError),                                            # CPU tensors
     (False, dict(exp_avgs=[]), ValueError),

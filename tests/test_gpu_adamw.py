@@ -677,6 +677,60 @@ def test_graph_outlives_its_plan_in_the_optimizer(state_bits):
     del junk
 
 
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_states_changed_from_outside(state_bits):
+    """A step uses the states that the optimizer holds: after they were replaced by copies, moved
+    to the host and back, or cleared. Against an optimizer whose states changed in place."""
+    print(f"[adamw] states from outside, {state_bits} bits", flush=True)
+    r = np.random.default_rng(17)
+    sizes = (300, 5, 4097)
+    x = [on(r.normal(0, 1, n), torch.bfloat16) for n in sizes]
+    sets = [[torch.nn.Parameter(t.clone()) for t in x] for _ in range(2)]
+    opts = [om.AdamW([{"params": ps[:2]}, {"params": ps[2:], "lr": 1e-2}], state_bits=state_bits,
+                     master_weights=True, weight_decay=0.1) for ps in sets]
+    mine, other = opts
+
+    def step():
+        gs = [on(r.normal(0, 1, n), torch.bfloat16) for n in sizes]
+        for ps, opt in zip(sets, opts):
+            for p, g in zip(ps, gs):
+                p.grad = g.clone()
+            opt.step()
+        torch.cuda.synchronize()
+        for a, b in zip(*sets):
+            assert torch.equal(a.detach(), b.detach())
+            assert mine.state[a].keys() == other.state[b].keys()
+            for k, t in mine.state[a].items():
+                assert (torch.equal(t.view(torch.uint8), other.state[b][k].view(torch.uint8))
+                        if torch.is_tensor(t) else t == other.state[b][k]), k
+
+    step()
+    step()
+    plans = [opt._plans[0][0] for opt in opts]
+    step()
+    assert all(opt._plans[0][0] is plan for opt, plan in zip(opts, plans))     # as long as they fit
+    for st in mine.state.values():                     # the same values in other tensors
+        for k, t in st.items():
+            if torch.is_tensor(t):
+                st[k] = t.cpu().to(dev())
+    step()
+    mine.state[sets[0][2]] = dict(mine.state[sets[0][2]])                      # another dict
+    step()
+    mine.state[sets[0][2]]["exp_avg"] = torch.zeros_like(mine.state[sets[0][2]]["exp_avg"])
+    other.state[sets[1][2]]["exp_avg"].view(torch.uint8).zero_()
+    step()
+    mine.state.clear()                                 # as before the first step
+    for p, st in other.state.items():
+        for k, t in st.items():
+            if torch.is_tensor(t):
+                t.copy_(p.detach()) if k == "master" else t.view(torch.uint8).zero_()
+        st["step"] = 0
+    step()
+    mine.state[sets[0][0]]["exp_avg"] = mine.state[sets[0][0]]["exp_avg"].cpu()
+    with pytest.raises(ValueError):
+        mine.step()
+
+
 def test_skipped_steps_of_the_optimizer():
     print("[adamw] optimizer skip", flush=True)
     p = torch.nn.Parameter(torch.ones(1000, device=dev()))
