@@ -25,6 +25,8 @@ _SCALE_AT = L.muon_adamw_config.grad_scale.offset
 # the current stream's handle without a Stream object around it (2 us of a 10 us step)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or (
+    torch.cuda.is_current_stream_capturing)
 
 
 def make_adamw_config(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
@@ -200,7 +202,7 @@ class AdamWPlan(_TensorList):
             on = self._stream()
             if on != self._made_on and self._table is not None:
                 self._table.record_stream(torch.cuda.current_stream(self.device))
-            self.captured = self.captured or torch.cuda.is_current_stream_capturing()
+            self.captured = self.captured or _capturing()
             code = L.args().adamw_step(self._step, self.handle or 0, grads, self._numels, self._dtypes,
                                        self.device.index, cfg, grad_scale, _SCALE_AT, on)
         if code is not None:

@@ -179,8 +179,12 @@ PyObject* adamw_step(PyObject*, PyObject* args) {
 }
 
 // grad_norm(function, plan, tensors, numels, dtypes, device, max_norm, per_tensor, workspace_bytes,
-// stream) -> (norm, scale) or (norm, scale, norms), or as adamw_step. Results and workspace are one
-// new allocation of the current stream: norm, scale, norms, then 16-byte aligned the workspace.
+// stream) -> (norm, scale) or (norm, scale, norms), or as adamw_step. Results and workspace are new
+// allocations of the current stream: a workspace over kShared bytes one of its own, so that results
+// that a caller keeps, a norm of each step, do not hold it, a smaller one behind the results (16-byte
+// aligned), since the second allocation takes 0.6 us of a call of 10 (122 vectors).
+constexpr Py_ssize_t kShared = 4096;
+
 PyObject* grad_norm(PyObject*, PyObject* args) {
   List list;
   PyObject* tensors;
@@ -198,17 +202,21 @@ PyObject* grad_norm(PyObject*, PyObject* args) {
     const Py_ssize_t bad = list.addresses(grads.data());
     if (bad >= 0) return PyLong_FromSsize_t(bad);
     const int64_t each = per_tensor ? list.n : 0, ws = (2 + each + 3) / 4 * 4;
-    const at::Tensor out = at::empty(
-        {ws + (ws_bytes + 3) / 4},
-        at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, c10::DeviceIndex(list.device)));
+    const int64_t ws_floats = (ws_bytes + 3) / 4;
+    const bool shared = ws_bytes <= kShared;
+    const auto options =
+        at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, c10::DeviceIndex(list.device));
+    const at::Tensor out = at::empty({shared ? ws + ws_floats : 2 + each}, options);
+    const at::Tensor own = shared ? at::Tensor() : at::empty({ws_floats}, options);
     float* const base = static_cast<float*>(out.data_ptr());
+    void* const workspace = shared ? base + ws : own.data_ptr();
     typedef int (*Norm)(const void*, const void*, int64_t, float, float*, float*, void*, size_t,
                         void*);
     int status;
     Py_BEGIN_ALLOW_THREADS
     status = reinterpret_cast<Norm>(function)(
         reinterpret_cast<const void*>(plan), grads.data(), list.n, max_norm, base,
-        each ? base + 2 : nullptr, ws_bytes ? base + ws : nullptr, size_t(ws_bytes),
+        each ? base + 2 : nullptr, workspace, size_t(ws_bytes),
         reinterpret_cast<void*>(stream));
     Py_END_ALLOW_THREADS
     if (status) return PyLong_FromLong(status);

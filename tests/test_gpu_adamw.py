@@ -403,6 +403,16 @@ def test_grad_norm_sizes(dts):
         assert float(norm) == 0.0 and float(scale) == 1.0 and norms.numel() == len(empty)
 
 
+def test_norms_kept_do_not_hold_a_workspace():
+    print("[norm] kept results", flush=True)
+    gs = [torch.ones(1 << 22, device=dev()) for _ in range(16)]
+    plan = om.GradNormPlan(gs)
+    assert plan.ws_bytes > 8192
+    out = plan.norm(gs, 1.0, per_tensor=True)
+    assert all(t.untyped_storage().nbytes() == 4 * (2 + len(gs)) for t in out)
+    assert out[0].item() == 2.0 ** 13 and bool((out[2] == 2.0 ** 11).all())
+
+
 def test_grad_norm_range_and_specials():
     print("[norm] range", flush=True)
     for x in (1e-38, 1e-44, 1e-20, 1e20, 3e38):
