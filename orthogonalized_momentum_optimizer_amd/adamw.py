@@ -343,7 +343,14 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """As the base class's, except that states keep the dtypes they were saved with. One of
-        ``torch.optim.AdamW`` will do: its moments are the 32-bit states."""
+        ``torch.optim.AdamW`` will do: its moments are the 32-bit states. Options of torch's that
+        would step otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam) are refused."""
+        for group in state_dict["param_groups"]:
+            for k in ("amsgrad", "maximize"):
+                if group.get(k):
+                    raise ValueError(f"AdamW has no {k}")
+            if group.get("decoupled_weight_decay") is False and group.get("weight_decay"):
+                raise ValueError("AdamW's weight decay is decoupled")
         super().load_state_dict(state_dict)
         for group in self.param_groups:
             for k, v in self.defaults.items():

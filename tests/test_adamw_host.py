@@ -396,6 +396,19 @@ def test_state_dict_of_torch_adamw_loads():
     assert torch.equal(st["exp_avg"], theirs.state[p]["exp_avg"])
 
 
+@pytest.mark.parametrize("make", [
+    lambda p: torch.optim.AdamW(p, amsgrad=True), lambda p: torch.optim.AdamW(p, maximize=True),
+    lambda p: torch.optim.Adam(p, weight_decay=0.1)], ids=["amsgrad", "maximize", "coupled"])
+def test_state_dict_of_another_step_is_refused(make):
+    p = torch.nn.Parameter(torch.ones(5))
+    opt = om.AdamW([p], lr=0.5)
+    with pytest.raises(ValueError):
+        opt.load_state_dict(make([p]).state_dict())
+    assert opt.param_groups[0]["lr"] == 0.5 and not opt.state
+    opt.load_state_dict(torch.optim.Adam([p], lr=0.25).state_dict())      # nothing decays
+    assert opt.param_groups[0]["lr"] == 0.25
+
+
 def test_optimizer_copies_and_checkpoints():
     import copy
     import io
