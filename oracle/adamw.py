@@ -20,6 +20,7 @@ from .cautious_adam import _f64, adam_direction, adam_moments
 
 BLOCK = 256
 TOP = 256.0 * (1.0 + 0x629146 / 2.0 ** 23)   # a block's largest value, in units of its scale
+ROOT_TOP = 240.0 * 2.0 ** 56                 # the largest r held: the last code whose square fp32 holds
 
 
 def adamw_step(p, g, m, v, t: int, lr: float, beta1: float, beta2: float, eps: float,
@@ -60,9 +61,12 @@ def block_scale(x):
 
 
 def hold(x, up=None, floor=False):
-    """The values x (any shape) is held as: (codes' values, scales), rows of 256."""
+    """The values x (any shape; fp32's finite ones) is held as: (codes' values, scales), rows of
+    256. ``floor``: x is r."""
     b = blocks_of(x)
     s = block_scale(b)
+    if floor:
+        b = np.minimum(b, ROOT_TOP)
     if up is not None:
         up = blocks_of(up)
     y = e4m3(b / s[:, None], up)

@@ -219,6 +219,8 @@ __device__ __forceinline__ float scale_of(int b) {            // 2^(b - 127)
   return __uint_as_float(b == 0 ? 0x00400000u : uint32_t(b) << 23);
 }
 
+constexpr float kRootTop = 240.f * 0x1p56f;
+
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0xEB26D985u;
   x = (x ^ (x >> 15)) * 0x4A08C6EDu;
@@ -401,7 +403,7 @@ __device__ __forceinline__ void step_8bit(const Item& I, const void* grad, const
 #pragma unroll
     for (int e = 0; e < kOwn; ++e) r[e] = sqrtf(r[e]);
 #pragma unroll
-    for (int k = 0; k < BLOCKS; ++k)             // an infinite v is held as the largest finite one
+    for (int k = 0; k < BLOCKS; ++k)             // the scale of an infinite v: the largest finite one's
       rtop[k] = sqrtf(fminf(rtop[k], 3.402823466e38f));
   } else {
 #pragma unroll
@@ -415,7 +417,9 @@ __device__ __forceinline__ void step_8bit(const Item& I, const void* grad, const
     mb[k] = scale_byte(block_max<LANES>(mtop[k]));
     rb[k] = scale_byte(rtop[k]);
     const float rs = scale_of(rb[k]);
-    const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, 0x1.fffffep63f);
+    // up to the largest code whose square is finite: 240 2^56, at the largest scale. (What rounds
+    // to the next one, 2^64, would make v infinite in the next step and from then on.)
+    const float low = rs * 0x1p-9f, high = fminf(rs * 448.f, kRootTop);
 #pragma unroll
     for (int x = k * PER; x < (k + 1) * PER; ++x) {
       const uint32_t i = element(x);

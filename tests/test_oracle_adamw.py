@@ -145,3 +145,17 @@ def test_planted_mistakes_show(mistake):
     assert np.array_equal(oa.hold(m)[0].reshape(-1), adamw_ref.e4m3_values(mc))
     assert not np.array_equal(MISTAKES[mistake](rr, floor=True)[0].reshape(-1),
                               adamw_ref.e4m3_values(rc))
+
+
+def test_square_of_the_largest_held_root_is_finite():
+    """r as the next step squares it: the largest code times the largest scale that fp32's range
+    of v calls for, 2^64, has no fp32 square, and the one below it has."""
+    top = np.sqrt(np.finfo(np.float32).max)              # of a v at fp32's end
+    for x in (top, 250.0 * 2.0 ** 56, 248.0 * 2.0 ** 56, oa.ROOT_TOP):
+        r = np.full(256, 1.0)
+        r[3] = x
+        for up in (None, np.full(256, 1 - 2.0 ** -17)):
+            y, s = oa.hold(r, up, floor=True)
+            assert s[0] == 2.0 ** 56 and y[0, 3] * s[0] == oa.ROOT_TOP
+    with np.errstate(over="ignore"):
+        assert np.isfinite(np.float32(oa.ROOT_TOP) ** 2) and np.isinf(np.float32(2.0 ** 64) ** 2)
