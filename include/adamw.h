@@ -40,8 +40,9 @@
  *
  * NaN and infinities are propagated and never leave their tensor. In the 8-bit form a NaN
  * stays NaN in m and v; an infinite m is held as NaN and takes its block's scale to the
- * largest, so that the block's other m become 0; an r over 240 * 2^56 (a v over 0.88 * 2^128,
- * infinity included) is held as 240 * 2^56, the largest code whose square is finite.
+ * largest, so that the block's other m become 0; a finite |m| over 240 * 2^120 is held as that,
+ * the largest finite code there; an r over 240 * 2^56 (a v over 0.88 * 2^128, infinity
+ * included) is held as 240 * 2^56, the largest code whose square is finite.
  * cfg->skip_nonfinite is the guard against what is not finite. An eps below 2^-126 counts as 0.
  *
  * Conventions are those of muon.h: device buffers on the current HIP device, contiguous, owned

@@ -20,6 +20,7 @@ from .cautious_adam import _f64, adam_direction, adam_moments
 
 BLOCK = 256
 TOP = 256.0 * (1.0 + 0x629146 / 2.0 ** 23)   # a block's largest value, in units of its scale
+MEAN_TOP = 240.0 * 2.0 ** 120                # the largest |m| held: the last code that fp32 holds
 ROOT_TOP = 240.0 * 2.0 ** 56                 # the largest r held: the last code whose square fp32 holds
 
 
@@ -65,8 +66,7 @@ def hold(x, up=None, floor=False):
     256. ``floor``: x is r."""
     b = blocks_of(x)
     s = block_scale(b)
-    if floor:
-        b = np.minimum(b, ROOT_TOP)
+    b = np.minimum(b, ROOT_TOP) if floor else np.clip(b, -MEAN_TOP, MEAN_TOP)
     if up is not None:
         up = blocks_of(up)
     y = e4m3(b / s[:, None], up)

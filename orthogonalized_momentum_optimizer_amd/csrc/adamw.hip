@@ -220,6 +220,8 @@ __device__ __forceinline__ float scale_of(int b) {            // 2^(b - 127)
 }
 
 constexpr float kRootTop = 240.f * 0x1p56f;
+constexpr float kMeanTop = 240.f * 0x1p120f;     // of m: the largest code that is finite there
+constexpr int kMeanTopByte = 120 + 127;          // its scale, the largest there is
 
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0xEB26D985u;
@@ -431,6 +433,11 @@ __device__ __forceinline__ void step_8bit(const Item& I, const void* grad, const
         p[x][e] = updated(S, lam, p[x][e], mx[e], rx[e]);
         // NaN and 0 as they are
         rx[e] = rx[e] > 0.f ? __builtin_amdgcn_fmed3f(rx[e], low, high) : rx[e];
+      }
+      if (mb[k] == kMeanTopByte) {               // rare: 2^128, the next code, would read as infinite
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e)
+          if (fabsf(mx[e]) <= 3.402823466e38f) mx[e] = copysignf(fminf(fabsf(mx[e]), kMeanTop), mx[e]);
       }
       mc[x] = encode<PIECE>(mx, scale_of(mb[k]));
       if (S.stochastic) {

@@ -159,3 +159,15 @@ def test_square_of_the_largest_held_root_is_finite():
             assert s[0] == 2.0 ** 56 and y[0, 3] * s[0] == oa.ROOT_TOP
     with np.errstate(over="ignore"):
         assert np.isfinite(np.float32(oa.ROOT_TOP) ** 2) and np.isinf(np.float32(2.0 ** 64) ** 2)
+
+
+def test_largest_held_mean_is_finite():
+    """Beside a scale of 2^120 the code above 240 stands for 2^128, which fp32 does not hold."""
+    top = float(np.finfo(np.float32).max)
+    x = np.full(256, 1e38)
+    x[:4] = top, -top, 249.0 * 2.0 ** 120, 238.0 * 2.0 ** 120
+    y, s = oa.hold(x)
+    assert s[0] == 2.0 ** 120
+    assert np.array_equal(y[0, :4] * s[0], np.array([1, -1, 1, 1]) * oa.MEAN_TOP)
+    with np.errstate(over="ignore"):
+        assert np.isfinite(np.float32(oa.MEAN_TOP)) and np.isinf(np.float32(2.0 ** 128))
