@@ -41,6 +41,24 @@ def make_adamw_config(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, 
     return cfg
 
 
+_MEAN_TOP, _ROOT_TOP = 240.0 * 2.0 ** 120, 240.0 * 2.0 ** 56   # the largest |m| and r held
+
+
+def _hold(x: torch.Tensor, lost: torch.Tensor, floor: bool = False):
+    """x (fp32, within the range held) as e4m3 codes, rounded to nearest, and the scales of its
+    blocks; NaN where ``lost``. ``floor``: an x over zero does not become zero."""
+    rows = x.new_zeros(-(-x.numel() // L.MUON_ADAMW_BLOCK), L.MUON_ADAMW_BLOCK)
+    rows.view(-1)[:x.numel()] = x.flatten()
+    top = rows.abs().nan_to_num(0.0).amax(1)
+    # top = 2^(E - 127) f has the scale byte E - 8, or E - 7 where f is over 1 + 0x629146 / 2^23
+    byte = (((top.view(torch.int32) + (0x7fffff - 0x629146)) >> 23) - 8).clamp_min(0).int()
+    y = (rows * ((254 - byte) << 23).view(torch.float32)[:, None]).clamp(-448.0, 448.0)
+    if floor:
+        y = torch.where(rows > 0, y.clamp_min(2.0 ** -9), y)
+    y = y.view(-1)[:x.numel()].view(x.shape).masked_fill(lost, math.nan)
+    return y.to(torch.float8_e4m3fn), byte.to(torch.uint8).view(torch.float8_e8m0fnu)
+
+
 def _one_device(tensors: Sequence[torch.Tensor]) -> torch.device:
     for t in tensors:
         if not t.is_cuda:
@@ -343,8 +361,9 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """As the base class's, except that states keep the dtypes they were saved with. One of
-        ``torch.optim.AdamW`` will do: its moments are the 32-bit states. Options of torch's that
-        would step otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam) are refused."""
+        ``torch.optim.AdamW`` will do: its moments, in whatever dtype, become float32, or where the
+        group has ``state_bits`` 8 the nearest 8-bit states. Options of torch's that would step
+        otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam) are refused."""
         for group in state_dict["param_groups"]:
             for k in ("amsgrad", "maximize"):
                 if group.get(k):
@@ -363,6 +382,20 @@ class AdamW(torch.optim.Optimizer):
                     self.state[p][k] = int(v)
                 elif isinstance(v, torch.Tensor):
                     self.state[p][k] = v.detach().clone().to(p.device)
+        for group in self.param_groups:
+            for p in group["params"]:
+                if p in self.state:
+                    self._complete_state(self.state[p], group)
+
+    @staticmethod
+    def _complete_state(st, group):
+        """Brings a loaded state to the form that the group's steps take."""
+        if "exp_avg" in st and "exp_avg_scale" not in st:
+            m, v = (st[k].float().contiguous() for k in ("exp_avg", "exp_avg_sq"))
+            if group["state_bits"] == 8:
+                m, st["exp_avg_scale"] = _hold(m.clamp(-_MEAN_TOP, _MEAN_TOP), m.isinf())
+                v, st["exp_avg_sq_scale"] = _hold(v.sqrt().clamp(max=_ROOT_TOP), v < 0, floor=True)
+            st["exp_avg"], st["exp_avg_sq"] = m, v
 
     def _drop_plan(self, gi):
         """Forgets a group's plan, unless a graph was captured with it: its table and the states

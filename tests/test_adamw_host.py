@@ -443,3 +443,68 @@ def test_c_program_uses_the_abi(tmp_path):
                     f"-Wl,-rpath,{rocm}/lib", "-L", f"{rocm}/lib", "-lamdhip64"], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and "abi ok" in r.stdout, r.stdout + r.stderr
+
+
+def torch_state_dict(ps, steps=2, **kw):
+    """The state dict of a torch.optim.AdamW after steps with random gradients."""
+    theirs = torch.optim.AdamW(ps, **kw)
+    for _ in range(steps):
+        for p in ps:
+            p.grad = torch.randn_like(p)
+        theirs.step()
+    for p in ps:
+        p.grad = None
+    return theirs.state_dict()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32, torch.float64], ids=str)
+def test_moments_of_torch_adamw_become_float32(dt):
+    """torch's moments have the dtype of the parameters that they were saved beside."""
+    p = [torch.nn.Parameter(torch.randn(s).to(dt)) for s in ((300,), (3, 5))]
+    saved = torch_state_dict(p)
+    q = [torch.nn.Parameter(x.detach().to(torch.bfloat16)) for x in p]
+    mine = om.AdamW(q)
+    mine.load_state_dict(saved)
+    for i, x in enumerate(q):
+        st = mine.state[x]
+        assert st["step"] == 2 and "exp_avg_scale" not in st
+        for k in ("exp_avg", "exp_avg_sq"):
+            assert saved["state"][i][k].dtype == dt and st[k].dtype == torch.float32
+            assert st[k].shape == x.shape and torch.equal(st[k], saved["state"][i][k].float())
+
+
+def test_moments_of_torch_adamw_become_8_bit_states():
+    """As adamw.h defines them, by the oracle: m and sqrt(v) to nearest, v = 0 only where it was;
+    and at the ends of fp32's range."""
+    import numpy as np
+    import oracle.adamw as oa
+    r = np.random.default_rng(0)
+    for n in (1, 255, 256, 2500):
+        p = torch.nn.Parameter(torch.zeros(n))
+        saved = torch_state_dict([p])
+        m = torch.tensor(r.normal(0, 1, n) * 10.0 ** r.uniform(-40, 3, n), dtype=torch.float32)
+        v = torch.tensor(10.0 ** r.uniform(-44, 4, n), dtype=torch.float32)
+        if n > 1000:
+            v[1::3] = 0.0
+            top = torch.finfo(torch.float32).max
+            m[300], m[301], v[600], v[1200] = top, -top, top, math.inf
+            m[900], m[1500], v[1600] = math.nan, -math.inf, math.nan
+            m[1800:2050], v[2060:] = 0.0, 0.0                         # whole blocks among them
+            m[2100:2300] = 1e-42
+        saved["state"][0].update(exp_avg=m, exp_avg_sq=v)
+        mine = om.AdamW([p], state_bits=8)
+        saved["param_groups"][0]["state_bits"] = 8
+        mine.load_state_dict(saved)
+        st = mine.state[p]
+        m, v = m.double().numpy(), v.double().numpy()
+        lost_m, lost_v = ~np.isfinite(m), np.isnan(v)
+        m = np.where(np.isinf(m), np.sign(m) * float(torch.finfo(torch.float32).max), np.nan_to_num(m))
+        v = np.nan_to_num(v, posinf=float(torch.finfo(torch.float32).max))
+        root = np.sqrt(v.astype(np.float32)).astype(np.float64)
+        for k, want, lost, floor in (("exp_avg", m, lost_m, False), ("exp_avg_sq", root, lost_v, True)):
+            codes, scales = oa.hold(want, floor=floor)
+            assert st[k].dtype == torch.float8_e4m3fn and st[k].shape == p.shape
+            got = st[k].float().double().numpy()
+            assert np.array_equal(np.isnan(got), lost)
+            assert np.array_equal(got[~lost], codes.reshape(-1)[:n][~lost])
+            assert np.array_equal(st[k + "_scale"].float().double().numpy(), scales)
