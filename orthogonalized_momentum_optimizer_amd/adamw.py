@@ -362,8 +362,10 @@ class AdamW(torch.optim.Optimizer):
     def load_state_dict(self, state_dict):
         """As the base class's, except that states keep the dtypes they were saved with. One of
         ``torch.optim.AdamW`` will do: its moments, in whatever dtype, become float32, or where the
-        group has ``state_bits`` 8 the nearest 8-bit states. Options of torch's that would step
-        otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam) are refused."""
+        group has ``state_bits`` 8 the nearest 8-bit states, and where the group has
+        ``master_weights`` the parameters' present values become the master copies. Options of
+        torch's that would step otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam)
+        are refused."""
         for group in state_dict["param_groups"]:
             for k in ("amsgrad", "maximize"):
                 if group.get(k):
@@ -385,10 +387,10 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             for p in group["params"]:
                 if p in self.state:
-                    self._complete_state(self.state[p], group)
+                    self._complete_state(p, self.state[p], group)
 
     @staticmethod
-    def _complete_state(st, group):
+    def _complete_state(p, st, group):
         """Brings a loaded state to the form that the group's steps take."""
         if "exp_avg" in st and "exp_avg_scale" not in st:
             m, v = (st[k].float().contiguous() for k in ("exp_avg", "exp_avg_sq"))
@@ -396,6 +398,9 @@ class AdamW(torch.optim.Optimizer):
                 m, st["exp_avg_scale"] = _hold(m.clamp(-_MEAN_TOP, _MEAN_TOP), m.isinf())
                 v, st["exp_avg_sq_scale"] = _hold(v.sqrt().clamp(max=_ROOT_TOP), v < 0, floor=True)
             st["exp_avg"], st["exp_avg_sq"] = m, v
+        if ("exp_avg" in st and "master" not in st and group["master_weights"]
+                and p.dtype == torch.bfloat16):
+            st["master"] = p.detach().float()
 
     def _drop_plan(self, gi):
         """Forgets a group's plan, unless a graph was captured with it: its table and the states

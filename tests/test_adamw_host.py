@@ -508,3 +508,23 @@ def test_moments_of_torch_adamw_become_8_bit_states():
             assert np.array_equal(np.isnan(got), lost)
             assert np.array_equal(got[~lost], codes.reshape(-1)[:n][~lost])
             assert np.array_equal(st[k + "_scale"].float().double().numpy(), scales)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_states_of_torch_adamw_get_masters(dt):
+    """Without them the steps would round bf16 parameters each time, whatever the option says."""
+    p = [torch.nn.Parameter(torch.randn(s).to(dt)) for s in (300, 7)]
+    saved = torch_state_dict(p)
+    q = [torch.nn.Parameter(p[0].detach().to(torch.bfloat16)), torch.nn.Parameter(p[1].detach().float())]
+    mine = om.AdamW(q, master_weights=True)
+    mine.load_state_dict(saved)
+    master = mine.state[q[0]]["master"]
+    assert master.dtype == torch.float32 and torch.equal(master, q[0].detach().float())
+    assert "master" not in mine.state[q[1]]                   # an fp32 parameter needs none
+    master.fill_(9.0)                                         # one that was saved is kept
+    other = om.AdamW([torch.nn.Parameter(x.detach().clone()) for x in q], master_weights=True)
+    other.load_state_dict(mine.state_dict())
+    assert bool((other.state[other.param_groups[0]["params"][0]]["master"] == 9.0).all())
+    plain = om.AdamW(q)
+    plain.load_state_dict(saved)
+    assert all("master" not in st for st in plain.state.values())

@@ -75,3 +75,22 @@ def test_steps_from_moments_of_torch_adamw(saved_dt, state_bits):
             assert np.array_equal(v, oa.held(z, w, q.numel()) ** 2)
     for t in (4, 5):
         step_and_compare(opt, qs, r, t)
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+@pytest.mark.parametrize("saved_dt", [torch.bfloat16, torch.float32], ids=str)
+def test_masters_beside_states_of_torch_adamw(saved_dt, state_bits):
+    print(f"[adamw] masters beside states of torch, {saved_dt}, {state_bits} bits", flush=True)
+    r, ps, saved = saved_by_torch(saved_dt, 22)
+    qs = [torch.nn.Parameter(p.detach().to(torch.bfloat16)) for p in ps]
+    opt = om.AdamW(qs, state_bits=state_bits, master_weights=True)
+    saved["param_groups"][0].update(state_bits=state_bits, master_weights=True)
+    opt.load_state_dict(saved)
+    assert all(torch.equal(opt.state[q]["master"], q.detach().float()) for q in qs)
+    for t in (4, 5):
+        step_and_compare(opt, qs, r, t)
+    assert any(not torch.equal(opt.state[q]["master"], q.detach().float()) for q in qs)
+    with torch.no_grad():
+        qs[0].fill_(0.25)
+    opt.refresh_masters()
+    assert bool((opt.state[qs[0]]["master"] == 0.25).all())
