@@ -363,18 +363,19 @@ class AdamW(torch.optim.Optimizer):
         """As the base class's, except that states keep the dtypes they were saved with. One of
         ``torch.optim.AdamW`` will do: its moments, in whatever dtype, become float32, or where the
         group has ``state_bits`` 8 the nearest 8-bit states, and where the group has
-        ``master_weights`` the parameters' present values become the master copies. Options of
-        torch's that would step otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam)
-        are refused."""
+        ``master_weights`` the parameters' present values become the master copies; options that
+        torch's does not have stay as each group has them. Options of torch's that would step
+        otherwise (``amsgrad``, ``maximize``, the coupled decay of Adam) are refused."""
         for group in state_dict["param_groups"]:
             for k in ("amsgrad", "maximize"):
                 if group.get(k):
                     raise ValueError(f"AdamW has no {k}")
             if group.get("decoupled_weight_decay") is False and group.get("weight_decay"):
                 raise ValueError("AdamW's weight decay is decoupled")
+        own = [{k: group.get(k, v) for k, v in self.defaults.items()} for group in self.param_groups]
         super().load_state_dict(state_dict)
-        for group in self.param_groups:
-            for k, v in self.defaults.items():
+        for group, options in zip(self.param_groups, own):
+            for k, v in options.items():
                 group.setdefault(k, v)
         ids = [i for g in state_dict["param_groups"] for i in g["params"]]
         ps = [p for g in self.param_groups for p in g["params"]]

@@ -528,3 +528,28 @@ def test_states_of_torch_adamw_get_masters(dt):
     plain = om.AdamW(q)
     plain.load_state_dict(saved)
     assert all("master" not in st for st in plain.state.values())
+
+
+def test_groups_keep_the_options_that_torch_adamw_has_not():
+    """Saved options are loaded; wd_mul, state_bits and the like stay as each group was built."""
+    p = [torch.nn.Parameter(torch.randn(300)) for _ in range(3)]
+    theirs = torch.optim.AdamW([{"params": p[:1]}, {"params": p[1:], "lr": 5e-4}], lr=2e-4, weight_decay=0.3)
+    for x in p:
+        x.grad = torch.randn_like(x)
+    theirs.step()
+    saved = theirs.state_dict()
+    q = [torch.nn.Parameter(x.detach().to(torch.bfloat16)) for x in p]
+    mine = om.AdamW([{"params": q[:1], "wd_mul": 0.0, "state_bits": 8, "seed": 9, "stochastic": False},
+                     {"params": q[1:], "wd_mul": 2.0, "master_weights": False}],
+                    master_weights=True, seed=4, weight_decay=0.01)
+    mine.load_state_dict(saved)
+    a, b = mine.param_groups
+    own = ("wd_mul", "state_bits", "master_weights", "stochastic", "seed")
+    assert [a[k] for k in own] == [0.0, 8, True, False, 9]
+    assert [b[k] for k in own] == [2.0, 32, False, True, 4]
+    assert (a["lr"], a["weight_decay"], b["lr"], b["weight_decay"]) == (2e-4, 0.3, 5e-4, 0.3)
+    assert mine.state[q[0]]["exp_avg"].dtype == torch.float8_e4m3fn and "master" in mine.state[q[0]]
+    assert mine.state[q[1]]["exp_avg"].dtype == torch.float32 and "master" not in mine.state[q[1]]
+    other = om.AdamW([{"params": q[:1]}, {"params": q[1:]}])        # its own dict brings them all
+    other.load_state_dict(mine.state_dict())
+    assert [[g[k] for k in own] for g in other.param_groups] == [[g[k] for k in own] for g in (a, b)]
