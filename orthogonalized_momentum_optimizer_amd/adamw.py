@@ -411,8 +411,8 @@ class AdamW(torch.optim.Optimizer):
             self._captured.append(cached[0])
 
     def _init_state(self, p, group):
-        st = self.state[p]
-        st["step"] = 0
+        """Makes p's state, or where memory runs out none of it."""
+        st = {"step": 0}
         zeros = lambda shape, dt: torch.zeros(  # noqa: E731
             shape, dtype=torch.uint8 if dt.itemsize == 1 else dt, device=p.device).view(dt)
         if group["state_bits"] == 8:
@@ -425,6 +425,7 @@ class AdamW(torch.optim.Optimizer):
                 st[k] = zeros(p.shape, torch.float32)
         if group["master_weights"] and p.dtype == torch.bfloat16:
             st["master"] = p.detach().float()
+        self.state[p].update(st)
 
     @torch.no_grad()
     def refresh_masters(self):

@@ -553,3 +553,25 @@ def test_groups_keep_the_options_that_torch_adamw_has_not():
     other = om.AdamW([{"params": q[:1]}, {"params": q[1:]}])        # its own dict brings them all
     other.load_state_dict(mine.state_dict())
     assert [[g[k] for k in own] for g in other.param_groups] == [[g[k] for k in own] for g in (a, b)]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_is_made_whole_or_not_at_all(bits, monkeypatch):
+    """Memory that runs out in the middle leaves nothing behind that a later step would take for
+    a state."""
+    p = torch.nn.Parameter(torch.randn(300).to(torch.bfloat16))
+    opt = om.AdamW([p], state_bits=bits, master_weights=True)
+    zeros, calls = torch.zeros, []
+
+    def short(*args, **kw):
+        calls.append(args)
+        if len(calls) == 2:
+            raise torch.OutOfMemoryError("out of memory")
+        return zeros(*args, **kw)
+
+    monkeypatch.setattr(torch, "zeros", short)
+    with pytest.raises(torch.OutOfMemoryError):
+        opt._init_state(p, opt.param_groups[0])
+    assert not opt.state.get(p)
+    opt._init_state(p, opt.param_groups[0])
+    assert opt.state[p]["step"] == 0 and "master" in opt.state[p] and "exp_avg_sq" in opt.state[p]
