@@ -331,6 +331,8 @@ class AdamW(torch.optim.Optimizer):
         defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
                         wd_mul=wd_mul, state_bits=state_bits, master_weights=master_weights,
                         stochastic=stochastic, seed=seed)
+        if max_grad_norm is not None and not max_grad_norm >= 0.0:
+            raise ValueError(f"max_grad_norm must be >= 0, not {max_grad_norm}")
         self._plans = {}
         self._every = []                 # the parameters' states that the plans were checked with
         self._captured = []              # plans no longer used here that a graph may replay
@@ -341,9 +343,27 @@ class AdamW(torch.optim.Optimizer):
 
     def add_param_group(self, param_group):
         super().add_param_group(param_group)
-        if self.param_groups[-1]["state_bits"] not in (8, 32):
+        try:
+            self._check_options(self.param_groups[-1])
+        except ValueError:
             self.param_groups.pop()
+            raise
+
+    @staticmethod
+    def _check_options(group):
+        """What no step would take, as torch.optim.AdamW has it, is refused here already. (Steps
+        take fp32 options: a beta that rounds to 1 is one.)"""
+        fp32 = lambda x: ctypes.c_float(float(x)).value  # noqa: E731
+        if group["state_bits"] not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
+        for k in ("lr", "eps", "weight_decay"):
+            if not 0.0 <= fp32(group[k]) < math.inf:
+                raise ValueError(f"{k} must be finite and >= 0, not {group[k]}")
+        if len(group["betas"]) != 2 or not all(0.0 <= fp32(b) < 1.0 for b in group["betas"]):
+            raise ValueError(f"betas must be two numbers in [0, 1), not {group['betas']}")
+        if not math.isfinite(fp32(group["wd_mul"] * float(group["weight_decay"]))):
+            raise ValueError(f"wd_mul * weight_decay must be finite, not {group['wd_mul']} * "
+                             f"{group['weight_decay']}")
 
     def __getstate__(self):
         state = super().__getstate__()

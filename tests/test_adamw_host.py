@@ -575,3 +575,27 @@ def test_a_state_is_made_whole_or_not_at_all(bits, monkeypatch):
     assert not opt.state.get(p)
     opt._init_state(p, opt.param_groups[0])
     assert opt.state[p]["step"] == 0 and "master" in opt.state[p] and "exp_avg_sq" in opt.state[p]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(lr=-1.0), dict(lr=math.nan), dict(lr=math.inf), dict(betas=(0.9, 1.5)), dict(betas=(-0.1, 0.9)),
+    dict(betas=(0.9, 1 - 1e-9)), dict(betas=(0.9,)), dict(betas=(math.nan, 0.9)), dict(eps=-1.0),
+    dict(eps=math.inf), dict(weight_decay=-0.1), dict(weight_decay=1e39), dict(wd_mul=math.nan),
+    dict(wd_mul=3e38, weight_decay=10.0)], ids=str)
+def test_options_are_checked_where_they_are_given(bad):
+    """...and not by the first step."""
+    p = [torch.nn.Parameter(torch.ones(5)) for _ in range(2)]
+    with pytest.raises(ValueError):
+        om.AdamW(p, **bad)
+    opt = om.AdamW(p[:1])
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": p[1:], **bad})
+    assert len(opt.param_groups) == 1
+    opt.add_param_group({"params": p[1:], "lr": 0.0, "betas": (0.0, 0.0), "eps": 0.0, "weight_decay": 0.0})
+
+
+@pytest.mark.parametrize("bad", [-1.0, math.nan])
+def test_max_grad_norm_is_checked_where_it_is_given(bad):
+    with pytest.raises(ValueError):
+        om.AdamW([torch.nn.Parameter(torch.ones(5))], max_grad_norm=bad)
+    om.AdamW([torch.nn.Parameter(torch.ones(5))], max_grad_norm=0.0)
