@@ -345,7 +345,7 @@ class AdamW(torch.optim.Optimizer):
         super().add_param_group(param_group)
         try:
             self._check_options(self.param_groups[-1])
-        except ValueError:
+        except Exception:
             self.param_groups.pop()
             raise
 
@@ -361,9 +361,10 @@ class AdamW(torch.optim.Optimizer):
                 raise ValueError(f"{k} must be finite and >= 0, not {group[k]}")
         if len(group["betas"]) != 2 or not all(0.0 <= fp32(b) < 1.0 for b in group["betas"]):
             raise ValueError(f"betas must be two numbers in [0, 1), not {group['betas']}")
-        if not math.isfinite(fp32(group["wd_mul"] * float(group["weight_decay"]))):
-            raise ValueError(f"wd_mul * weight_decay must be finite, not {group['wd_mul']} * "
-                             f"{group['weight_decay']}")
+        wd_mul = fp32(group["wd_mul"])
+        if not math.isfinite(wd_mul) or not math.isfinite(fp32(wd_mul * fp32(group["weight_decay"]))):
+            raise ValueError(f"wd_mul and wd_mul * weight_decay must be finite, not {group['wd_mul']} "
+                             f"and {group['weight_decay']}")
 
     def __getstate__(self):
         state = super().__getstate__()

@@ -599,3 +599,13 @@ def test_max_grad_norm_is_checked_where_it_is_given(bad):
     with pytest.raises(ValueError):
         om.AdamW([torch.nn.Parameter(torch.ones(5))], max_grad_norm=bad)
     om.AdamW([torch.nn.Parameter(torch.ones(5))], max_grad_norm=0.0)
+
+
+@pytest.mark.parametrize("bad", [dict(betas=0.9), dict(lr="fast"), dict(wd_mul=1e39, weight_decay=1e-9)], ids=str)
+def test_a_refused_group_is_not_kept(bad):
+    """Also where an option is not a number at all, or fits fp32 only in the product."""
+    p = [torch.nn.Parameter(torch.ones(5)) for _ in range(2)]
+    opt = om.AdamW(p[:1])
+    with pytest.raises((TypeError, ValueError)):
+        opt.add_param_group({"params": p[1:], **bad})
+    assert len(opt.param_groups) == 1
