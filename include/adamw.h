@@ -142,6 +142,11 @@ int muon_adamw_plan_upload(muon_adamw_plan *plan, void *table, size_t table_byte
 int muon_adamw_step(const muon_adamw_plan *plan, const void *const *grads, int64_t n,
                     const muon_adamw_config *cfg, hipStream_t stream);
 
+/* What muon_adamw_step would return of its arguments, without the step: for a caller whose step
+ * is several calls, so that none is made where a later one would be refused. */
+int muon_adamw_check(const muon_adamw_plan *plan, const void *const *grads, int64_t n,
+                     const muon_adamw_config *cfg);
+
 void muon_adamw_plan_destroy(muon_adamw_plan *plan); /* NULL is ignored */
 
 #ifdef __cplusplus

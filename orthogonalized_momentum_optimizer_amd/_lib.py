@@ -36,6 +36,7 @@ EXPORTED = (
     "muon_adam_config_default", "muon_cautious_adam_step", "muon_step_noalloc",
     "muon_plan_set_concurrency", "muon_plan_set_fused",
     "muon_adamw_config_default", "muon_adamw_plan_create", "muon_adamw_step",
+    "muon_adamw_check",
     "muon_adamw_plan_table_size", "muon_adamw_plan_upload",
     "muon_adamw_plan_destroy", "muon_grad_plan_create", "muon_grad_plan_workspace_size",
     "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
@@ -220,6 +221,8 @@ def lib() -> ctypes.CDLL:
     L.muon_adamw_step.argtypes = [vp, ctypes.POINTER(vp), i64,
                                   ctypes.POINTER(muon_adamw_config), vp]
     L.muon_adamw_step.restype = ctypes.c_int
+    L.muon_adamw_check.argtypes = [vp, ctypes.POINTER(vp), i64, ctypes.POINTER(muon_adamw_config)]
+    L.muon_adamw_check.restype = ctypes.c_int
     L.muon_adamw_plan_table_size.argtypes = [vp]
     L.muon_adamw_plan_table_size.restype = sz
     L.muon_adamw_plan_upload.argtypes = [vp, vp, sz, vp]
@@ -411,6 +414,10 @@ def muon_adamw_plan_upload(plan: int, table: int, table_bytes: int, stream: int)
 def muon_adamw_step(plan: int, grads, n: int, cfg: muon_adamw_config, stream: int) -> None:
     """``grads``: a ctypes array of pointers (make_pointers)."""
     _check(lib().muon_adamw_step(plan, grads, n, ctypes.byref(cfg), stream))
+
+
+def muon_adamw_check(plan: int, grads, n: int, cfg: muon_adamw_config) -> None:
+    _check(lib().muon_adamw_check(plan, grads, n, ctypes.byref(cfg)))
 
 
 def muon_adamw_plan_destroy(plan: int) -> None:

@@ -226,6 +226,18 @@ class AdamWPlan(_TensorList):
         if code is not None:
             self._refuse(grads, code)
 
+    def check(self, grads: Sequence[Optional[torch.Tensor]], cfg: L.muon_adamw_config,
+              grad_scale: Optional[torch.Tensor] = None) -> None:
+        """Raises what ``step`` would raise for these arguments; nothing is stepped."""
+        grads = self._list(grads)
+        ptrs = L.tensor_addresses(grads, self._numels, self._dtypes, self.device.index)
+        if isinstance(ptrs, int):
+            self._refuse(grads, ptrs)
+        cfg = type(cfg).from_buffer_copy(cfg)
+        if grad_scale is not None:
+            cfg.grad_scale = grad_scale.data_ptr()
+        L.muon_adamw_check(self.handle, ptrs, len(ptrs), cfg)
+
     def close(self):
         if getattr(self, "handle", None):
             L.muon_adamw_plan_destroy(self.handle)
@@ -531,6 +543,7 @@ class AdamW(torch.optim.Optimizer):
                 plan = self._plans["norm"] = GradNormPlan(every)
             self.last_grad_norm, scale = plan.norm(
                 every, math.inf if self.max_grad_norm is None else self.max_grad_norm)
+        calls = []                       # (plan, gradients, configuration, states)
         for group, plan, states, grads in todo:
             at = [st["step"] + 1 for st in states]
             for t in sorted(set(at)):
@@ -538,9 +551,16 @@ class AdamW(torch.optim.Optimizer):
                                         group["weight_decay"], t,
                                         self.skip_nonfinite,
                                         group["stochastic"], group["seed"])
-                mine = grads if len(set(at)) == 1 else [g if k == t else None
-                                                        for g, k in zip(grads, at)]
-                plan.step(mine, cfg, scale)
-            for st, t in zip(states, at):
-                st["step"] = t
+                if len(set(at)) == 1:
+                    calls.append((plan, grads, cfg, states))
+                else:
+                    calls.append((plan, [g if k == t else None for g, k in zip(grads, at)], cfg,
+                                  [st for st, k in zip(states, at) if k == t]))
+        if len(calls) > 1:               # none is made where a later one would be refused
+            for plan, grads, cfg, _ in calls:
+                plan.check(grads, cfg, scale)
+        for plan, grads, cfg, states in calls:
+            plan.step(grads, cfg, scale)
+            for st in states:
+                st["step"] = cfg.step
         return loss

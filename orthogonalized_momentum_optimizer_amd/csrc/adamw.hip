@@ -616,6 +616,40 @@ class Buffers {
   uintptr_t gap_lo_ = 1, gap_hi_ = 0;
 };
 
+int check_step(const muon_adamw_plan* plan, const void* const* grads, int64_t n,
+               const muon_adamw_config* cfg) {
+  if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+  if (n != (int64_t)plan->tensors.size())
+    return fail(MUON_ERR_INVALID_ARG, "n = %lld but the plan has %zu tensors", (long long)n,
+                plan->tensors.size());
+  if (int st = check_config(cfg)) return st;
+  if (n > 0 && !grads) return fail(MUON_ERR_INVALID_ARG, "grads is NULL");
+  Buffers buffers(plan->ranges);
+  bool any = false;
+  for (int64_t i = 0; i < n; ++i) {
+    const muon_adamw_tensor& T = plan->tensors[i];
+    if (!std::isfinite(cfg->weight_decay * T.wd_mul))
+      return fail(MUON_ERR_INVALID_ARG, "tensor %lld: weight_decay * wd_mul overflows",
+                  (long long)i);
+    if (T.numel == 0 || !grads[i]) continue;
+    any = true;
+    if (!is_aligned16(grads[i]))
+      return fail(MUON_ERR_INVALID_ARG, "gradient %lld must be 16-byte aligned", (long long)i);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
+    if (buffers.meet(lo, lo + (size_t)T.numel * dtype_bytes(T.grad_dtype)))
+      return fail(MUON_ERR_INVALID_ARG, "gradient %lld overlaps a buffer of the plan",
+                  (long long)i);
+  }
+  if (cfg->grad_scale) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
+    if (buffers.meet(lo, lo + sizeof(float)))
+      return fail(MUON_ERR_INVALID_ARG, "grad_scale overlaps a buffer of the plan");
+  }
+  if (any && !plan->table)
+    return fail(MUON_ERR_WORKSPACE, "muon_adamw_plan_upload has not been called on the plan");
+  return MUON_OK;
+}
+
 uint32_t key_of(uint64_t seed, int64_t step) {
   uint64_t z = seed + (uint64_t)step * 0x1493FA689CA113ADull;
   for (int k = 0; k < 2; ++k) z = (z ^ (z >> 32)) * 0xE9F8AC216EBC06F5ull;
@@ -734,35 +768,15 @@ int muon_adamw_plan_upload(muon_adamw_plan* plan, void* table, size_t table_byte
 
 void muon_adamw_plan_destroy(muon_adamw_plan* plan) { delete plan; }
 
+int muon_adamw_check(const muon_adamw_plan* plan, const void* const* grads, int64_t n,
+                     const muon_adamw_config* cfg) {
+  return c_entry([&]() -> int { return check_step(plan, grads, n, cfg); });
+}
+
 int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64_t n,
                     const muon_adamw_config* cfg, hipStream_t stream) {
   return c_entry([&]() -> int {
-    if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
-    if (n != (int64_t)plan->tensors.size())
-      return fail(MUON_ERR_INVALID_ARG, "n = %lld but the plan has %zu tensors", (long long)n,
-                  plan->tensors.size());
-    if (int st = check_config(cfg)) return st;
-    if (n > 0 && !grads) return fail(MUON_ERR_INVALID_ARG, "grads is NULL");
-    Buffers buffers(plan->ranges);
-    for (int64_t i = 0; i < n; ++i) {
-      const muon_adamw_tensor& T = plan->tensors[i];
-      if (!std::isfinite(cfg->weight_decay * T.wd_mul))
-        return fail(MUON_ERR_INVALID_ARG, "tensor %lld: weight_decay * wd_mul overflows",
-                    (long long)i);
-      if (T.numel == 0 || !grads[i]) continue;
-      if (!is_aligned16(grads[i]))
-        return fail(MUON_ERR_INVALID_ARG, "gradient %lld must be 16-byte aligned", (long long)i);
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]);
-      if (buffers.meet(lo, lo + (size_t)T.numel * dtype_bytes(T.grad_dtype)))
-        return fail(MUON_ERR_INVALID_ARG, "gradient %lld overlaps a buffer of the plan",
-                    (long long)i);
-    }
-    if (cfg->grad_scale) {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(cfg->grad_scale);
-      if (buffers.meet(lo, lo + sizeof(float)))
-        return fail(MUON_ERR_INVALID_ARG, "grad_scale overlaps a buffer of the plan");
-    }
-
+    if (int st = check_step(plan, grads, n, cfg)) return st;
     AdamwLaunch L;
     L.s.lr = cfg->lr;
     L.s.beta1 = cfg->beta1;
@@ -784,8 +798,6 @@ int muon_adamw_step(const muon_adamw_plan* plan, const void* const* grads, int64
         any = any || g;
       }
       if (!any) continue;
-      if (!plan->table)
-        return fail(MUON_ERR_WORKSPACE, "muon_adamw_plan_upload has not been called on the plan");
       L.item = plan->table + l.lo;
       L.first = reinterpret_cast<const int*>(plan->table + plan->items.size()) + l.lo;
       L.count = l.count;

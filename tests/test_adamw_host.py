@@ -609,3 +609,25 @@ def test_a_refused_group_is_not_kept(bad):
     with pytest.raises((TypeError, ValueError)):
         opt.add_param_group({"params": p[1:], **bad})
     assert len(opt.param_groups) == 1
+
+
+@no_gpu_only
+def test_check_returns_what_the_step_would():
+    ents = entries()
+    ents[2]["wd"] = 3e38
+    plan = create(ents)
+    cfg, other = L.muon_adamw_config_default(), L.muon_adamw_config_default()
+    other.step = 0
+    free, P = BASE + (64 << 20), L.make_pointers
+    for grads, n, c in ((P([None] * 3), 3, other), (P([None] * 3), 2, cfg), (None, 3, cfg),
+                        (P([free + 2, None, None]), 3, cfg), (P([BASE, None, None]), 3, cfg),
+                        (P([free, None, None]), 3, cfg)):                     # no table yet
+        want = status_of(L.muon_adamw_step, plan, grads, n, c, 0)
+        assert status_of(L.muon_adamw_check, plan, grads, n, c) == want
+    assert status_of(L.muon_adamw_check, None, P([None] * 3), 3, cfg)[0] == INV
+    assert L.lib().muon_adamw_check(plan, P([None] * 3), 3, None) == INV
+    cfg.weight_decay = 10.0
+    assert status_of(L.muon_adamw_check, plan, P([None] * 3), 3, cfg)[0] == INV
+    cfg.weight_decay = 0.0
+    L.muon_adamw_check(plan, P([None] * 3), 3, cfg)
+    L.muon_adamw_plan_destroy(plan)
