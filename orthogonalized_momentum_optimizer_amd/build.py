@@ -2,10 +2,12 @@
 
     python -m orthogonalized_momentum_optimizer_amd.build
 
-(and _tensor_args.so, the binding's check of tensor lists, with the C++ compiler). Every HIP source under csrc/ is compiled with hipcc for gfx950 only and linked into
+Every HIP source under csrc/ is compiled with hipcc for gfx950 only and linked into
 orthogonalized_momentum_optimizer_amd/libmuon.so, except mfma_loop.hip, a measurement kernel
-for bench.py that goes into libmuon_mfma_loop.so. Objects go to _build/ at the repository
-root. The library links against the HIP runtime by its soname, so inside a process that has
+for bench.py that goes into libmuon_mfma_loop.so. _tensor_args.so, the check of tensor lists
+that AdamW and the gradient norm use, is built with the C++ compiler against PyTorch's headers;
+where that fails the other libraries (all that Muon and CautiousAdam need) are there before the
+error is raised. Objects go to _build/ at the repository root. The library links against the HIP runtime by its soname, so inside a process that has
 already loaded PyTorch's HIP runtime the library binds to that same runtime.
 """
 from __future__ import annotations
@@ -96,7 +98,6 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(4, len(SOURCES) + len(PROBE_SOURCES))) as ex:
         args = ex.submit(build_args)
         objs = list(ex.map(one, SOURCES + PROBE_SOURCES))
-        args.result()
     for lib, part in ((LIB, objs[:len(SOURCES)]), (PROBE_LIB, objs[len(SOURCES):])):
         tmp = lib + ".tmp"
         _run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,--no-undefined", "-o", tmp,
@@ -104,6 +105,7 @@ def build(verbose: bool = False) -> str:
         os.replace(tmp, lib)
         if verbose:
             print(f"built {lib}")
+    args.result()                                # raises what build_args raised
     return LIB
 
 
