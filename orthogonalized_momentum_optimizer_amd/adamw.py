@@ -12,7 +12,7 @@ import contextlib
 import ctypes
 import math
 import operator
-from typing import Iterable, List, Optional, Sequence, Union
+from typing import Iterable, Optional, Sequence, Union
 
 import torch
 
@@ -334,7 +334,12 @@ class AdamW(torch.optim.Optimizer):
     ``skip_nonfinite`` leaves a step out whose norm is not finite (its index still counts).
     ``last_grad_norm`` is the norm of the last step that had either, on the device. A step under
     graph capture replays with the index, and so the bias corrections and the random bits, that
-    it was captured with."""
+    it was captured with.
+
+    A parameter without a gradient is left out of a step. A step waits for the current stream only
+    where it meets a parameter's gradient for the first time, or after parameters, states or
+    gradients' dtypes were exchanged from outside (a new plan's table is filled then); such a step
+    cannot be captured. Parameters, states and gradients start at multiples of 16 bytes."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, wd_mul: float = 1.0, state_bits: int = 32,
@@ -478,46 +483,90 @@ class AdamW(torch.optim.Optimizer):
                 self._drop_plan(gi)
         self._every = list(self.state.values())
 
-    def _plan(self, gi, group, ps: List[torch.Tensor], grads):
-        """The group's plan and the states of ``ps``. A plan is kept while the parameters, their
-        states, both's addresses, the gradients' layout and the decay's multiplier stay."""
+    @staticmethod
+    def _in_order(of, ps, grads):
+        """The gradients of the parameters ``of``, a part of ``ps``; None if another one has any."""
+        if len(of) == len(ps) and all(map(operator.is_, of, ps)):
+            return grads
+        mine = []
+        for p, g in zip(ps, grads):
+            if len(mine) < len(of) and of[len(mine)] is p:
+                mine.append(g)
+            elif g is not None:
+                return None
+        return mine if len(mine) == len(of) else None
+
+    def _plan(self, gi, group, grads):
+        """The group's plan, the states of its parameters and their gradients. A plan is kept while
+        its parameters, their states, both's addresses, the gradients' layout and the decay's
+        multiplier stay; gradients may come and go. (Eager steps that leave parameters out go on
+        with another one than a graph's.)"""
+        ps = group["params"]
         cached = self._plans.get(gi)
         if cached is not None:
             plan, of, wd_mul, states, numels, pdt, at, states_at = cached
-            if (len(of) == len(ps) and all(map(operator.is_, of, ps)) and wd_mul == group["wd_mul"]
-                    and L.args().entries_at(states, _STATES, states_at) and plan.fits(grads)):
-                now = L.tensor_addresses(ps, numels, pdt, plan.device.index)
+            mine = self._in_order(of, ps, grads)
+            if (mine is not None and wd_mul == group["wd_mul"]
+                    and L.args().entries_at(states, _STATES, states_at) and plan.fits(mine)
+                    and not (plan.captured and any(g is None for g in mine) and not _capturing())):
+                now = L.tensor_addresses(of, numels, pdt, plan.device.index)
                 if not isinstance(now, int) and bytes(now) == at:
-                    return plan, states
-        if ps[0].is_cuda:
-            with torch.cuda.device(ps[0].device):
+                    return plan, states, mine
+        live = [(p, g) for p, g in zip(ps, grads) if g is not None]
+        device = live[0][0].device
+        if device.type == "cuda":
+            with torch.cuda.device(device):
                 if torch.cuda.is_current_stream_capturing():   # before a state is made in the graph
                     raise RuntimeError("AdamW: take a step with these parameters and gradients "
                                        "before the capture")
-        for p, g in zip(ps, grads):
+        for p, g in live:
             if not p.is_contiguous() or not g.is_contiguous():
                 raise ValueError("AdamW needs contiguous parameters and gradients")
             if "step" not in self.state[p]:
                 self._init_state(p, group)
-        states = [self.state[p] for p in ps]
-        small = "exp_avg_scale" in states[0]
+        small = "exp_avg_scale" in self.state[live[0][0]]
+        absent = self._unmoved(cached, device, small)          # {id: dtype of its last gradient}
+        of, mine, grad_dtypes = [], [], []
+        for p, g in zip(ps, grads):
+            if g is not None or id(p) in absent:
+                of.append(p)
+                mine.append(g)
+                grad_dtypes.append(absent[id(p)] if g is None else g.dtype)
+        states = [self.state[p] for p in of]
         if any(("exp_avg_scale" in st) != small for st in states):
             raise ValueError("a group's states must all have the same state_bits")
-        plan = AdamWPlan([p.detach() for p in ps], [s["exp_avg"] for s in states],
-                         [s["exp_avg_sq"] for s in states], [g.dtype for g in grads],
+        plan = AdamWPlan([p.detach() for p in of], [s["exp_avg"] for s in states],
+                         [s["exp_avg_sq"] for s in states], grad_dtypes,
                          [s.get("master") for s in states],
                          [s["exp_avg_scale"] for s in states] if small else None,
                          [s["exp_avg_sq_scale"] for s in states] if small else None,
-                         [group["wd_mul"]] * len(ps))
+                         [group["wd_mul"]] * len(of))
         self._drop_plan(gi)
-        n = len(ps)
-        numels = (ctypes.c_int64 * n)(*[p.numel() for p in ps])
-        pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in ps])
-        at = bytes((ctypes.c_void_p * n)(*[p.data_ptr() for p in ps]))
+        n = len(of)
+        numels = (ctypes.c_int64 * n)(*[p.numel() for p in of])
+        pdt = (ctypes.c_int32 * n)(*[dtype_code(p.dtype) for p in of])
+        at = bytes((ctypes.c_void_p * n)(*[p.data_ptr() for p in of]))
         states_at = (ctypes.c_uint64 * (n * len(_STATES)))(
             *[st[k].data_ptr() if k in st else 0 for st in states for k in _STATES])
-        self._plans[gi] = (plan, list(ps), group["wd_mul"], states, numels, pdt, at, states_at)
-        return plan, states
+        self._plans[gi] = (plan, of, group["wd_mul"], states, numels, pdt, at, states_at)
+        return plan, states, mine
+
+    def _unmoved(self, cached, device, small):
+        """Those parameters of a plan that are, with their states, where the plan has them, by id:
+        the next plan holds them without a gradient too, so that sets which alternate share one."""
+        if cached is None or cached[0].device != device:
+            return {}
+        plan, of, _, states, numels, pdt, at, states_at = cached
+        dtypes, k, found = (torch.bfloat16, torch.float32), len(_STATES), {}
+        for i, (p, st) in enumerate(zip(of, states)):
+            now = L.tensor_addresses([p], (ctypes.c_int64 * 1)(numels[i]), (ctypes.c_int32 * 1)(pdt[i]),
+                                     device.index)
+            if (not isinstance(now, int) and bytes(now) == at[8 * i:8 * i + 8]
+                    and self.state.get(p) is st and ("exp_avg_scale" in st) == small
+                    and L.args().entries_at([st], _STATES, (ctypes.c_uint64 * k)(
+                        *states_at[k * i:k * i + k]))):
+                found[id(p)] = dtypes[plan._dtypes[i]]
+        return found
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -529,15 +578,11 @@ class AdamW(torch.optim.Optimizer):
         todo = []
         for gi, group in enumerate(self.param_groups):
             grads = [p.grad for p in group["params"]]
-            ps = group["params"]
-            if any(g is None for g in grads):
-                ps = [p for p, g in zip(ps, grads) if g is not None]
-                grads = [g for g in grads if g is not None]
-            if ps:
-                todo.append((group, *self._plan(gi, group, ps, grads), grads))
+            if any(g is not None for g in grads):
+                todo.append((group, *self._plan(gi, group, grads)))
         scale = None
         if (self.max_grad_norm is not None or self.skip_nonfinite) and todo:
-            every = [g for *_, grads in todo for g in grads]
+            every = [g for *_, grads in todo for g in grads if g is not None]
             plan = self._plans.get("norm")
             if plan is None or not plan.fits(every):
                 plan = self._plans["norm"] = GradNormPlan(every)
@@ -545,17 +590,16 @@ class AdamW(torch.optim.Optimizer):
                 every, math.inf if self.max_grad_norm is None else self.max_grad_norm)
         calls = []                       # (plan, gradients, configuration, states)
         for group, plan, states, grads in todo:
-            at = [st["step"] + 1 for st in states]
-            for t in sorted(set(at)):
+            at = [0 if g is None else st["step"] + 1 for st, g in zip(states, grads)]
+            ts = set(at) - {0}
+            for t in sorted(ts):
                 cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],
                                         group["weight_decay"], t,
                                         self.skip_nonfinite,
                                         group["stochastic"], group["seed"])
-                if len(set(at)) == 1:
-                    calls.append((plan, grads, cfg, states))
-                else:
-                    calls.append((plan, [g if k == t else None for g, k in zip(grads, at)], cfg,
-                                  [st for st, k in zip(states, at) if k == t]))
+                calls.append((plan, grads if len(ts) == 1 else [g if k == t else None for g, k in
+                                                                zip(grads, at)], cfg,
+                              [st for st, k in zip(states, at) if k == t]))
         if len(calls) > 1:               # none is made where a later one would be refused
             for plan, grads, cfg, _ in calls:
                 plan.check(grads, cfg, scale)
