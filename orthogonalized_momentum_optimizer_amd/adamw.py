@@ -20,6 +20,7 @@ from . import _lib as L
 from .optim import dtype_code
 
 _NOTHING = contextlib.nullcontext()
+_NONE = type(None)
 _STATES = ("exp_avg", "exp_avg_sq", "master", "exp_avg_scale", "exp_avg_sq_scale")
 _SCALE_AT = L.muon_adamw_config.grad_scale.offset
 # the current stream's handle without a Stream object around it (2 us of a 10 us step)
@@ -169,6 +170,7 @@ class AdamWPlan(_TensorList):
         self.handle = L.muon_adamw_plan_create(packed if n else None, n,
                                                L.MUON_ADAMW_8BIT if small else L.MUON_ADAMW_F32)
         self._step = L.address_of(L.lib().muon_adamw_step)
+        self._check = L.address_of(L.lib().muon_adamw_check)
         self._held = held
         self._table = self._made_on = None
         self.captured = False            # whether a graph may read the table
@@ -230,13 +232,10 @@ class AdamWPlan(_TensorList):
               grad_scale: Optional[torch.Tensor] = None) -> None:
         """Raises what ``step`` would raise for these arguments; nothing is stepped."""
         grads = self._list(grads)
-        ptrs = L.tensor_addresses(grads, self._numels, self._dtypes, self.device.index)
-        if isinstance(ptrs, int):
-            self._refuse(grads, ptrs)
-        cfg = type(cfg).from_buffer_copy(cfg)
-        if grad_scale is not None:
-            cfg.grad_scale = grad_scale.data_ptr()
-        L.muon_adamw_check(self.handle, ptrs, len(ptrs), cfg)
+        code = L.args().adamw_check(self._check, self.handle or 0, grads, self._numels, self._dtypes,
+                                    self.device.index, cfg, grad_scale, _SCALE_AT)
+        if code is not None:
+            self._refuse(grads, code)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -578,33 +577,42 @@ class AdamW(torch.optim.Optimizer):
         todo = []
         for gi, group in enumerate(self.param_groups):
             grads = [p.grad for p in group["params"]]
-            if any(g is not None for g in grads):
-                todo.append((group, *self._plan(gi, group, grads)))
+            absent = list(map(type, grads)).count(_NONE)
+            if absent < len(grads):
+                todo.append((group, *self._plan(gi, group, grads), absent > 0))
         scale = None
         if (self.max_grad_norm is not None or self.skip_nonfinite) and todo:
-            every = [g for *_, grads in todo for g in grads if g is not None]
+            every = [g for *_, grads, absent in todo
+                     for g in (filter(torch.is_tensor, grads) if absent else grads)]
             plan = self._plans.get("norm")
             if plan is None or not plan.fits(every):
                 plan = self._plans["norm"] = GradNormPlan(every)
             self.last_grad_norm, scale = plan.norm(
                 every, math.inf if self.max_grad_norm is None else self.max_grad_norm)
-        calls = []                       # (plan, gradients, configuration, states)
-        for group, plan, states, grads in todo:
-            at = [0 if g is None else st["step"] + 1 for st, g in zip(states, grads)]
+        calls = []                       # (plan, gradients, configuration, states, their index)
+        for group, plan, states, grads, absent in todo:
+            at = ([0 if g is None else st["step"] + 1 for st, g in zip(states, grads)] if absent
+                  else [st["step"] + 1 for st in states])
             ts = set(at) - {0}
             for t in sorted(ts):
                 cfg = make_adamw_config(group["lr"], group["betas"], group["eps"],
                                         group["weight_decay"], t,
                                         self.skip_nonfinite,
                                         group["stochastic"], group["seed"])
-                calls.append((plan, grads if len(ts) == 1 else [g if k == t else None for g, k in
-                                                                zip(grads, at)], cfg,
-                              [st for st, k in zip(states, at) if k == t]))
+                if len(ts) > 1:
+                    mine = [g if k == t else None for g, k in zip(grads, at)]
+                else:
+                    mine = grads
+                if len(ts) > 1 or absent:
+                    states_t = [st for st, k in zip(states, at) if k == t]
+                else:
+                    states_t = states
+                calls.append((plan, mine, cfg, states_t, t))
         if len(calls) > 1:               # none is made where a later one would be refused
-            for plan, grads, cfg, _ in calls:
+            for plan, grads, cfg, *_ in calls:
                 plan.check(grads, cfg, scale)
-        for plan, grads, cfg, states in calls:
+        for plan, grads, cfg, states, t in calls:
             plan.step(grads, cfg, scale)
             for st in states:
-                st["step"] = cfg.step
+                st["step"] = t
         return loss

@@ -130,17 +130,16 @@ PyObject* entries_at(PyObject*, PyObject* args) {
   Py_RETURN_TRUE;
 }
 
-// adamw_step(function, plan, tensors, numels, dtypes, device, cfg, scale, offset, stream) -> None,
-// the index (>= 0) of a gradient that does not fit, or the library's status (< 0). scale: None, or
-// one float32 on the device, whose address goes into the copy of cfg at `offset`.
-PyObject* adamw_step(PyObject*, PyObject* args) {
+// A step's arguments, given to muon_adamw_step, or without a stream to muon_adamw_check.
+PyObject* adamw_call(PyObject* args, bool step) {
   List list;
   Buffer cfg;
   PyObject *tensors, *scale;
-  unsigned long long function, plan, stream;
+  unsigned long long function, plan, stream = 0;
   Py_ssize_t offset;
-  if (!PyArg_ParseTuple(args, "KKOy*y*ly*OnK", &function, &plan, &tensors, &list.numels.view,
-                        &list.dtypes.view, &list.device, &cfg.view, &scale, &offset, &stream) ||
+  if (!PyArg_ParseTuple(args, step ? "KKOy*y*ly*OnK" : "KKOy*y*ly*On", &function, &plan, &tensors,
+                        &list.numels.view, &list.dtypes.view, &list.device, &cfg.view, &scale,
+                        &offset, &stream) ||
       !list.open(tensors))
     return nullptr;
   try {
@@ -165,10 +164,13 @@ PyObject* adamw_step(PyObject*, PyObject* args) {
       std::memcpy(config + offset, &at, sizeof at);
     }
     typedef int (*Step)(const void*, const void*, int64_t, const void*, void*);
+    typedef int (*Check)(const void*, const void*, int64_t, const void*);
+    const void* const p = reinterpret_cast<const void*>(plan);
     int status;
     Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<Step>(function)(reinterpret_cast<const void*>(plan), grads.data(),
-                                              list.n, config, reinterpret_cast<void*>(stream));
+    status = step ? reinterpret_cast<Step>(function)(p, grads.data(), list.n, config,
+                                                     reinterpret_cast<void*>(stream))
+                  : reinterpret_cast<Check>(function)(p, grads.data(), list.n, config);
     Py_END_ALLOW_THREADS
     if (status) return PyLong_FromLong(status);
   } catch (const std::exception& e) {
@@ -177,6 +179,14 @@ PyObject* adamw_step(PyObject*, PyObject* args) {
   }
   Py_RETURN_NONE;
 }
+
+// adamw_step(function, plan, tensors, numels, dtypes, device, cfg, scale, offset, stream) -> None,
+// the index (>= 0) of a gradient that does not fit, or the library's status (< 0). scale: None, or
+// one float32 on the device, whose address goes into the copy of cfg at `offset`.
+PyObject* adamw_step(PyObject*, PyObject* args) { return adamw_call(args, true); }
+
+// adamw_check: the same without `stream`, and without the step.
+PyObject* adamw_check(PyObject*, PyObject* args) { return adamw_call(args, false); }
 
 // grad_norm(function, plan, tensors, numels, dtypes, device, max_norm, per_tensor, workspace_bytes,
 // stream) -> (norm, scale) or (norm, scale, norms), or as adamw_step. Results and workspace are new
@@ -236,6 +246,7 @@ PyMethodDef methods[] = {
     {"addresses", addresses, METH_VARARGS, "Addresses of the tensors of a plan's layout."},
     {"entries_at", entries_at, METH_VARARGS, "Whether dicts hold tensors at these addresses."},
     {"adamw_step", adamw_step, METH_VARARGS, "muon_adamw_step over a list of gradients."},
+    {"adamw_check", adamw_check, METH_VARARGS, "muon_adamw_check over a list of gradients."},
     {"grad_norm", grad_norm, METH_VARARGS, "muon_grad_norm over a list of gradients."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods,
