@@ -128,9 +128,10 @@ class AdamWPlan(_TensorList):
     ``exp_avgs`` and ``exp_avg_sqs``: float32, or all float8_e4m3fn (the 8-bit states, the
     second one holding sqrt(v)) with ``exp_avg_scales`` and ``exp_avg_sq_scales``, one
     float8_e8m0fnu per 256 elements of a tensor. ``grad_dtypes``: of the gradients that steps
-    will receive. ``masters``: per parameter None or, for a bfloat16 one, its
-    float32 master copy. ``wd_muls``: per parameter the multiplier of the weight decay (default 1). All contiguous; all states and
-    scales zero before step 1."""
+    will receive. ``masters``: per parameter None or, for a bfloat16 one, its float32 master
+    copy. ``wd_muls``: per parameter the multiplier of the weight decay (default 1). All
+    contiguous and, scales apart, starting at multiples of 16 bytes; all states and scales zero
+    before step 1. Making a plan waits once for the current stream, which fills its table."""
 
     def __init__(self, params: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
                  exp_avg_sqs: Sequence[torch.Tensor], grad_dtypes: Sequence[torch.dtype],
@@ -301,7 +302,8 @@ class GradNormPlan(_TensorList):
 
 
 def grad_norm(grads: Iterable[torch.Tensor], max_norm: float = math.inf):
-    """(norm, scale) of a list of CUDA gradients (bfloat16 or float32, contiguous)."""
+    """(norm, scale) of a list of CUDA gradients (bfloat16 or float32, contiguous, starting at
+    multiples of 16 bytes)."""
     grads = list(grads)
     return GradNormPlan(grads).norm(grads, max_norm)
 
@@ -310,7 +312,9 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]],
                     max_norm: float) -> torch.Tensor:
     """Scales the gradients of ``parameters`` in place to a global 2-norm of at most
     ``max_norm`` and returns their norm before it (a float32 on the device; nothing
-    synchronises). If the norm is not finite, every gradient becomes NaN."""
+    synchronises). If the norm is not finite, every gradient becomes NaN. Gradients are
+    contiguous, on one device, start at multiples of 16 bytes and do not overlap (a view into a
+    bucket of odd-sized tensors may start elsewhere: MuonError, and no gradient changes)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
@@ -409,7 +413,8 @@ class AdamW(torch.optim.Optimizer):
                     raise ValueError(f"AdamW has no {k}")
             if group.get("decoupled_weight_decay") is False and group.get("weight_decay"):
                 raise ValueError("AdamW's weight decay is decoupled")
-        own = [{k: group.get(k, v) for k, v in self.defaults.items()} for group in self.param_groups]
+        own = [{k: group.get(k, v) for k, v in self.defaults.items()}
+               for group in self.param_groups]
         super().load_state_dict(state_dict)
         for group, options in zip(self.param_groups, own):
             for k, v in options.items():
@@ -478,7 +483,8 @@ class AdamW(torch.optim.Optimizer):
         if len(every) == len(self._every) and all(map(operator.is_, every, self._every)):
             return
         for gi, cached in list(self._plans.items()):
-            if gi != "norm" and not all(self.state.get(p) is st for p, st in zip(cached[1], cached[3])):
+            if gi != "norm" and not all(self.state.get(p) is st
+                                        for p, st in zip(cached[1], cached[3])):
                 self._drop_plan(gi)
         self._every = list(self.state.values())
 
@@ -558,8 +564,8 @@ class AdamW(torch.optim.Optimizer):
         plan, of, _, states, numels, pdt, at, states_at = cached
         dtypes, k, found = (torch.bfloat16, torch.float32), len(_STATES), {}
         for i, (p, st) in enumerate(zip(of, states)):
-            now = L.tensor_addresses([p], (ctypes.c_int64 * 1)(numels[i]), (ctypes.c_int32 * 1)(pdt[i]),
-                                     device.index)
+            now = L.tensor_addresses([p], (ctypes.c_int64 * 1)(numels[i]),
+                                     (ctypes.c_int32 * 1)(pdt[i]), device.index)
             if (not isinstance(now, int) and bytes(now) == at[8 * i:8 * i + 8]
                     and self.state.get(p) is st and ("exp_avg_scale" in st) == small
                     and L.args().entries_at([st], _STATES, (ctypes.c_uint64 * k)(

@@ -7,8 +7,9 @@ orthogonalized_momentum_optimizer_amd/libmuon.so, except mfma_loop.hip, a measur
 for bench.py that goes into libmuon_mfma_loop.so. _tensor_args.so, the check of tensor lists
 that AdamW and the gradient norm use, is built with the C++ compiler against PyTorch's headers;
 where that fails the other libraries (all that Muon and CautiousAdam need) are there before the
-error is raised. Objects go to _build/ at the repository root. The library links against the HIP runtime by its soname, so inside a process that has
-already loaded PyTorch's HIP runtime the library binds to that same runtime.
+error is raised. Objects go to _build/ at the repository root. The library links against the HIP
+runtime by its soname, so inside a process that has already loaded PyTorch's HIP runtime the
+library binds to that same runtime.
 """
 from __future__ import annotations
 
