@@ -435,14 +435,15 @@ class AdamW(torch.optim.Optimizer):
     @staticmethod
     def _complete_state(p, st, group):
         """Brings a loaded state to the form that the group's steps take."""
-        if "exp_avg" in st and "exp_avg_scale" not in st:
+        if "exp_avg" not in st or "exp_avg_sq" not in st:          # another optimizer's
+            return
+        if "exp_avg_scale" not in st:
             m, v = (st[k].float().contiguous() for k in ("exp_avg", "exp_avg_sq"))
             if group["state_bits"] == 8:
                 m, st["exp_avg_scale"] = _hold(m.clamp(-_MEAN_TOP, _MEAN_TOP), m.isinf())
                 v, st["exp_avg_sq_scale"] = _hold(v.sqrt().clamp(max=_ROOT_TOP), v < 0, floor=True)
             st["exp_avg"], st["exp_avg_sq"] = m, v
-        if ("exp_avg" in st and "master" not in st and group["master_weights"]
-                and p.dtype == torch.bfloat16):
+        if "master" not in st and group["master_weights"] and p.dtype == torch.bfloat16:
             st["master"] = p.detach().float()
 
     def _drop_plan(self, gi):

@@ -631,3 +631,15 @@ def test_check_returns_what_the_step_would():
     cfg.weight_decay = 0.0
     L.muon_adamw_check(plan, P([None] * 3), 3, cfg)
     L.muon_adamw_plan_destroy(plan)
+
+
+def test_states_of_another_optimizer_load_as_they_are():
+    """torch's Adamax has a first moment and no second one."""
+    p = torch.nn.Parameter(torch.randn(7))
+    theirs = torch.optim.Adamax([p])
+    p.grad = torch.randn(7)
+    theirs.step()
+    mine = om.AdamW([p], master_weights=True)
+    mine.load_state_dict(theirs.state_dict())
+    assert torch.equal(mine.state[p]["exp_avg"], theirs.state[p]["exp_avg"])
+    assert "exp_avg_sq" not in mine.state[p] and "master" not in mine.state[p]
