@@ -531,9 +531,18 @@ class AdamW(torch.optim.Optimizer):
             if "step" not in self.state[p]:
                 self._init_state(p, group)
         small = "exp_avg_scale" in self.state[live[0][0]]
-        absent = self._unmoved(cached, device, small)          # {id: dtype of its last gradient}
+        absent = self._unmoved(cached, device, small)
+        try:
+            return self._new_plan(gi, group, grads, absent, small)
+        except L.MuonError:
+            if not absent:
+                raise
+        return self._new_plan(gi, group, grads, {}, small)     # one lies where a live one is now
+
+    def _new_plan(self, gi, group, grads, absent, small):
+        """A plan of the parameters with gradients and of ``absent``: {id: gradient's dtype}."""
         of, mine, grad_dtypes = [], [], []
-        for p, g in zip(ps, grads):
+        for p, g in zip(group["params"], grads):
             if g is not None or id(p) in absent:
                 of.append(p)
                 mine.append(g)

@@ -185,3 +185,22 @@ def test_a_step_of_some_gradients_can_be_captured(state_bits):
         a.compare()
         if k % 3 == 2:
             a.step([0, 1, 2, 3])
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_a_parameter_set_into_an_absent_one_steps(state_bits):
+    """The absent one is left out of the plan: no buffer of it stands in the way."""
+    print(f"[adamw] live one in an absent one's memory, {state_bits} bits", flush=True)
+    a = Alternating(state_bits, sizes=(700, 5000, 700))     # (0 and 2 are bf16)
+    a.step([0, 1, 2])
+    for ps in (a.ps, a.qs):
+        ps[2].data = ps[0].data
+    a.step([1, 2])
+    assert len(a.opt._plans[0][1]) == 2
+    plan = a.plan()
+    a.step([2])
+    assert a.plan() is plan
+    for ps in (a.ps, a.qs):
+        ps[2].data = ps[0].detach().clone()
+    a.step([0, 1, 2])
+    assert len(a.opt._plans[0][1]) == 3
