@@ -340,9 +340,10 @@ class AdamW(torch.optim.Optimizer):
     it was captured with.
 
     A parameter without a gradient is left out of a step. A step waits for the current stream only
-    where it meets a parameter's gradient for the first time, or after parameters, states or
-    gradients' dtypes were exchanged from outside (a new plan's table is filled then); such a step
-    cannot be captured. Parameters, states and gradients start at multiples of 16 bytes."""
+    where it meets a parameter's gradient for the first time, or after parameters, states,
+    gradients' dtypes or ``wd_mul`` were exchanged from outside (a new plan's table is filled then);
+    such a step cannot be captured. Parameters, states and gradients start at multiples of 16
+    bytes."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, wd_mul: float = 1.0, state_bits: int = 32,
