@@ -23,6 +23,14 @@ from .adamw import (  # noqa: F401
     grad_norm,
     make_adamw_config,
 )
+from .mx4 import (  # noqa: F401
+    MX4Copies,
+    MX4Tensor,
+    mx4_linear,
+    mx4_matmul,
+    mx4_quantize,
+    mx4_quantize_both,
+)
 from .optim import (  # noqa: F401
     CautiousAdam,
     Muon,

@@ -40,6 +40,8 @@ EXPORTED = (
     "muon_adamw_plan_table_size", "muon_adamw_plan_upload",
     "muon_adamw_plan_destroy", "muon_grad_plan_create", "muon_grad_plan_workspace_size",
     "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
+    "muon_mx_codes_size", "muon_mx_scales_size", "muon_mx_quantize", "muon_mx_dequantize",
+    "muon_mx_matmul_workspace_size", "muon_mx_matmul",
 )
 MUON_MAX_STREAMS = 4
 MUON_ADAMW_F32 = 0
@@ -136,6 +138,20 @@ class muon_adamw_config(ctypes.Structure):
         ("skip_nonfinite", ctypes.c_int),
         ("stochastic", ctypes.c_int),
         ("seed", ctypes.c_uint64),
+    ]
+
+
+class muon_mx_source(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("codes_t", ctypes.c_void_p),
+        ("scales_t", ctypes.c_void_p),
     ]
 
 
@@ -240,6 +256,18 @@ def lib() -> ctypes.CDLL:
     L.muon_grad_scale.restype = ctypes.c_int
     L.muon_grad_plan_destroy.argtypes = [vp]
     L.muon_grad_plan_destroy.restype = None
+    for size in (L.muon_mx_codes_size, L.muon_mx_scales_size):
+        size.argtypes = [i64, i64]
+        size.restype = sz
+    L.muon_mx_quantize.argtypes = [ctypes.POINTER(muon_mx_source), i64, ctypes.c_int,
+                                   ctypes.c_uint64, vp]
+    L.muon_mx_quantize.restype = ctypes.c_int
+    L.muon_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, ctypes.c_int, vp]
+    L.muon_mx_dequantize.restype = ctypes.c_int
+    L.muon_mx_matmul_workspace_size.argtypes = [i64, i64, i64]
+    L.muon_mx_matmul_workspace_size.restype = sz
+    L.muon_mx_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ctypes.c_int, vp, sz, vp]
+    L.muon_mx_matmul.restype = ctypes.c_int
     L.muon_status_string.argtypes = [ctypes.c_int]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_last_error.argtypes = []
@@ -450,3 +478,40 @@ def muon_grad_scale(plan: int, grads, n: int, scale: int, stream: int) -> None:
 
 def muon_grad_plan_destroy(plan: int) -> None:
     lib().muon_grad_plan_destroy(plan)
+
+
+def muon_mx_codes_size(rows: int, cols: int) -> int:
+    return int(lib().muon_mx_codes_size(rows, cols))
+
+
+def muon_mx_scales_size(rows: int, cols: int) -> int:
+    return int(lib().muon_mx_scales_size(rows, cols))
+
+
+def make_mx_sources(entries) -> ctypes.Array:
+    """entries: iterable of (x, rows, cols, row_stride, dtype, codes, scales, codes_t, scales_t)."""
+    entries = list(entries)
+    arr = (muon_mx_source * max(len(entries), 1))()
+    for i, e in enumerate(entries):
+        arr[i] = muon_mx_source(*e)
+    return arr
+
+
+def muon_mx_quantize(sources, n: int, stochastic: int, seed: int, stream: int) -> None:
+    """``sources``: a ctypes array of muon_mx_source (or None when n == 0)."""
+    _check(lib().muon_mx_quantize(sources, n, int(stochastic), seed, stream))
+
+
+def muon_mx_dequantize(codes: int, scales: int, rows: int, cols: int, out: int, dtype: int,
+                       stream: int) -> None:
+    _check(lib().muon_mx_dequantize(codes, scales, rows, cols, out, dtype, stream))
+
+
+def muon_mx_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().muon_mx_matmul_workspace_size(m, n, k))
+
+
+def muon_mx_matmul(a_codes: int, a_scales: int, b_codes: int, b_scales: int, m: int, n: int, k: int,
+                   out: int, dtype: int, workspace, workspace_bytes: int, stream: int) -> None:
+    _check(lib().muon_mx_matmul(a_codes, a_scales, b_codes, b_scales, m, n, k, out, dtype,
+                                workspace, workspace_bytes, stream))

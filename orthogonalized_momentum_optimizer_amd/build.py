@@ -34,7 +34,8 @@ PROBE_SOURCES = ["mfma_loop.hip"]
 
 SOURCES = ["plan.hip", "elementwise.hip", "ns_gemm_bf16.hip", "ns_sym256_bf16.hip",
            "ns_quad_bf16.hip", "ns_apply_bf16.hip", "ns_fused_bf16.hip", "ns_gemm_f32.hip",
-           "cautious_adam.hip", "noalloc.hip", "adamw.hip", "grad_norm.hip"]
+           "cautious_adam.hip", "noalloc.hip", "adamw.hip", "grad_norm.hip", "mx4_quantize.hip",
+           "mx4_matmul.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,410 @@
+// The product of two matrices held in microscaled 4-bit values, out = A B^T (include/mx4.h), on the
+// scaled matrix instructions: kernels and host side.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes 32 rows x 64 values of either operand, one block of 32 values
+// a lane (lane l: row l % 32, block l / 32), and that block's scale byte beside it, so that codes and
+// scales go from memory into the instruction as they are held. Products are exact and sums are
+// fp32. (With data-like operands and nothing else the matrix cores give 6.2 PFLOP/s by these and 3.7
+// by the 16x16x128 form.)
+#include <algorithm>
+#include <vector>
+
+#include "mfma_common.h"
+#include "mx4.h"
+#include "mx4_common.h"
+
+namespace muon {
+namespace {
+
+using mfma::ds_read_b128_at;
+using mfma::f32x16;
+using mfma::static_for;
+using mfma::vm_wait;
+using mfma::xcd_remap;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+struct MmArgs {
+  const uint8_t* a;
+  const uint8_t* sa;
+  const uint8_t* b;
+  const uint8_t* sb;
+  void* out;
+  int64_t split_stride;                          // elements between the parts of a split product
+  int m, n, steps;
+  int panels_a, panels_b;
+  int tiles_m, tiles_n, total;                   // total: tiles times splits
+  int split_steps;                               // steps of a part
+};
+
+template <int OFF>
+__device__ __forceinline__ uint32_t ds_read_b32_at(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "n"(OFF));
+  return r;
+}
+
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+
+// 4 consecutive values of a row of out, from column `col` on; OUT 0: bf16, 1: fp32.
+template <int OUT>
+__device__ __forceinline__ void store4(void* out, int64_t at, int col, int n, f32x4 v) {
+  if (col + 4 <= n) {
+    if (OUT == 0) {
+      typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+      *reinterpret_cast<u32x2_a2*>(static_cast<uint16_t*>(out) + at) =
+          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+      *reinterpret_cast<f32x4_a4*>(static_cast<float*>(out) + at) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) store_one<OUT>(out, at + e, v[e]);
+  }
+}
+
+// ---- tiles -----------------------------------------------------------------------------------
+//
+// Four waves (2 x 2) take a tile of 64 WM x 64 WN, each WM x WN blocks of 32 x 32. A step of 128
+// columns is a stage of a ring of S in LDS: the tile's rows of 64 bytes of codes and 4 bytes of
+// scales, loaded directly (16 rows, a contiguous kilobyte, an instruction). Chunk c of row r lies at
+// c ^ (r / 4 % 4), so that a fragment's 64 lanes read all banks alike. In a stage the two slices of
+// 64 columns are read in turn: while the matrix cores work on the first, the second's fragments
+// arrive; then a barrier for the next stage; while they work on the second, the loads of the stage
+// S ahead go out (into the buffer just read) and the next stage's first fragments arrive.
+template <int WM, int WN, int S, int OUT>
+__device__ __forceinline__ void mx_tile(const MmArgs& g) {
+  constexpr int TM = 64 * WM, TN = 64 * WN;
+  constexpr int PANELS = (TM + TN) / 16, PER = PANELS / 4;             // per stage, per wave
+  constexpr int SLOADS = (TM + TN) / 64, SPER = (SLOADS + 3) / 4;      // of scales
+  constexpr int LOADS = PER + SPER;
+  constexpr int CODES = (TM + TN) * 64, STAGE = CODES + (TM + TN) * 4;
+  __shared__ uint4 smem[S * STAGE / 16];
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+
+  // ---- the tile: an XCD has a contiguous range of them, in strips of four tiles' columns ----
+  const int item = xcd_remap(blockIdx.x, g.total);
+  const int tiles = g.tiles_m * g.tiles_n;
+  const int z = item / tiles, tile = item - z * tiles;
+  const int strip = tile / (4 * g.tiles_m), in = tile - strip * 4 * g.tiles_m;
+  const int width = min(4, g.tiles_n - 4 * strip);
+  const int tm = in / width, tn = 4 * strip + in - tm * width;
+  const int row0 = tm * TM, col0 = tn * TN;
+  const int k0 = z * g.split_steps, KT = min(g.steps - k0, g.split_steps);
+
+  // ---- loads ----
+  const char* src[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int p = wave * PER + i;
+    const bool left = p < TM / 16;
+    const int panel = left ? min(row0 / 16 + p, g.panels_a - 1)
+                           : min(col0 / 16 + p - TM / 16, g.panels_b - 1);
+    src[i] = reinterpret_cast<const char*>(left ? g.a : g.b) +
+             (int64_t(panel) * g.steps + k0) * kMxTileBytes;
+  }
+  const char* ssrc[SPER];
+  int sdst[SPER];
+#pragma unroll
+  for (int i = 0; i < SPER; ++i) {
+    const int q = (wave * SPER + i) % SLOADS;    // (waves beyond the last load some again)
+    const bool left = q < TM / 64;
+    const int p = 4 * (left ? q : q - TM / 64) + lane / 16;
+    const int panel = left ? min(row0 / 16 + p, g.panels_a - 1) : min(col0 / 16 + p, g.panels_b - 1);
+    ssrc[i] = reinterpret_cast<const char*>(left ? g.sa : g.sb) +
+              (int64_t(panel) * g.steps + k0) * kMxTileScales + lane % 16 * 4;
+    sdst[i] = CODES + q * 256;
+  }
+  const uint32_t lane_at = lane / 4 * 64 + ((lane % 4) ^ (lane / 16)) * 16;
+  char* const lds = reinterpret_cast<char*>(smem);
+  auto load = [&](int kt, int buf, int op) {
+    char* const st = lds + buf * STAGE;
+    if (op < PER)
+      __builtin_amdgcn_global_load_lds(src[op] + int64_t(kt) * kMxTileBytes + lane_at,
+                                       MUON_LDS_PTR(st + (wave * PER + op) * 1024), 16, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds(ssrc[op - PER] + int64_t(kt) * kMxTileScales,
+                                       MUON_LDS_PTR(st + sdst[op - PER]), 4, 0, 0);
+  };
+
+  // ---- fragments ----
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(MUON_LDS_PTR(smem)));
+  const int r = lane & 31, h = lane >> 5, sw = (r >> 2) & 3;
+  const uint32_t arow = (wr * 32 * WM + r) * 64, brow = (TM + wc * 32 * WN + r) * 64;
+  const uint32_t ch0 = (h ^ sw) * 16, ch1 = ((2 + h) ^ sw) * 16;
+  const uint32_t asc = CODES + (wr * 32 * WM + r) * 4, bsc = CODES + (TM + wc * 32 * WN + r) * 4;
+  struct Frags {
+    u32x4 a[WM], b[WN];
+  } f0, f1;
+  uint32_t na[WM], nb[WN], sa[WM], sb[WN];       // scales of the next stage and of this one
+  f32x16 acc[WM][WN];
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) acc[i][j] = f32x16{};
+
+  auto read = [&](uint32_t base, uint32_t ch, Frags& f, auto op_t) {
+    constexpr int op = decltype(op_t)::value;
+    if constexpr (op < WM) f.a[op] = ds_read_b128_at<2048 * op>(base + arow + ch);
+    else f.b[op - WM] = ds_read_b128_at<2048 * (op - WM)>(base + brow + ch);
+  };
+  auto read_scale = [&](uint32_t base, auto op_t) {
+    constexpr int op = decltype(op_t)::value;
+    if constexpr (op < WM) na[op] = ds_read_b32_at<128 * op>(base + asc);
+    else nb[op - WM] = ds_read_b32_at<128 * (op - WM)>(base + bsc);
+  };
+  // Waits for every LDS read; the results pass through empty assembly after the wait, so that no use
+  // of them moves above it.
+  auto arrived = [&](Frags& f) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < WM; ++i) asm volatile("" : "+v"(f.a[i]));
+#pragma unroll
+    for (int j = 0; j < WN; ++j) asm volatile("" : "+v"(f.b[j]));
+  };
+  auto scales_arrived = [&]() {                  // byte 2 s of a lane's scales is slice s's
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      asm volatile("" : "+v"(na[i]));
+      sa[i] = na[i] >> (8 * h);
+    }
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      asm volatile("" : "+v"(nb[j]));
+      sb[j] = nb[j] >> (8 * h);
+    }
+  };
+  auto mma = [&](const Frags& f, auto m_t, auto slice_t) {
+    constexpr int m = decltype(m_t)::value, i = m / WN, j = m % WN, op = 2 * decltype(slice_t)::value;
+    const i32x8 x = {int(f.b[j][0]), int(f.b[j][1]), int(f.b[j][2]), int(f.b[j][3]), 0, 0, 0, 0};
+    const i32x8 y = {int(f.a[i][0]), int(f.a[i][1]), int(f.a[i][2]), int(f.a[i][3]), 0, 0, 0, 0};
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc[i][j], 4, 4, op, int(sb[j]),
+                                                               op, int(sa[i]));
+  };
+  // This wave's loads of a stage are there (`later` stages went out after it), then everyone's.
+  auto stage_ready = [&](int later) {
+    static_for<S>([&](auto N) {
+      if (later == decltype(N)::value) vm_wait<decltype(N)::value * LOADS>();
+    });
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  constexpr int READS = WM + WN, MMAS = WM * WN;
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  if (KT > 0) {
+    for (int st = 0; st < min(S, KT); ++st)
+#pragma unroll
+      for (int op = 0; op < LOADS; ++op) load(st, st, op);
+    stage_ready(min(S, KT) - 1);
+    static_for<READS>([&](auto O) { read_scale(lds0, O); });
+    static_for<READS>([&](auto O) { read(lds0, ch0, f0, O); });
+    arrived(f0);
+    scales_arrived();
+  }
+  int buf = 0;
+  for (int kt = 0; kt < KT; ++kt) {
+    const uint32_t cur = lds0 + buf * STAGE;
+    const int nbuf = buf + 1 == S ? 0 : buf + 1;
+    const uint32_t nxt = lds0 + nbuf * STAGE;
+    const bool more = kt + 1 < KT, refill = kt + S < KT;
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<MMAS>([&](auto M) {
+      constexpr int m = decltype(M)::value;
+      mma(f0, M, I0{});
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<READS>([&](auto O) {
+        if constexpr (decltype(O)::value * MMAS / READS == m) read(cur, ch1, f1, O);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    arrived(f1);
+    if (more) stage_ready(min(S - 2, KT - 2 - kt));
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<MMAS>([&](auto M) {
+      constexpr int m = decltype(M)::value;
+      mma(f1, M, I1{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (refill)
+        static_for<LOADS>([&](auto O) {
+          if constexpr (decltype(O)::value * MMAS / LOADS == m) load(kt + S, buf, decltype(O)::value);
+        });
+      if (more)
+        static_for<READS>([&](auto O) {
+          if constexpr (decltype(O)::value * MMAS / READS == m) {
+            read(nxt, ch0, f0, O);
+            read_scale(nxt, O);
+          }
+        });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    arrived(f0);
+    scales_arrived();
+    buf = nbuf;
+  }
+
+  // ---- out: register quad q of lane l is row l % 32, columns 8 q + 4 (l / 32) .. + 3 of a block ----
+  char* const out = static_cast<char*>(g.out) + z * g.split_stride * 4;
+#pragma unroll
+  for (int i = 0; i < WM; ++i) {
+    const int row = row0 + wr * 32 * WM + 32 * i + r;
+    if (row >= g.m) continue;
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = col0 + wc * 32 * WN + 32 * j + 8 * q + 4 * h;
+        store4<OUT>(out, int64_t(row) * g.n + col, col, g.n,
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                          acc[i][j][4 * q + 3]});
+      }
+  }
+}
+
+template <int WM, int WN, int S, int OUT>
+__global__ __launch_bounds__(256, 1) void mx_matmul_kernel(const MmArgs g) {
+  mx_tile<WM, WN, S, OUT>(g);
+}
+
+// The parts of a split product, added in their order.
+template <int OUT>
+__global__ __launch_bounds__(256) void mx_sum_kernel(const float* part, int64_t count, int parts,
+                                                     void* out) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  if (i + 4 <= count) {
+    f32x4 s = *reinterpret_cast<const f32x4_a4*>(part + i);
+    for (int z = 1; z < parts; ++z) s += *reinterpret_cast<const f32x4_a4*>(part + z * count + i);
+    store4<OUT>(out, i, 0, 4, s);
+  } else {
+    for (int64_t e = i; e < count; ++e) {
+      float s = part[e];
+      for (int z = 1; z < parts; ++z) s += part[z * count + e];
+      store_one<OUT>(out, e, s);
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+struct Choice {
+  int wm, wn;                                    // the tile is 64 wm x 64 wn
+  int splits;
+};
+
+constexpr int kCus = 256;
+
+Choice choose(int64_t m, int64_t n, int64_t steps) {
+  Choice c{4, 4, 1};
+  auto tiles = [&](int wm, int wn) {
+    return ((m + 64 * wm - 1) / (64 * wm)) * ((n + 64 * wn - 1) / (64 * wn));
+  };
+  if (tiles(4, 4) < kCus) c.wm = c.wn = 2;
+  const int64_t count = tiles(c.wm, c.wn);
+  if (count < kCus) c.splits = int(std::max<int64_t>(1, std::min<int64_t>(2 * kCus / count, steps / 4)));
+  return c;
+}
+
+bool limits_ok(int64_t m, int64_t n, int64_t k) {
+  return mx_sides_ok(m, k) && mx_sides_ok(n, k) && mx_sides_ok(m, n) &&
+         ((m + 127) / 128) * ((n + 127) / 128) <= (int64_t(1) << 23);
+}
+
+int parts_of(const Choice& c, int64_t steps) {
+  const int64_t each = (steps + c.splits - 1) / c.splits;
+  return steps == 0 ? 1 : int((steps + each - 1) / each);
+}
+
+template <int OUT>
+void launch(const Choice& c, const MmArgs& g, hipStream_t s) {
+  if (c.wm == 4)
+    hipLaunchKernelGGL((mx_matmul_kernel<4, 4, 4, OUT>), dim3((unsigned)g.total), dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((mx_matmul_kernel<2, 2, 4, OUT>), dim3((unsigned)g.total), dim3(256), 0, s, g);
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t muon_mx_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (!limits_ok(m, n, k)) return SIZE_MAX;
+  if (m == 0 || n == 0 || k == 0) return 0;
+  const int parts = parts_of(choose(m, n, mx_steps(k)), mx_steps(k));
+  return parts > 1 ? size_t(parts) * size_t(m) * size_t(n) * 4 : 0;
+}
+
+int muon_mx_matmul(const void* a_codes, const void* a_scales, const void* b_codes,
+                   const void* b_scales, int64_t m, int64_t n, int64_t k, void* out,
+                   muon_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return c_entry([&]() -> int {
+    if (!dtype_known(dtype)) return fail(MUON_ERR_INVALID_ARG, "unknown dtype");
+    if (m < 0 || n < 0 || k < 0) return fail(MUON_ERR_INVALID_ARG, "negative size");
+    if (!limits_ok(m, n, k))
+      return fail(MUON_ERR_UNSUPPORTED, "sides up to 2^31 - 256, 2^40 values a matrix and 2^23 tiles "
+                  "of 128 x 128 in out");
+    if (m == 0 || n == 0) return MUON_OK;
+    if (!out || (reinterpret_cast<uintptr_t>(out) & (dtype_bytes(dtype) - 1)))
+      return fail(MUON_ERR_INVALID_ARG, "out must be non-NULL and aligned to its elements");
+    if (k > 0)
+      for (const void* p : {a_codes, a_scales, b_codes, b_scales})
+        if (!p || !is_aligned16(p))
+          return fail(MUON_ERR_INVALID_ARG, "codes and scales must be non-NULL and 16-byte aligned");
+    const size_t need = muon_mx_matmul_workspace_size(m, n, k);
+    if (need > 0 && (!workspace || !is_aligned16(workspace) || workspace_bytes < need))
+      return fail(MUON_ERR_WORKSPACE, "a workspace of %zu bytes, 16-byte aligned, is needed", need);
+    std::vector<Range> rs = {mx_range(out, size_t(m) * size_t(n) * dtype_bytes(dtype), true),
+                             mx_range(workspace, need, true)};
+    if (k > 0) {
+      rs.push_back(mx_range(a_codes, muon_mx_codes_size(m, k), false));
+      rs.push_back(mx_range(a_scales, muon_mx_scales_size(m, k), false));
+      rs.push_back(mx_range(b_codes, muon_mx_codes_size(n, k), false));
+      rs.push_back(mx_range(b_scales, muon_mx_scales_size(n, k), false));
+    }
+    if (int st = check_overlaps(rs)) return st;
+
+    const int64_t steps = mx_steps(k);
+    const Choice c = choose(m, n, steps);
+    const int parts = parts_of(c, steps);
+    MmArgs g;
+    g.a = static_cast<const uint8_t*>(a_codes);
+    g.sa = static_cast<const uint8_t*>(a_scales);
+    g.b = static_cast<const uint8_t*>(b_codes);
+    g.sb = static_cast<const uint8_t*>(b_scales);
+    g.out = parts > 1 ? workspace : out;
+    g.split_stride = m * n;
+    g.m = (int)m;
+    g.n = (int)n;
+    g.steps = (int)steps;
+    g.panels_a = (int)mx_panels(m);
+    g.panels_b = (int)mx_panels(n);
+    g.tiles_m = (int)((m + 64 * c.wm - 1) / (64 * c.wm));
+    g.tiles_n = (int)((n + 64 * c.wn - 1) / (64 * c.wn));
+    g.total = g.tiles_m * g.tiles_n * parts;
+    g.split_steps = (int)((steps + c.splits - 1) / c.splits);
+    if (parts > 1 || dtype == MUON_DT_F32) launch<1>(c, g, stream);
+    else launch<0>(c, g, stream);
+    if (int st = mx_launched("4-bit product")) return st;
+    if (parts > 1) {
+      const int64_t blocks = (m * n + 1023) / 1024;
+      if (dtype == MUON_DT_F32)
+        hipLaunchKernelGGL(mx_sum_kernel<1>, dim3((unsigned)blocks), dim3(256), 0, stream,
+                           static_cast<const float*>(workspace), m * n, parts, out);
+      else
+        hipLaunchKernelGGL(mx_sum_kernel<0>, dim3((unsigned)blocks), dim3(256), 0, stream,
+                           static_cast<const float*>(workspace), m * n, parts, out);
+      return mx_launched("4-bit product's sum");
+    }
+    return MUON_OK;
+  });
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@
 // come as addresses, so that nothing here binds to it.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -242,7 +243,224 @@ PyObject* grad_norm(PyObject*, PyObject* args) {
   }
 }
 
+// ---- microscaled 4-bit values (include/mx4.h) ----
+
+// muon_mx_source, for calls through an address.
+struct MxSource {
+  const void* x;
+  int64_t rows, cols, row_stride;
+  int dtype;
+  void *codes, *scales, *codes_t, *scales_t;
+};
+
+int64_t mx_codes(int64_t rows, int64_t cols) { return (rows + 15) / 16 * ((cols + 127) / 128) * 1024; }
+
+// Whether t is rows of its last dimension: its leading dimensions collapse into rows of one stride and
+// the last has stride 1, or (transposed) it is 2-D and its transpose is.
+bool rows_of(const at::Tensor& t, MxSource& s, bool& transposed) {
+  const auto size = t.sizes(), stride = t.strides();
+  const int64_t d = t.dim();
+  transposed = false;
+  if (d == 0) return false;
+  s.cols = size[d - 1];
+  s.rows = 1;
+  s.row_stride = s.cols;
+  bool first = true, fits = s.cols <= 1 || stride[d - 1] == 1;
+  for (int64_t i = d - 2; i >= 0; --i) {
+    if (size[i] != 1) {
+      if (first) s.row_stride = stride[i];
+      else fits = fits && stride[i] == s.row_stride * s.rows;
+      first = false;
+    }
+    s.rows *= size[i];
+  }
+  if (t.numel() == 0 || (fits && (s.rows <= 1 || s.row_stride >= s.cols))) return true;
+  if (d != 2 || stride[0] != 1 || stride[1] < size[0]) return false;
+  transposed = true;
+  s.rows = size[1];
+  s.cols = size[0];
+  s.row_stride = stride[1];
+  return true;
+}
+
+// What a native call returns to Python for a refused argument; the text is the error's.
+PyObject* refuse(PyObject* type, const char* text) {
+  PyErr_SetString(type, text);
+  return nullptr;
+}
+
+// mx_quantize(function, tensors, results, stochastic, seed, stream) -> for each tensor (rows, cols,
+// data, data_t), rows x cols the matrix that it is as rows of its last dimension, data and data_t the
+// held form of that and of its transpose, codes and then scales in one uint8 tensor (None where
+// `results`, a bytes of 1: rows, 2: transposed, 3: both for each tensor, does not ask for it); or the
+// library's status.
+PyObject* mx_quantize(PyObject*, PyObject* args) {
+  PyObject* tensors;
+  Buffer results;
+  unsigned long long function, seed, stream;
+  int stochastic;
+  if (!PyArg_ParseTuple(args, "KOy*pKK", &function, &tensors, &results.view, &stochastic, &seed,
+                        &stream))
+    return nullptr;
+  if (!PyTuple_Check(tensors) || PyTuple_GET_SIZE(tensors) != results.view.len)
+    return refuse(PyExc_ValueError, "a tuple of tensors and a result kind for each expected");
+  const Py_ssize_t n = PyTuple_GET_SIZE(tensors);
+  const char* const kinds = static_cast<const char*>(results.view.buf);
+  try {
+    std::vector<MxSource> sources(n);
+    std::vector<at::Tensor> out(2 * n);
+    std::vector<bool> turned(n);
+    c10::OptionalDeviceGuard guard;
+    long device = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* const o = PyTuple_GET_ITEM(tensors, i);
+      if (!THPVariable_Check(o)) return refuse(PyExc_TypeError, "a tensor expected");
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_cuda() || t.layout() != at::kStrided)
+        return refuse(PyExc_ValueError, "a CUDA tensor expected");
+      if (dtype_code(t) != 0 && dtype_code(t) != 1)
+        return refuse(PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32");
+      if (device < 0) {
+        device = t.get_device();
+        guard.reset_device(t.device());
+      }
+      MxSource& s = sources[i];
+      bool transposed = false;
+      if (t.get_device() != device || t.is_neg() || !rows_of(t, s, transposed))
+        return refuse(PyExc_ValueError, t.get_device() != device
+                          ? "all tensors must be on one device"
+                          : "rows of the last dimension expected: a tensor with stride 1 there (or, in "
+                            "two dimensions, along the other) and one stride between rows");
+      s.x = t.numel() ? t.const_data_ptr() : nullptr;
+      if (!s.x && t.numel()) return refuse(PyExc_ValueError, "a tensor with memory expected");
+      s.dtype = dtype_code(t);
+      turned[i] = transposed;
+      s.codes = s.scales = s.codes_t = s.scales_t = nullptr;
+      if (s.rows > (int64_t(1) << 31) || s.cols > (int64_t(1) << 31))
+        return refuse(PyExc_ValueError, "sides up to 2^31 - 256");
+      const auto options = at::TensorOptions().dtype(at::kByte).device(t.device());
+      for (int k = 0; k < 2; ++k) {              // 0: as it is in memory, 1: the transpose of that
+        if (!(kinds[i] & ((k == 1) != transposed ? 2 : 1))) continue;
+        const int64_t codes = k ? mx_codes(s.cols, s.rows) : mx_codes(s.rows, s.cols);
+        at::Tensor& d = out[2 * i + ((k == 1) != transposed ? 1 : 0)];
+        d = at::empty({codes / 16 * 17}, options);
+        char* const p = static_cast<char*>(d.data_ptr());
+        (k ? s.codes_t : s.codes) = p;
+        (k ? s.scales_t : s.scales) = p ? p + codes : nullptr;
+      }
+    }
+    typedef int (*Quantize)(const void*, int64_t, int, uint64_t, void*);
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = reinterpret_cast<Quantize>(function)(sources.data(), n, stochastic, seed,
+                                                  reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    if (status) return PyLong_FromLong(status);
+    PyObject* const result = PyTuple_New(n);
+    if (!result) return nullptr;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const MxSource& s = sources[i];
+      PyObject* const each =
+          Py_BuildValue("LLNN", (long long)(turned[i] ? s.cols : s.rows),
+                        (long long)(turned[i] ? s.rows : s.cols), THPVariable_Wrap(out[2 * i]),
+                        THPVariable_Wrap(out[2 * i + 1]));
+      if (!each) {
+        Py_DECREF(result);
+        return nullptr;
+      }
+      PyTuple_SET_ITEM(result, i, each);
+    }
+    return result;
+  } catch (const std::exception& e) {
+    return refuse(PyExc_RuntimeError, e.what());
+  }
+}
+
+// The held form in `o`: a uint8 tensor of the size that rows x cols take. Null with an error set.
+const char* held(PyObject* o, int64_t rows, int64_t cols, at::Device* device) {
+  if (THPVariable_Check(o)) {
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.is_cuda() && t.scalar_type() == at::kByte && t.is_contiguous() &&
+        t.numel() == mx_codes(rows, cols) / 16 * 17 && (!device->has_index() || t.device() == *device)) {
+      *device = t.device();
+      static const char empty = 0;
+      return t.numel() ? static_cast<const char*>(t.const_data_ptr()) : &empty;
+    }
+  }
+  PyErr_SetString(PyExc_ValueError, "held values of these sizes, on one device, expected");
+  return nullptr;
+}
+
+at::ScalarType out_type(int dtype) { return dtype ? at::kFloat : at::kBFloat16; }
+
+// mx_dequantize(function, data, rows, cols, dtype, stream) -> a rows x cols tensor, or the status.
+PyObject* mx_dequantize(PyObject*, PyObject* args) {
+  PyObject* data;
+  unsigned long long function, stream;
+  long long rows, cols;
+  int dtype;
+  if (!PyArg_ParseTuple(args, "KOLLiK", &function, &data, &rows, &cols, &dtype, &stream))
+    return nullptr;
+  try {
+    at::Device device(at::kCUDA);
+    const char* const p = held(data, rows, cols, &device);
+    if (!p) return nullptr;
+    const c10::DeviceGuard guard(device);
+    const at::Tensor out =
+        at::empty({rows, cols}, at::TensorOptions().dtype(out_type(dtype)).device(device));
+    typedef int (*Back)(const void*, const void*, int64_t, int64_t, void*, int, void*);
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = reinterpret_cast<Back>(function)(p, p + mx_codes(rows, cols), rows, cols,
+                                              out.data_ptr(), dtype,
+                                              reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
+  } catch (const std::exception& e) {
+    return refuse(PyExc_RuntimeError, e.what());
+  }
+}
+
+// mx_matmul(function, workspace_size, a, b, m, n, k, dtype, stream) -> an m x n tensor, or the status.
+PyObject* mx_matmul(PyObject*, PyObject* args) {
+  PyObject *a, *b;
+  unsigned long long function, size, stream;
+  long long m, n, k;
+  int dtype;
+  if (!PyArg_ParseTuple(args, "KKOOLLLiK", &function, &size, &a, &b, &m, &n, &k, &dtype, &stream))
+    return nullptr;
+  try {
+    at::Device device(at::kCUDA);
+    const char* const p = held(a, m, k, &device);
+    const char* const q = p ? held(b, n, k, &device) : nullptr;
+    if (!q) return nullptr;
+    const c10::DeviceGuard guard(device);
+    const at::Tensor out =
+        at::empty({m, n}, at::TensorOptions().dtype(out_type(dtype)).device(device));
+    typedef size_t (*Size)(int64_t, int64_t, int64_t);
+    const size_t need = reinterpret_cast<Size>(size)(m, n, k);
+    at::Tensor ws;
+    if (need && need != SIZE_MAX)
+      ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(device));
+    typedef int (*Product)(const void*, const void*, const void*, const void*, int64_t, int64_t,
+                           int64_t, void*, int, void*, size_t, void*);
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = reinterpret_cast<Product>(function)(
+        p, p + mx_codes(m, k), q, q + mx_codes(n, k), m, n, k, out.data_ptr(), dtype,
+        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? need : 0,
+        reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
+  } catch (const std::exception& e) {
+    return refuse(PyExc_RuntimeError, e.what());
+  }
+}
+
 PyMethodDef methods[] = {
+    {"mx_quantize", mx_quantize, METH_VARARGS, "muon_mx_quantize of tensors into new ones."},
+    {"mx_dequantize", mx_dequantize, METH_VARARGS, "muon_mx_dequantize into a new tensor."},
+    {"mx_matmul", mx_matmul, METH_VARARGS, "muon_mx_matmul into a new tensor."},
     {"addresses", addresses, METH_VARARGS, "Addresses of the tensors of a plan's layout."},
     {"entries_at", entries_at, METH_VARARGS, "Whether dicts hold tensors at these addresses."},
     {"adamw_step", adamw_step, METH_VARARGS, "muon_adamw_step over a list of gradients."},
