@@ -209,17 +209,20 @@ class Muon(torch.optim.Optimizer):
     its last two dimensions. 1-D parameters are rejected (they belong to another optimizer).
     ``row_equalize`` adds the per-row energy equaliser of the NorMuon family between the
     orthogonalisation and the update (state: one float per row of every matrix).
+    ``mx4_copies``: the ``MX4Copies`` of a model's weights, refreshed at the end of every step, for
+    layers that multiply in microscaled 4-bit values (``mx4_linear``).
     """
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
                  ns_steps: int = 5, precision: str = "bf16", row_equalize: bool = False,
-                 row_beta: float = 0.95, row_eps: float = 1e-8):
+                 row_beta: float = 0.95, row_eps: float = 1e-8, mx4_copies=None):
         defaults = dict(lr=lr, momentum=momentum, nesterov=nesterov, ns_steps=ns_steps,
                         row_equalize=row_equalize, row_beta=row_beta, row_eps=row_eps)
         super().__init__(params, defaults)
         if precision not in _PREC:
             raise ValueError(f"precision must be one of {sorted(_PREC)}")
         self.precision = precision
+        self.mx4_copies = mx4_copies
         for group in self.param_groups:
             for p in group["params"]:
                 if p.dim() < 2:
@@ -272,6 +275,8 @@ class Muon(torch.optim.Optimizer):
                               row_equalize=group["row_equalize"], row_beta=group["row_beta"],
                               row_eps=group["row_eps"])
             plan.step(params, grads, moms, cfg, row_vars=rvars if group["row_equalize"] else None)
+        if self.mx4_copies is not None:
+            self.mx4_copies.refresh()
         return loss
 
 
