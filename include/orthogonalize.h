@@ -1,0 +1,56 @@
+/*
+ * orthogonalize.h - C ABI of the Newton-Schulz orthogonalisation of a stack of small matrices
+ * (attention heads, low-rank factors: the shorter side up to 128), strided as they lie in a
+ * larger tensor, in one set of launches.
+ *
+ * What it computes for every matrix X of the stack (short side s, long side l, X taken with the
+ * short side as its rows): X_0 = X / (||X||_F + eps), then per round X <- (a I + b A + c A A) X,
+ * A = X X^T: the rounds of muon.h, with its coefficients, schedules and limits on rounds. Here
+ * the rounds run on the Gram matrix alone: every X_r is P_r X_0 with P_r a polynomial of
+ * A_0 = X_0 X_0^T, so the stack is read once for A_0 and once for P X_0, whatever the rounds.
+ * A small singular value is known from A_0 to the square root of its precision only, and so the
+ * Gram matrix and the rounds are formed in double and P is rounded to fp32 once; the result is
+ * as exact as rounds in fp32 on X itself. It is rounded to bf16 once where that is its dtype.
+ *
+ * Every finite fp32 value is in range. A matrix of zeros gives zeros (for eps > 0). A NaN or
+ * infinity makes its own matrix NaN and no other. Equal inputs give equal bits, wherever in a
+ * stack a matrix stands, as long as the stack's sizes are equal.
+ *
+ * Conventions are those of muon.h, but that stacks need be aligned to their elements only.
+ */
+#ifndef MUON_ORTHOGONALIZE_H
+#define MUON_ORTHOGONALIZE_H
+
+#include "muon.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The stack: outer * inner matrices of rows x cols; element (o, i, r, c) at
+ * o * stride[0] + i * stride[1] + r * stride[2] + c * stride[3] elements. One of stride[2] and
+ * stride[3] must be 1 (or its side 1). The same strides hold for the result, whose elements
+ * must have places of their own. */
+typedef struct {
+  const void *in;
+  void *out;
+  int64_t outer, inner, rows, cols;
+  int64_t in_stride[4];
+  int64_t out_stride[4];
+  muon_dtype dtype; /* of both */
+} muon_stack;
+
+/* Bytes of workspace (256-byte aligned, no initial contents required) that a stack of these
+ * sizes needs: SIZE_MAX for sizes outside the limits (min(rows, cols) <= 128, max <= 2^24,
+ * outer * inner <= 2^24). */
+size_t muon_orthogonalize_workspace_size(int64_t outer, int64_t inner, int64_t rows, int64_t cols);
+
+/* out <- the orthogonalised matrices; of cfg: ns_steps (>= 0), a, b, c, schedule and eps. in and
+ * out may not overlap (but in == out with equal strides is taken: in place). */
+int muon_orthogonalize(const muon_stack *stack, const muon_config *cfg, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MUON_ORTHOGONALIZE_H */

@@ -38,5 +38,6 @@ from .optim import (  # noqa: F401
     cautious_adam_step,
     make_adam_config,
     make_config,
+    orthogonalize,
     zeropower_via_newtonschulz5,
 )

@@ -42,6 +42,7 @@ EXPORTED = (
     "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
     "muon_mx_codes_size", "muon_mx_scales_size", "muon_mx_quantize", "muon_mx_dequantize",
     "muon_mx_matmul_workspace_size", "muon_mx_matmul",
+    "muon_orthogonalize_workspace_size", "muon_orthogonalize",
 )
 MUON_MAX_STREAMS = 4
 MUON_ADAMW_F32 = 0
@@ -152,6 +153,20 @@ class muon_mx_source(ctypes.Structure):
         ("scales", ctypes.c_void_p),
         ("codes_t", ctypes.c_void_p),
         ("scales_t", ctypes.c_void_p),
+    ]
+
+
+class muon_stack(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("outer", ctypes.c_int64),
+        ("inner", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("in_stride", ctypes.c_int64 * 4),
+        ("out_stride", ctypes.c_int64 * 4),
+        ("dtype", ctypes.c_int),
     ]
 
 
@@ -268,6 +283,10 @@ def lib() -> ctypes.CDLL:
     L.muon_mx_matmul_workspace_size.restype = sz
     L.muon_mx_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ctypes.c_int, vp, sz, vp]
     L.muon_mx_matmul.restype = ctypes.c_int
+    L.muon_orthogonalize_workspace_size.argtypes = [i64, i64, i64, i64]
+    L.muon_orthogonalize_workspace_size.restype = sz
+    L.muon_orthogonalize.argtypes = [ctypes.POINTER(muon_stack), ctypes.POINTER(muon_config), vp, sz, vp]
+    L.muon_orthogonalize.restype = ctypes.c_int
     L.muon_status_string.argtypes = [ctypes.c_int]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_last_error.argtypes = []
@@ -515,3 +534,13 @@ def muon_mx_matmul(a_codes: int, a_scales: int, b_codes: int, b_scales: int, m: 
                    out: int, dtype: int, workspace, workspace_bytes: int, stream: int) -> None:
     _check(lib().muon_mx_matmul(a_codes, a_scales, b_codes, b_scales, m, n, k, out, dtype,
                                 workspace, workspace_bytes, stream))
+
+
+def muon_orthogonalize_workspace_size(outer: int, inner: int, rows: int, cols: int) -> int:
+    return int(lib().muon_orthogonalize_workspace_size(outer, inner, rows, cols))
+
+
+def muon_orthogonalize(stack: muon_stack, cfg: muon_config, workspace, workspace_bytes: int,
+                       stream: int) -> None:
+    _check(lib().muon_orthogonalize(ctypes.byref(stack), ctypes.byref(cfg), workspace,
+                                    workspace_bytes, stream))

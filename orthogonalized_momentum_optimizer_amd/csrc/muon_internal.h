@@ -12,6 +12,8 @@
 
 #include <vector>
 
+#include "muon.h"
+
 namespace muon {
 
 // Host-side error reporting shared by every entry point (muon_last_error reads it): fail
@@ -26,6 +28,9 @@ struct Range {
 };
 // MUON_OK, or MUON_ERR_INVALID_ARG when a written range overlaps any other range.
 int check_overlaps(std::vector<Range>& rs);
+// MUON_OK, or the failure of what a configuration says about the rounds (ns_steps, a, b, c, schedule,
+// eps).
+int check_config(const muon_config* cfg);
 
 constexpr int kPad = 128;        // wide shapes are padded to multiples of this
 

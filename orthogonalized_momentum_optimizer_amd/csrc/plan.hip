@@ -140,6 +140,12 @@ int check_cfg(const muon_config* cfg, bool momentum) {
   return MUON_OK;
 }
 
+}  // namespace
+
+int muon::check_config(const muon_config* cfg) { return check_cfg(cfg, false); }
+
+namespace {
+
 int check_workspace(const muon_plan* p, const void* ws, size_t bytes) {
   if (p->ws_bytes == 0) return MUON_OK;
   if (!ws) return fail(MUON_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", p->ws_bytes);

@@ -11,6 +11,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <vector>
@@ -457,7 +458,106 @@ PyObject* mx_matmul(PyObject*, PyObject* args) {
   }
 }
 
+// ---- orthogonalisation of stacks (include/orthogonalize.h) ----
+
+// muon_stack, for calls through an address.
+struct Stack {
+  const void* in;
+  void* out;
+  int64_t side[4];
+  int64_t in_stride[4], out_stride[4];
+  int dtype;
+};
+
+// orthogonalize(function, workspace_size, x, out, cfg, stream) -> out (a new tensor in x's order of
+// strides where it is None), or the status. x: at least 2-D, its leading dimensions two strides at
+// most.
+PyObject* orthogonalize(PyObject*, PyObject* args) {
+  PyObject *xo, *oo;
+  Buffer cfg;
+  unsigned long long function, size, stream;
+  if (!PyArg_ParseTuple(args, "KKOOy*K", &function, &size, &xo, &oo, &cfg.view, &stream))
+    return nullptr;
+  if (!THPVariable_Check(xo) || (oo != Py_None && !THPVariable_Check(oo)))
+    return refuse(PyExc_TypeError, "tensors expected");
+  try {
+    const at::Tensor& x = THPVariable_Unpack(xo);
+    if (!x.is_cuda() || x.layout() != at::kStrided || x.is_neg())
+      return refuse(PyExc_ValueError, "a CUDA tensor whose memory holds its values expected");
+    if (dtype_code(x) != 0 && dtype_code(x) != 1)
+      return refuse(PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32");
+    const int64_t d = x.dim();
+    if (d < 2) return refuse(PyExc_ValueError, "a matrix or a stack of them expected");
+    const c10::DeviceGuard guard(x.device());
+    at::Tensor out;
+    if (oo == Py_None) {                         // dense, dimensions in x's order of strides
+      std::vector<int64_t> order(d), strides(d);
+      for (int64_t i = 0; i < d; ++i) order[i] = i;
+      auto far = [&](int64_t i) {                // (a dimension without strides goes outside)
+        return x.size(i) > 1 && x.stride(i) == 0 ? INT64_MAX : x.stride(i);
+      };
+      std::stable_sort(order.begin(), order.end(), [&](int64_t a, int64_t b) { return far(a) > far(b); });
+      int64_t step = 1;
+      for (int64_t i = d; i-- > 0;) {
+        strides[order[i]] = step;
+        step *= std::max<int64_t>(x.size(order[i]), 1);
+      }
+      out = at::empty_strided(x.sizes(), strides, x.options().requires_grad(false));
+    } else {
+      out = THPVariable_Unpack(oo);
+      if (out.device() != x.device() || out.scalar_type() != x.scalar_type() ||
+          out.sizes() != x.sizes() || out.layout() != at::kStrided || out.is_neg())
+        return refuse(PyExc_ValueError, "out must be a tensor of x's shape, dtype and device");
+    }
+    Stack k{};
+    k.dtype = dtype_code(x);
+    k.in = x.numel() ? x.const_data_ptr() : nullptr;
+    k.out = x.numel() ? out.data_ptr() : nullptr;
+    // leading dimensions, from the last: each joins the group behind it or opens the next one outside
+    int64_t sides[2] = {1, 1}, si[2] = {0, 0}, so[2] = {0, 0};
+    int groups = 0;
+    for (int64_t i = d - 3; i >= 0; --i) {
+      const int64_t n = x.size(i);
+      if (n == 1) continue;
+      if (groups && x.stride(i) == si[groups - 1] * sides[groups - 1] &&
+          out.stride(i) == so[groups - 1] * sides[groups - 1]) {
+        sides[groups - 1] *= n;
+        continue;
+      }
+      if (groups == 2)
+        return refuse(PyExc_ValueError, "leading dimensions of more than two strides");
+      sides[groups] = n;
+      si[groups] = x.stride(i);
+      so[groups] = out.stride(i);
+      ++groups;
+    }
+    for (int j = 0; j < 2; ++j) {                // group 0 is the inner one
+      k.side[1 - j] = sides[j];
+      k.in_stride[1 - j] = si[j];
+      k.out_stride[1 - j] = so[j];
+      k.side[2 + j] = x.size(d - 2 + j);
+      k.in_stride[2 + j] = x.stride(d - 2 + j);
+      k.out_stride[2 + j] = out.stride(d - 2 + j);
+    }
+    typedef size_t (*Size)(int64_t, int64_t, int64_t, int64_t);
+    const size_t need = reinterpret_cast<Size>(size)(k.side[0], k.side[1], k.side[2], k.side[3]);
+    at::Tensor ws;
+    if (need && need != SIZE_MAX)
+      ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(x.device()));
+    typedef int (*Run)(const void*, const void*, void*, size_t, void*);
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = reinterpret_cast<Run>(function)(&k, cfg.view.buf, ws.defined() ? ws.data_ptr() : nullptr,
+                                             ws.defined() ? need : 0, reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
+  } catch (const std::exception& e) {
+    return refuse(PyExc_RuntimeError, e.what());
+  }
+}
+
 PyMethodDef methods[] = {
+    {"orthogonalize", orthogonalize, METH_VARARGS, "muon_orthogonalize of a stack."},
     {"mx_quantize", mx_quantize, METH_VARARGS, "muon_mx_quantize of tensors into new ones."},
     {"mx_dequantize", mx_dequantize, METH_VARARGS, "muon_mx_dequantize into a new tensor."},
     {"mx_matmul", mx_matmul, METH_VARARGS, "muon_mx_matmul into a new tensor."},

@@ -203,6 +203,46 @@ def zeropower_via_newtonschulz5(G: torch.Tensor, steps: int = 5, precision: str 
     return out
 
 
+_configs = {}
+_orthogonalize_calls = None
+
+
+def orthogonalize(x: torch.Tensor, steps: int = 5, abc=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  schedule=None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """NS(X / (||X||_F + eps)) for every matrix of x (.., rows, cols), a stack of small ones (the
+    shorter side up to 128: attention heads, low-rank factors), in fp32 accuracy: Newton-Schulz
+    rounds as in ``zeropower_via_newtonschulz5``, whose bf16 rounds and 2-D matrices of any size are
+    the other form. x: bfloat16 or float32, strided as it lies in a larger tensor, with rows or
+    columns contiguous and at most two strides among the leading dimensions, e.g. the heads of a
+    projection as ``w.view(heads, d, cols)`` or ``w.view(rows, heads, d).transpose(0, 1)``. The
+    result has x's dtype and order of strides. ``out``: where it goes (x itself: in place).
+    ``schedule``: None, or ``steps`` triples (a, b, c), one per round. Runs on the current stream and
+    may be captured."""
+    global _orthogonalize_calls
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("a CUDA tensor expected")
+    if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+        raise ValueError("orthogonalize has no backward pass: call it on x.detach() or under no_grad")
+    if schedule is None:
+        key = (steps, abc[0], abc[1], abc[2], eps)
+        cfg = _configs.get(key)
+        if cfg is None:
+            if len(_configs) > 64:
+                _configs.clear()
+            cfg = _configs[key] = make_config(ns_steps=steps, abc=abc, eps=eps)
+    else:
+        cfg = make_config(ns_steps=steps, abc=abc, eps=eps, schedule=schedule)
+    if _orthogonalize_calls is None:
+        lib = L.lib()
+        _orthogonalize_calls = (L.address_of(lib.muon_orthogonalize),
+                                L.address_of(lib.muon_orthogonalize_workspace_size))
+    result = L.args().orthogonalize(*_orthogonalize_calls, x, out, cfg,
+                                    torch.cuda.current_stream(x.device).cuda_stream)
+    if type(result) is int:
+        L.raise_status(result)
+    return result if out is None else out
+
+
 class Muon(torch.optim.Optimizer):
     """Muon: SGD-Nesterov momentum orthogonalised by Newton-Schulz, for 2-D (or stacked
     >= 3-D) weight matrices. Each >= 3-D parameter is treated as a stack of matrices over
