@@ -207,46 +207,57 @@ __device__ __forceinline__ void mx_tile(const MmArgs& g) {
     arrived(f0);
     scales_arrived();
   }
+  // One stage. Whether there is one to refill the buffer with, and a next one, is known at compile
+  // time: a branch between two products lets the compiler move products past the reads between them.
   int buf = 0;
-  for (int kt = 0; kt < KT; ++kt) {
+  auto iteration = [&](int kt, auto refill_t, auto more_t) {
+    constexpr bool refill = decltype(refill_t)::value, more = decltype(more_t)::value;
     const uint32_t cur = lds0 + buf * STAGE;
     const int nbuf = buf + 1 == S ? 0 : buf + 1;
     const uint32_t nxt = lds0 + nbuf * STAGE;
-    const bool more = kt + 1 < KT, refill = kt + S < KT;
     __builtin_amdgcn_sched_barrier(0);
     static_for<MMAS>([&](auto M) {
       constexpr int m = decltype(M)::value;
       mma(f0, M, I0{});
       __builtin_amdgcn_sched_barrier(0);
       static_for<READS>([&](auto O) {
-        if constexpr (decltype(O)::value * MMAS / READS == m) read(cur, ch1, f1, O);
+        if constexpr (decltype(O)::value * MMAS / READS / 2 == m) read(cur, ch1, f1, O);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
     arrived(f1);
-    if (more) stage_ready(min(S - 2, KT - 2 - kt));
+    if constexpr (refill) stage_ready(S - 2);
+    else if constexpr (more) stage_ready(min(S - 2, KT - 2 - kt));
     __builtin_amdgcn_sched_barrier(0);
     static_for<MMAS>([&](auto M) {
       constexpr int m = decltype(M)::value;
       mma(f1, M, I1{});
       __builtin_amdgcn_sched_barrier(0);
-      if (refill)
+      if constexpr (refill)
         static_for<LOADS>([&](auto O) {
           if constexpr (decltype(O)::value * MMAS / LOADS == m) load(kt + S, buf, decltype(O)::value);
         });
-      if (more)
+      if constexpr (more)
         static_for<READS>([&](auto O) {
-          if constexpr (decltype(O)::value * MMAS / READS == m) {
+          if constexpr (decltype(O)::value * MMAS / READS / 2 == m) {
             read(nxt, ch0, f0, O);
             read_scale(nxt, O);
           }
         });
       __builtin_amdgcn_sched_barrier(0);
     });
-    arrived(f0);
-    scales_arrived();
+    if constexpr (more) {
+      arrived(f0);
+      scales_arrived();
+    }
     buf = nbuf;
-  }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  int kt = 0;
+  for (; kt < KT - S; ++kt) iteration(kt, Yes{}, Yes{});
+  for (; kt < KT - 1; ++kt) iteration(kt, No{}, Yes{});
+  if (KT > 0) iteration(KT - 1, No{}, No{});
 
   // ---- out: register quad q of lane l is row l % 32, columns 8 q + 4 (l / 32) .. + 3 of a block ----
   char* const out = static_cast<char*>(g.out) + z * g.split_stride * 4;
