@@ -43,24 +43,23 @@ __device__ __forceinline__ uint32_t ds_read_b32_at(uint32_t addr) {
   return r;
 }
 
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
-// 4 consecutive values of a row of out, from column `col` on; OUT 0: bf16, 1: fp32.
+// 16 bytes of a row of out from element `at` on, of whose values `left` (any number) are there; OUT 0:
+// bf16, 1: fp32.
 template <int OUT>
-__device__ __forceinline__ void store4(void* out, int64_t at, int col, int n, f32x4 v) {
-  if (col + 4 <= n) {
-    if (OUT == 0) {
-      typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-      *reinterpret_cast<u32x2_a2*>(static_cast<uint16_t*>(out) + at) =
-          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    } else {
-      *reinterpret_cast<f32x4_a4*>(static_cast<float*>(out) + at) = v;
-    }
-  } else {
+__device__ __forceinline__ void store16(void* out, int64_t at, int left, u32x4 v) {
+  constexpr int N = OUT == 0 ? 8 : 4;
+  typedef u32x4 W __attribute__((aligned(2)));
+  if (left >= N) {
+    *reinterpret_cast<W*>(static_cast<char*>(out) + at * (16 / N)) = v;
+    return;
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n) store_one<OUT>(out, at + e, v[e]);
+  for (int e = 0; e < N; ++e) {
+    if (e >= left) continue;
+    if (OUT == 0) static_cast<uint16_t*>(out)[at + e] = uint16_t(v[e / 2] >> 16 * (e & 1));
+    else static_cast<uint32_t*>(out)[at + e] = v[e % 4];
   }
 }
 
@@ -260,20 +259,38 @@ __device__ __forceinline__ void mx_tile(const MmArgs& g) {
   if (KT > 0) iteration(KT - 1, No{}, No{});
 
   // ---- out: register quad q of lane l is row l % 32, columns 8 q + 4 (l / 32) .. + 3 of a block ----
+  // 32 rows at a time go through a part of LDS of the wave's own (rows 16 bytes further apart than
+  // they are long, so that the quads fall on all banks) and leave as whole rows, 16 bytes a lane.
+  constexpr int E = OUT == 0 ? 2 : 4, COLS = 32 * WN, PITCH = COLS * E + 16;
+  constexpr int LANES = COLS * E / 16, ROWS = 64 / LANES;      // lanes of a row, rows of a store
+  static_assert(4 * 32 * PITCH <= S * STAGE, "the waves' parts fit the ring");
+  __builtin_amdgcn_s_barrier();                  // everyone is done with the ring
+  asm volatile("" ::: "memory");
+  char* const part = lds + wave * (32 * PITCH);
   char* const out = static_cast<char*>(g.out) + z * g.split_stride * 4;
+  const int col = col0 + wc * COLS + lane % LANES * (16 / E);
 #pragma unroll
   for (int i = 0; i < WM; ++i) {
-    const int row = row0 + wr * 32 * WM + 32 * i + r;
-    if (row >= g.m) continue;
 #pragma unroll
     for (int j = 0; j < WN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int col = col0 + wc * 32 * WN + 32 * j + 8 * q + 4 * h;
-        store4<OUT>(out, int64_t(row) * g.n + col, col, g.n,
-                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                          acc[i][j][4 * q + 3]});
+        char* const to = part + r * PITCH + (32 * j + 8 * q + 4 * h) * E;
+        const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if constexpr (OUT == 0)
+          *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else
+          *reinterpret_cast<f32x4*>(to) = v;
       }
+    asm volatile("" ::: "memory");               // a wave's LDS accesses complete in their order
+    const int row0i = row0 + wr * 32 * WM + 32 * i;
+#pragma unroll
+    for (int k = 0; k < 32 / ROWS; ++k) {
+      const int rr = k * ROWS + lane / LANES, row = row0i + rr;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + rr * PITCH + lane % LANES * 16);
+      if (row < g.m) store16<OUT>(out, int64_t(row) * g.n + col, g.n - col, v);
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -291,7 +308,13 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(const float* part, int64_t 
   if (i + 4 <= count) {
     f32x4 s = *reinterpret_cast<const f32x4_a4*>(part + i);
     for (int z = 1; z < parts; ++z) s += *reinterpret_cast<const f32x4_a4*>(part + z * count + i);
-    store4<OUT>(out, i, 0, 4, s);
+    if (OUT == 0) {
+      typedef u32x2 W __attribute__((aligned(2)));
+      *reinterpret_cast<W*>(static_cast<uint16_t*>(out) + i) =
+          u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+    } else {
+      *reinterpret_cast<f32x4_a4*>(static_cast<float*>(out) + i) = s;
+    }
   } else {
     for (int64_t e = i; e < count; ++e) {
       float s = part[e];
