@@ -7,6 +7,7 @@
 // fp32. (With data-like operands and nothing else the matrix cores give 6.2 PFLOP/s by these and 3.7
 // by the 16x16x128 form.)
 #include <algorithm>
+#include <cmath>
 #include <vector>
 
 #include "mfma_common.h"
@@ -61,6 +62,24 @@ __device__ __forceinline__ void store16(void* out, int64_t at, int left, u32x4 v
     if (OUT == 0) static_cast<uint16_t*>(out)[at + e] = uint16_t(v[e / 2] >> 16 * (e & 1));
     else static_cast<uint32_t*>(out)[at + e] = v[e % 4];
   }
+}
+
+// 4 values likewise.
+template <int OUT>
+__device__ __forceinline__ void store4(void* out, int64_t at, int left, f32x4 v) {
+  if (left >= 4) {
+    if (OUT == 0) {
+      typedef u32x2 W __attribute__((aligned(2)));
+      *reinterpret_cast<W*>(static_cast<uint16_t*>(out) + at) =
+          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+      *reinterpret_cast<f32x4_a4*>(static_cast<float*>(out) + at) = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) store_one<OUT>(out, at + e, v[e]);
 }
 
 // ---- tiles -----------------------------------------------------------------------------------
@@ -295,8 +314,80 @@ __device__ __forceinline__ void mx_tile(const MmArgs& g) {
 }
 
 template <int WM, int WN, int S, int OUT>
-__global__ __launch_bounds__(256, 1) void mx_matmul_kernel(const MmArgs g) {
+__global__ __launch_bounds__(256, WM * WN == 16 ? 1 : 2) void mx_matmul_kernel(const MmArgs g) {
   mx_tile<WM, WN, S, OUT>(g);
+}
+
+// ---- few rows ----------------------------------------------------------------------------------
+//
+// Where one side has at most 64 rows the other operand (X) is read once and nothing else takes time: a
+// block takes one panel of it, its waves the steps in turn, straight from memory into the 16x16x128
+// instruction (a panel's step is a contiguous kilobyte, 16 bytes a lane), with up to four panels Y
+// of the short side, which stay in the caches. The waves' sums are added in LDS in their order. LEFT:
+// X is A. The operands' order puts four consecutive columns of out into a lane.
+template <int PANELS, int WAVES, bool LEFT, int OUT>
+__device__ __forceinline__ void mx_few_tile(const MmArgs& g) {
+  __shared__ f32x4 sums[PANELS][WAVES][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int panels_x = LEFT ? g.panels_a : g.panels_b, panels_y = LEFT ? g.panels_b : g.panels_a;
+  const uint8_t* const y = LEFT ? g.b : g.a;
+  const uint8_t* const sy = LEFT ? g.sb : g.sa;
+  // lane l: row l % 16, block l / 16
+  const int at = lane % 16 * 64 + lane / 16 * 16, sat = lane % 16 * 4 + lane / 16;
+  auto code = [&](const uint8_t* p, int64_t tile) {
+    return *reinterpret_cast<const u32x4*>(p + tile * kMxTileBytes + at);
+  };
+  auto wide = [](u32x4 v) { return i32x8{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0}; };
+  constexpr int AHEAD = 4;                       // steps whose loads are out at a time
+  for (int panel = blockIdx.x; panel < panels_x; panel += gridDim.x) {
+    const uint8_t* const x = (LEFT ? g.a : g.b) + int64_t(panel) * g.steps * kMxTileBytes;
+    const uint8_t* const sx = (LEFT ? g.sa : g.sb) + int64_t(panel) * g.steps * kMxTileScales;
+    f32x4 acc[PANELS] = {};
+    for (int k = wave; k < g.steps; k += WAVES * AHEAD) {
+      u32x4 cx[AHEAD], cy[AHEAD][PANELS];
+      int bx[AHEAD], by[AHEAD][PANELS];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int ku = min(k + u * WAVES, g.steps - 1);
+        cx[u] = code(x, ku);
+        bx[u] = sx[int64_t(ku) * kMxTileScales + sat];
+#pragma unroll
+        for (int p = 0; p < PANELS; ++p) {
+          const int64_t tile = int64_t(min(p, panels_y - 1)) * g.steps + ku;
+          cy[u][p] = code(y, tile);
+          by[u][p] = sy[tile * kMxTileScales + sat];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        // (a step beyond the last is the last again with codes of 0: it adds 0, or a NaN that is there)
+        if (k + u * WAVES >= g.steps) cx[u] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < PANELS; ++p)
+          acc[p] = LEFT ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cy[u][p]), wide(cx[u]), acc[p],
+                                                                          4, 4, 0, by[u][p], 0, bx[u])
+                        : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cx[u]), wide(cy[u][p]), acc[p],
+                                                                          4, 4, 0, bx[u], 0, by[u][p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PANELS; ++p) sums[p][wave][lane] = acc[p];
+    __syncthreads();
+    // register e of lane l: row l % 16 of the second operand's panel, row 4 (l / 16) + e of the first's
+    for (int p = wave; p < PANELS; p += WAVES) {
+      f32x4 v = sums[p][0][lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v += sums[p][w][lane];
+      const int row = 16 * (LEFT ? panel : p) + lane % 16, col = 16 * (LEFT ? p : panel) + lane / 16 * 4;
+      if (row < g.m) store4<OUT>(g.out, int64_t(row) * g.n + col, g.n - col, v);
+    }
+    __syncthreads();
+  }
+}
+
+template <int PANELS, int WAVES, bool LEFT, int OUT>
+__global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(const MmArgs g) {
+  mx_few_tile<PANELS, WAVES, LEFT, OUT>(g);
 }
 
 // The parts of a split product, added in their order.
@@ -308,13 +399,7 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(const float* part, int64_t 
   if (i + 4 <= count) {
     f32x4 s = *reinterpret_cast<const f32x4_a4*>(part + i);
     for (int z = 1; z < parts; ++z) s += *reinterpret_cast<const f32x4_a4*>(part + z * count + i);
-    if (OUT == 0) {
-      typedef u32x2 W __attribute__((aligned(2)));
-      *reinterpret_cast<W*>(static_cast<uint16_t*>(out) + i) =
-          u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
-    } else {
-      *reinterpret_cast<f32x4_a4*>(static_cast<float*>(out) + i) = s;
-    }
+    store4<OUT>(out, i, 4, s);
   } else {
     for (int64_t e = i; e < count; ++e) {
       float s = part[e];
@@ -326,21 +411,51 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(const float* part, int64_t 
 
 // ---- host ------------------------------------------------------------------------------------
 
+// How a product is done: `few` panels of the short side (few rows), or tiles of 64 wm x 64 wn in
+// `splits` parts of the steps.
 struct Choice {
-  int wm, wn;                                    // the tile is 64 wm x 64 wn
-  int splits;
+  int few;
+  bool left;                                     // few: the long side is A's
+  int wm, wn, splits;
 };
 
-constexpr int kCus = 256;
+constexpr int kFewRows = 64;
+
+// The tiles by estimated time, in us, from products measured on 256 compute units: a round of tiles
+// takes `stage` for each step and `fixed` (first loads, results); tiles of 256 x 256 have a compute
+// unit for themselves, the others two a unit. A split product's parts are written and read again (4 TB/s
+// and a launch).
+struct TileCost {
+  int wm, wn, slots;
+  double stage, fixed;
+};
+constexpr TileCost kTiles[] = {{4, 4, 256, 0.86, 6.0}, {2, 4, 512, 0.99, 1.6}, {4, 2, 512, 0.99, 1.6},
+                               {2, 2, 512, 0.53, 1.75}};
 
 Choice choose(int64_t m, int64_t n, int64_t steps) {
-  Choice c{4, 4, 1};
-  auto tiles = [&](int wm, int wn) {
-    return ((m + 64 * wm - 1) / (64 * wm)) * ((n + 64 * wn - 1) / (64 * wn));
-  };
-  if (tiles(4, 4) < kCus) c.wm = c.wn = 2;
-  const int64_t count = tiles(c.wm, c.wn);
-  if (count < kCus) c.splits = int(std::max<int64_t>(1, std::min<int64_t>(2 * kCus / count, steps / 4)));
+  Choice c{0, false, 4, 4, 1};
+  if (std::min(m, n) <= kFewRows) {
+    c.left = m > n;
+    c.few = int((std::min(m, n) + 15) / 16);
+    if (c.few == 3) c.few = 4;
+    return c;
+  }
+  double best = 1e300;
+  for (const TileCost& t : kTiles) {
+    const int64_t count = ((m + 64 * t.wm - 1) / (64 * t.wm)) * ((n + 64 * t.wn - 1) / (64 * t.wn));
+    for (int64_t z = 1; z == 1 || (z <= 64 && 2 * z <= steps && count * z <= 2 * t.slots); ++z) {
+      const double rounds = double(count * z) / t.slots;
+      const double each = double((steps + z - 1) / z) * t.stage + t.fixed;
+      double time = (rounds > 4 ? rounds + 0.5 : std::ceil(rounds)) * each;
+      if (z > 1) time += 3 + double(m) * double(n) * 8e-6 * double(z) / 4;
+      if (time < best) {
+        best = time;
+        c.wm = t.wm;
+        c.wn = t.wn;
+        c.splits = int(z);
+      }
+    }
+  }
   return c;
 }
 
@@ -350,16 +465,29 @@ bool limits_ok(int64_t m, int64_t n, int64_t k) {
 }
 
 int parts_of(const Choice& c, int64_t steps) {
-  const int64_t each = (steps + c.splits - 1) / c.splits;
+  const int64_t each = (steps + c.splits - 1) / c.splits;      // (few rows: one part)
   return steps == 0 ? 1 : int((steps + each - 1) / each);
+}
+
+template <int OUT, int PANELS, bool LEFT>
+void launch_few(const MmArgs& g, hipStream_t s) {
+  const unsigned blocks = unsigned(std::min(LEFT ? g.panels_a : g.panels_b, 1 << 20));
+  if (g.steps <= 16)
+    hipLaunchKernelGGL((mx_few_kernel<PANELS, 4, LEFT, OUT>), dim3(blocks), dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((mx_few_kernel<PANELS, 8, LEFT, OUT>), dim3(blocks), dim3(512), 0, s, g);
 }
 
 template <int OUT>
 void launch(const Choice& c, const MmArgs& g, hipStream_t s) {
-  if (c.wm == 4)
-    hipLaunchKernelGGL((mx_matmul_kernel<4, 4, 4, OUT>), dim3((unsigned)g.total), dim3(256), 0, s, g);
-  else
-    hipLaunchKernelGGL((mx_matmul_kernel<2, 2, 4, OUT>), dim3((unsigned)g.total), dim3(256), 0, s, g);
+  if (c.few == 1) return c.left ? launch_few<OUT, 1, true>(g, s) : launch_few<OUT, 1, false>(g, s);
+  if (c.few == 2) return c.left ? launch_few<OUT, 2, true>(g, s) : launch_few<OUT, 2, false>(g, s);
+  if (c.few) return c.left ? launch_few<OUT, 4, true>(g, s) : launch_few<OUT, 4, false>(g, s);
+  const dim3 grid((unsigned)g.total), block(256);
+  if (c.wm == 4 && c.wn == 4) hipLaunchKernelGGL((mx_matmul_kernel<4, 4, 4, OUT>), grid, block, 0, s, g);
+  else if (c.wm == 4) hipLaunchKernelGGL((mx_matmul_kernel<4, 2, 3, OUT>), grid, block, 0, s, g);
+  else if (c.wn == 4) hipLaunchKernelGGL((mx_matmul_kernel<2, 4, 3, OUT>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((mx_matmul_kernel<2, 2, 4, OUT>), grid, block, 0, s, g);
 }
 
 }  // namespace
