@@ -9,8 +9,9 @@
  * the rounds run on the Gram matrix alone: every X_r is P_r X_0 with P_r a polynomial of
  * A_0 = X_0 X_0^T, so the stack is read once for A_0 and once for P X_0, whatever the rounds.
  * A small singular value is known from A_0 to the square root of its precision only, and so the
- * Gram matrix and the rounds are formed in double and P is rounded to fp32 once; the result is
- * as exact as rounds in fp32 on X itself. It is rounded to bf16 once where that is its dtype.
+ * Gram matrix and the rounds are formed in double (bf16 stacks: of sums of 32 exact products in
+ * fp32) and P is rounded to fp32 once; the result is as exact as rounds in fp32 on X itself, or
+ * rounded to bf16 once where that is its dtype.
  *
  * Every finite fp32 value is in range. A matrix of zeros gives zeros (for eps > 0). A NaN or
  * infinity makes its own matrix NaN and no other. Equal inputs give equal bits, wherever in a

@@ -5,9 +5,9 @@
 // Gram matrix, so that X_r = P_r X_0 and A_r = P_r A_0 P_r, all of them s x s and, as polynomials of
 // A_0, symmetric and commuting:
 //   Q = a I + b A + c A A,   P <- Q P,   A <- Q A Q
-// Three launches: the Gram matrices (partial sums over pieces of the long side), the rounds on them
-// (a block a matrix), and P X. The stack is read twice and written once; rounds on X itself would
-// read and write it ten times.
+// The stack is read twice and written once, the second time mostly from the caches; rounds on X itself would
+// read and write it ten times. One launch, a block a matrix, or three where there are few matrices or they are
+// large: the Gram matrices (partial sums over pieces of the long side), the rounds on them, and P X.
 //
 // What A_0 costs in precision: an error E in A_0 moves a singular value's square by E, and the
 // rounds lift the small ones (by up to a^2 each), so that the result is off by about E / 2 sigma^2 for
@@ -15,6 +15,7 @@
 // several 1e-3 in its smallest directions; in double it is not.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "orthogonalize.h"
@@ -41,8 +42,8 @@ struct StackArgs {
   int count;                                     // of the batch
   int splits, span;                              // pieces of the long side, and a piece's length
   double* gram;                                  // count x splits x SP x SP
-  float* p;                                      // count x SP x SP
-  int* expo;                                     // count
+  uint16_t* p;                                   // count x 3 x SP x SP: P in parts
+  int* expo;                                     // count x 2: of two, for X and for the result
   double* scratch;                               // SP = 128: kBlocks x 3 x SP x SP
 };
 
@@ -110,293 +111,662 @@ __device__ __forceinline__ int64_t matrix_at(int64_t m, int inner, int64_t so, i
   return o * so + (m - o * inner) * si;
 }
 
+// ---- fp32 values as bf16 ones ---------------------------------------------------------------------
+//
+// x = x_1 + x_2 + x_3 with bf16 parts of 8 bits each, 24 together, so that a product of fp32 matrices is
+// six of bf16 on the matrix cores (x_1 y_1, x_1 y_2, x_2 y_1, x_2 y_2, x_1 y_3, x_3 y_1; what is left out
+// is 2^-24 of |x| |y|), 2.7 times as fast as their fp32 instructions.
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Two values' parts, packed.
+template <int PARTS>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[PARTS]) {
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    w[p] = pack_bf16x2(a, b);
+    if (p + 1 < PARTS) {
+      a -= __uint_as_float(w[p] << 16);
+      b -= __uint_as_float(w[p] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                 0, 0, 0);
+}
+
+// c += a b of operands in parts, the smallest terms first.
+template <int PA, int PB>
+__device__ __forceinline__ f32x4 mma_parts(const u32x4 (&a)[PA], const u32x4 (&b)[PB], f32x4 c) {
+  if constexpr (PA == 3) c = mma(a[2], b[0], c);
+  if constexpr (PB == 3) c = mma(a[0], b[2], c);
+  if constexpr (PA >= 2 && PB >= 2) c = mma(a[1], b[1], c);
+  if constexpr (PA >= 2) c = mma(a[1], b[0], c);
+  if constexpr (PB >= 2) c = mma(a[0], b[1], c);
+  return mma(a[0], b[0], c);
+}
+
+// ---- products in double ------------------------------------------------------------------------
+//
+// The matrix cores' 4x4x4 instruction, four products of 4 x 4 at a time, does 75 TFLOP/s in double and the
+// 16x16x4 one 38. A block of 16 x 16 is four of them: lane l has short index r = l % 16 of either
+// operand at step k = l / 16, and instruction t multiplies rows 4 b .. 4 b + 3 of the left one by
+// columns 4 ((b + t) % 4) .. of the right one, which comes 4 t lanes over. Sum t of lane l is then row
+// 4 (r / 4) + l / 16, column 4 ((r / 4 + t) % 4) + r % 4.
+
+template <int CTRL>
+__device__ __forceinline__ double row_rotate(double x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  return __builtin_bit_cast(
+      double, u32x2{uint32_t(__builtin_amdgcn_update_dpp(0, int(w[0]), CTRL, 0xf, 0xf, true)),
+                    uint32_t(__builtin_amdgcn_update_dpp(0, int(w[1]), CTRL, 0xf, 0xf, true))});
+}
+
+// x of the lanes 0, 4, 8 and 12 further on in each 16.
+struct Turns {
+  double v[4];
+  __device__ __forceinline__ explicit Turns(double x)
+      : v{x, row_rotate<0x12C>(x), row_rotate<0x128>(x), row_rotate<0x124>(x)} {}
+};
+
+__device__ __forceinline__ void mma_block(double a, const Turns& b, f64x4& acc) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f64_4x4x4f64(a, b.v[t], acc[t], 0, 0, 0);
+}
+__device__ __forceinline__ int block_row(int r, int q) { return 4 * (r / 4) + q; }
+__device__ __forceinline__ int block_col(int r, int t) { return (r + 4 * t) % 16; }
+
 // ---- the Gram matrix -------------------------------------------------------------------------
 //
-// A wave takes 16 long positions at a time: lane l holds, for each 16 short indexes (a block), the
-// values of short index r = l % 16 of it at positions 4 (l / 16) + 0..3, which are operands of four
-// v_mfma_f64_16x16x4 for every pair of blocks. Rows contiguous along the long side give them by one load
-// of four; contiguous along the short side (TALL) a load gives the values of all NB blocks at one
-// position, if block b has the short indexes NB r + b.
+// fp32: a wave takes 16 long positions at a time: lane l holds, for each 16 short indexes (a block), the
+// values of short index r = l % 16 of it at positions 4 (l / 16) + 0..3, operands of four steps in double for
+// every pair of blocks. bf16: 32 positions, eight a lane, are one operand of the bf16 instruction, whose
+// products are exact; its sums of 32 are fp32 and are added in double (in double throughout 64 x 768 takes a
+// compute unit 13 us more).
+// Rows contiguous along the long side give a lane's values by one load; contiguous along the short side
+// (TALL) a load gives the values of all NB blocks at one position, if block b has the short indexes
+// NB r + b. The next positions' values are on their way while these are multiplied.
+
+// Sums of the block's positions begin .. end - 1 into sum[SP * SP], where element (i, j) is there if
+// gram_held(i, j), else its mirror image is.
+template <bool TALL, int SP>
+__device__ __forceinline__ bool gram_held(int i, int j) {
+  constexpr int NB = SP / 16;
+  return TALL ? i % NB <= j % NB : i / 16 <= j / 16;
+}
+
+// LDS doubles that gram_part needs.
+template <int SP, int WAVES>
+struct GramShape {
+  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2, HALF = (WAVES + 1) / 2;
+  // what a wave passes on at a time: all its blocks, or at 128 a sixth of them
+  static constexpr int PASS = SP == 128 ? 6 : BLOCKS;
+  static constexpr int LDS = (WAVES / 2) * PASS * 256 > SP * SP ? (WAVES / 2) * PASS * 256 : SP * SP;
+};
+
+template <int DT, int NB>
+struct GramValues {
+  float x[NB][4];
+};
+template <int NB>
+struct GramValues<0, NB> {
+  u32x4 x[NB];
+};
+
+template <int DT, bool TALL, int SP, int WAVES>
+__device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, int begin, int end, int wave,
+                                          int lane, double* lds) {
+  using S = GramShape<SP, WAVES>;
+  constexpr int NB = SP / 16, STEP = DT ? 16 : 32;
+  const int r = lane & 15, q = lane >> 4;
+  f64x4 acc[S::BLOCKS];                          // blocks i <= j, row by row
+#pragma unroll
+  for (int u = 0; u < S::BLOCKS; ++u) acc[u] = f64x4{0, 0, 0, 0};
+  auto load = [&](int k0, GramValues<DT, NB>& to) {
+    const int k = k0 + STEP / 4 * q;
+    if constexpr (TALL) {
+      float v[STEP / 4][NB];
+#pragma unroll
+      for (int e = 0; e < STEP / 4; ++e)
+        load_n<DT, NB>(base, int64_t(k + e) * g.in_ld + NB * r, k + e < end ? g.s - NB * r : 0, v[e]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (DT) to.x[b][e] = v[e][b];
+          else to.x[b][e] = pack_bf16x2(v[2 * e][b], v[2 * e + 1][b]);
+        }
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float v[STEP / 4];
+        load_n<DT, STEP / 4>(base, int64_t(16 * b + r) * g.in_ld + k, 16 * b + r < g.s ? end - k : 0, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (DT) to.x[b][e] = v[e];
+          else to.x[b][e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        }
+      }
+    }
+  };
+  constexpr bool EARLY = SP < 128;               // (at 128 there are no registers for it)
+  GramValues<DT, NB> x, next;
+  int k0 = begin + STEP * wave;
+  if (EARLY) load(k0, x);
+  for (; k0 < end; k0 += STEP * WAVES) {
+    if (EARLY) load(k0 + STEP * WAVES, next);
+    else load(k0, x);
+    if constexpr (DT == 0) {
+#pragma unroll
+      for (int i = 0, u = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = i; j < NB; ++j, ++u) {
+          const f32x4 c = mma(x.x[i], x.x[j], f32x4{0, 0, 0, 0});
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[u][e] += double(c[e]);
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const Turns d(x.x[j][e]);
+#pragma unroll
+          for (int i = 0; i <= j; ++i) mma_block(double(x.x[i][e]), d, acc[i * NB - i * (i - 1) / 2 + j - i]);
+        }
+    }
+    if (EARLY) x = next;
+  }
+  // the waves' sums, the upper half's to the lower half until one wave has them all
+#pragma unroll
+  for (int n = WAVES; n > 1; n = (n + 1) / 2) {
+    const int half = (n + 1) / 2;
+#pragma unroll
+    for (int u0 = 0; u0 < S::BLOCKS; u0 += S::PASS) {
+      f64x4* const pass = reinterpret_cast<f64x4*>(lds) + lane;
+      if (wave >= half && wave < n)
+#pragma unroll
+        for (int u = 0; u < S::PASS; ++u) pass[((wave - half) * S::PASS + u) * 64] = acc[u0 + u];
+      __syncthreads();
+      if (wave < n - half)
+#pragma unroll
+        for (int u = 0; u < S::PASS; ++u) acc[u0 + u] += pass[(wave * S::PASS + u) * 64];
+      __syncthreads();
+    }
+  }
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 0, u = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = i; j < NB; ++j, ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int a = DT ? block_row(r, q) : 4 * q + e, c = DT ? block_col(r, e) : r;
+          lds[TALL ? (NB * a + i) * SP + NB * c + j : (16 * i + a) * SP + 16 * j + c] = acc[u][e];
+        }
+  }
+  __syncthreads();
+}
+
+// A part of a matrix's long side (grid: count * splits) into its own whole matrix.
 template <int DT, bool TALL, int SP>
 __global__ __launch_bounds__(256, 1) void gram_kernel(const StackArgs g) {
-  constexpr int NB = SP / 16;
-  __shared__ double sum[SP * SP];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, q = lane >> 4;
+  __shared__ double sum[GramShape<SP, 4>::LDS];
+  const int t = threadIdx.x;
   const int m = blockIdx.x / g.splits, z = blockIdx.x - m * g.splits;
   const char* const base = static_cast<const char*>(g.in) +
                            matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
-  const int begin = z * g.span, end = min(g.l, begin + g.span);
-
-  f64x4 acc[NB][NB];                             // b1 <= b2
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = f64x4{0, 0, 0, 0};
-  for (int k0 = begin + 16 * wave; k0 < end; k0 += 64) {
-    float x[NB][4];
-    const int k = k0 + 4 * q;
-    if constexpr (TALL) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v[NB];
-        load_n<DT, NB>(base, int64_t(k + e) * g.in_ld + NB * r, k + e < end ? g.s - NB * r : 0, v);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) x[b][e] = v[b];
-      }
-    } else {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        load_n<DT, 4>(base, int64_t(16 * b + r) * g.in_ld + k, 16 * b + r < g.s ? end - k : 0, x[b]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      double d[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) d[b] = x[b][e];
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = i; j < NB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[i], d[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  // the four waves' sums in their order; register e of lane l is row 4 e + l / 16, column l % 16
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = i; j < NB; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int a = 4 * e + q;
-            double* const to = &sum[TALL ? (NB * a + i) * SP + NB * r + j : (16 * i + a) * SP + 16 * j + r];
-            *to = w ? *to + acc[i][j][e] : acc[i][j][e];
-          }
-    }
-    __syncthreads();
-  }
+  const int begin = z * g.span;
+  gram_part<DT, TALL, SP, 4>(g, base, begin, min(g.l, begin + g.span), t >> 6, t & 63, sum);
   double* const out = g.gram + int64_t(blockIdx.x) * (SP * SP);
   for (int at = t; at < SP * SP; at += 256) {
     const int i = at / SP, j = at % SP;
-    const bool held = TALL ? i % NB <= j % NB : i / 16 <= j / 16;
-    out[at] = held ? sum[at] : sum[j * SP + i];
+    out[at] = gram_held<TALL, SP>(i, j) ? sum[at] : sum[j * SP + i];
   }
 }
 
 // ---- the rounds ------------------------------------------------------------------------------
 
-template <int SP>
-struct RoundShape {
-  static constexpr int BM = SP <= 32 ? 1 : 2, BN = SP <= 64 ? 1 : 2;   // blocks of 16 x 16 a wave
-  static constexpr int WAVES = SP / 16 / BM * (SP / 16 / BN);
-  static constexpr int PITCH = SP == 16 ? 16 : SP + 16;                // banks: rows apart by 128 bytes
+// What comes of the norm. The result is P X / norm. Where X's norm and `norm` are in the middle of fp32's
+// range the division goes to P; else X is taken at 2^-ex of itself, P and the result near 1, and
+// the result gets the power of two that is left.
+struct Norm {
+  double scale, p_scale;
+  int x_expo, out_expo;
+  __device__ __forceinline__ Norm(double trace, float eps) {
+    const double plain = sqrt(trace), norm = plain + double(eps);
+    scale = 1.0 / norm;
+    x_expo = out_expo = 0;
+    const bool fine = isfinite(norm) && norm > 0;
+    p_scale = fine ? scale : __longlong_as_double(0x7ff8000000000000ll);
+    if (!fine) return;
+    int ex, en;
+    frexp(plain, &ex);
+    const double mant = frexp(norm, &en);
+    if (plain == 0) ex = en;
+    if (abs(ex) <= 60 && abs(en) <= 60) return;
+    p_scale = 1.0 / mant;
+    x_expo = -ex;
+    out_expo = ex - en;
+  }
 };
 
-// acc = X Y of symmetric X and Y (element (i, j) at i * pitch + j).
-template <int SP, int PX, int PY>
-__device__ __forceinline__ void product(const double* X, const double* Y, int row0, int col0, int r, int q,
-                                        f64x4 (&acc)[RoundShape<SP>::BM][RoundShape<SP>::BN]) {
-  constexpr int BM = RoundShape<SP>::BM, BN = RoundShape<SP>::BN;
+// A block a matrix, in double. Every product is symmetric, so that a wave computes OWN of the
+// blocks of 16 x 16 on and above the diagonal and writes them twice: 10 of 16 blocks for SP = 64, by as many
+// waves, 36 of 64 for 128. A, Q, P and T = QA lie in LDS up to SP = 64; at 128 (a matrix is 128 KB) Q does,
+// and the others in the block's own scratch, in L2. A round has three parts with a barrier behind each:
+//   A A, written as Q;   Q P and Q A, written as T;   P is written, Q T, written as A.
+// No part writes what it or the part before reads in other waves.
+template <int SP>
+struct RoundShape {
+  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2, OWN = SP == 128 ? 3 : 1;
+  static constexpr int WAVES = BLOCKS / OWN;
+  static constexpr int PITCH = SP == 128 ? SP + 16 : SP + 4;
+  static constexpr bool FAR = SP > 64;
+  static constexpr int LDS = (FAR ? 1 : 4) * SP * PITCH;               // doubles
+};
+
+template <int SP>
+struct RoundBlocks {
+  static constexpr int OWN = RoundShape<SP>::OWN;
+  int row0[OWN], col0[OWN];                      // of this wave's blocks
+  int r, q;
+  __device__ __forceinline__ RoundBlocks(int wave, int lane) : r(lane & 15), q(lane >> 4) {
 #pragma unroll
-  for (int i = 0; i < BM; ++i)
-#pragma unroll
-    for (int j = 0; j < BN; ++j) acc[i][j] = f64x4{0, 0, 0, 0};
-#pragma unroll 4
-  for (int k = 0; k < SP; k += 4) {
-    double a[BM], b[BN];
-#pragma unroll
-    for (int i = 0; i < BM; ++i) a[i] = X[(k + q) * PX + row0 + 16 * i + r];
-#pragma unroll
-    for (int j = 0; j < BN; ++j) b[j] = Y[(k + q) * PY + col0 + 16 * j + r];
-#pragma unroll
-    for (int i = 0; i < BM; ++i)
-#pragma unroll
-      for (int j = 0; j < BN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[i], b[j], acc[i][j], 0, 0, 0);
+    for (int o = 0; o < OWN; ++o) {
+      int u = wave * OWN + o, i = 0;
+      while (u >= RoundShape<SP>::NB - i) u -= RoundShape<SP>::NB - i++;
+      row0[o] = 16 * i;
+      col0[o] = 16 * (i + u);
+    }
   }
+  // f(o, e, row, column) for the elements that this thread holds of a product
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    int lane_r = r;
+    asm volatile("" : "+v"(lane_r));             // (else every place's address stays in a register: spills at 128)
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(o, e, row0[o] + block_row(lane_r, q), col0[o] + block_col(lane_r, e));
+  }
+  // f(at, value) for the element and, outside the diagonal blocks, its mirror image
+  template <typename T>
+  __device__ __forceinline__ void put(T* M, int pitch, int row, int col, T v) const {
+    M[uint32_t(row * pitch + col)] = v;
+    if (row / 16 != col / 16) M[uint32_t(col * pitch + row)] = v;
+  }
+};
+
+// The rounds on c, this wave's blocks of the Gram matrix; p receives its blocks of P. lds: LDS doubles;
+// scratch: 3 SP SP doubles at SP = 128; trace_of: SP doubles of LDS.
+template <int SP>
+__device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<SP>& B, int lane, double* lds,
+                                            double* scratch, double* trace_of,
+                                            f64x4 (&c)[RoundShape<SP>::OWN], f64x4 (&p)[RoundShape<SP>::OWN]) {
+  using S = RoundShape<SP>;
+  constexpr int OWN = S::OWN;
+  constexpr bool FAR = S::FAR;
+  constexpr int P1 = S::PITCH, P2 = FAR ? SP : S::PITCH;
+  double* const Q = lds;
+  double* const A = FAR ? scratch : lds + SP * P1;
+  double* const P = A + SP * P2;
+  double* const T = P + SP * P2;
+  const int r = B.r, q = B.q;
+
+  // AHEAD steps' operands are read before the first of them is used.
+  constexpr int AHEAD = SP < 32 ? 4 : 8;
+  auto product = [&](const double* X, int px, const double* Y, int py, f64x4 (&acc)[OWN]) {
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      acc[o] = f64x4{0, 0, 0, 0};
+      uint32_t x = q * px + B.row0[o] + r, y = q * py + B.col0[o] + r;
+#pragma unroll 1
+      for (int k = 0; k < SP; k += 4 * AHEAD) {
+        double a[AHEAD], b[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          a[u] = X[x + uint32_t(4 * u * px)];
+          b[u] = Y[y + uint32_t(4 * u * py)];
+        }
+        x += 4 * AHEAD * px;
+        y += 4 * AHEAD * py;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) mma_block(a[u], Turns(b[u]), acc[o]);
+      }
+    }
+  };
+
+  B.each([&](int o, int e, int row, int col) {
+    if (row == col) trace_of[row] = c[o][e];
+  });
+  __syncthreads();
+  double trace = 0;                              // the same in every wave
+  for (int i = lane; i < SP; i += 64) trace += trace_of[i];
+  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
+  const Norm norm(trace, R.eps);
+  B.each([&](int o, int e, int row, int col) {
+    B.put(A, P2, row, col, c[o][e] * norm.scale * norm.scale);
+    p[o][e] = row == col ? 1.0 : 0.0;
+  });
+  __syncthreads();
+  for (int n = 0; n < R.n; ++n) {
+    const double a = R.abc[3 * n], b = R.abc[3 * n + 1], cc = R.abc[3 * n + 2];
+    product(A, P2, A, P2, c);
+    B.each([&](int o, int e, int row, int col) {
+      const double v = (row == col ? a : 0.0) + b * A[uint32_t(row * P2 + col)] + cc * c[o][e];
+      B.put(Q, P1, row, col, v);
+      if (n == 0) p[o][e] = v;
+    });
+    __syncthreads();
+    if (n > 0) product(Q, P1, P, P2, p);
+    if (n + 1 == R.n) break;
+    product(Q, P1, A, P2, c);
+    B.each([&](int o, int e, int row, int col) { B.put(T, P2, row, col, c[o][e]); });
+    __syncthreads();
+    B.each([&](int o, int e, int row, int col) { B.put(P, P2, row, col, p[o][e]); });
+    product(Q, P1, T, P2, c);
+    B.each([&](int o, int e, int row, int col) { B.put(A, P2, row, col, c[o][e]); });
+    __syncthreads();
+  }
+  return norm;
 }
 
-// A, Q and P lie in LDS up to SP = 64. At 128 (a matrix is 128 KB) LDS has Q, or A for its square, and
-// A, QA and P go through the block's own scratch, in L2.
+// P in three bf16 parts, element (i, j) of part k at (k SP + i) pitch + j.
+template <int SP>
+__device__ __forceinline__ void put_parts(const RoundBlocks<SP>& B, const Norm& norm,
+                                          const f64x4 (&p)[RoundShape<SP>::OWN], uint16_t* out, int pitch) {
+  B.each([&](int o, int e, int row, int col) {
+    float v = float(p[o][e] * norm.p_scale);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t w = pack_bf16x2(v, 0.f);
+      B.put(out + k * SP * pitch, pitch, row, col, uint16_t(w));
+      v -= __uint_as_float(w << 16);
+    }
+  });
+}
+
 template <int SP>
 __global__ __launch_bounds__(RoundShape<SP>::WAVES * 64, 1) void rounds_kernel(const StackArgs g,
                                                                               const Rounds R) {
   using S = RoundShape<SP>;
-  constexpr bool FAR = SP > 64;
-  constexpr int P1 = S::PITCH, P2 = FAR ? SP : S::PITCH, THREADS = S::WAVES * 64;
-  __shared__ double lds[(FAR ? 1 : 3) * SP * P1];
-  __shared__ double trace_of[1];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, q = lane >> 4;
-  constexpr int ACROSS = SP / 16 / S::BN;        // waves side by side
-  const int row0 = wave / ACROSS * 16 * S::BM, col0 = wave % ACROSS * 16 * S::BN;
-  double* const Q = lds;
-  double* const A = FAR ? g.scratch + int64_t(blockIdx.x) * 3 * SP * SP : lds + SP * P1;
-  double* const P = A + SP * P2;
-  double* const T = FAR ? P + SP * P2 : A;       // QA
-
-  auto each = [&](auto&& f) {                    // the elements that this thread holds of a product
-#pragma unroll
-    for (int i = 0; i < S::BM; ++i)
-#pragma unroll
-      for (int j = 0; j < S::BN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f(i, j, e, row0 + 16 * i + 4 * e + q, col0 + 16 * j + r);
-  };
-
+  __shared__ double lds[S::LDS];
+  __shared__ double trace_of[SP];
+  const int t = threadIdx.x, lane = t & 63;
+  const RoundBlocks<SP> B(__builtin_amdgcn_readfirstlane(t >> 6), lane);
   for (int m = blockIdx.x; m < g.count; m += gridDim.x) {
     const double* const part = g.gram + int64_t(m) * g.splits * (SP * SP);
-    f64x4 c[S::BM][S::BN], p[S::BM][S::BN], own[S::BM][S::BN];
-    auto gram_at = [&](int row, int col) {
-      double v = part[row * SP + col];
-      for (int z = 1; z < g.splits; ++z) v += part[int64_t(z) * SP * SP + row * SP + col];
-      return v;
-    };
-    each([&](int i, int j, int e, int row, int col) {
-      own[i][j][e] = gram_at(row, col);
-      p[i][j][e] = row == col ? 1.0 : 0.0;
-      A[row * P2 + col] = own[i][j][e];
-    });
-    __syncthreads();
-    if (t < 64) {
-      double v = 0;
-      for (int i = lane; i < SP; i += 64) v += A[i * P2 + i];
-      for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-      if (t == 0) trace_of[0] = v;
+    f64x4 c[S::OWN], p[S::OWN];
+    B.each([&](int o, int e, int row, int col) { c[o][e] = part[row * SP + col]; });
+#pragma unroll 4
+    for (int z = 1; z < g.splits; ++z)           // (all elements of a part are on their way at once)
+      B.each([&](int o, int e, int row, int col) { c[o][e] += part[z * (SP * SP) + row * SP + col]; });
+    const Norm norm = rounds_part<SP>(R, B, lane, lds, g.scratch + int64_t(blockIdx.x) * 3 * SP * SP, trace_of,
+                                      c, p);
+    if (t == 0) {
+      g.expo[2 * m] = norm.x_expo;
+      g.expo[2 * m + 1] = norm.out_expo;
     }
-    __syncthreads();
-    const double norm = sqrt(trace_of[0]) + double(R.eps), scale = 1.0 / norm;
-    each([&](int i, int j, int e, int row, int col) {
-      own[i][j][e] = own[i][j][e] * scale * scale;
-      A[row * P2 + col] = own[i][j][e];
-      if (FAR) Q[row * P1 + col] = own[i][j][e];
-    });
-    __syncthreads();
-    for (int n = 0; n < R.n; ++n) {
-      const double a = R.abc[3 * n], b = R.abc[3 * n + 1], cc = R.abc[3 * n + 2];
-      const bool last = n + 1 == R.n;
-      if (FAR) product<SP, P1, P1>(Q, Q, row0, col0, r, q, c);         // Q holds A here
-      else product<SP, P2, P2>(A, A, row0, col0, r, q, c);
-      __syncthreads();
-      each([&](int i, int j, int e, int row, int col) {
-        const double v = (row == col ? a : 0.0) + b * own[i][j][e] + cc * c[i][j][e];
-        Q[row * P1 + col] = v;
-        if (n == 0) p[i][j][e] = v;
-      });
-      __syncthreads();
-      if (n > 0) product<SP, P1, P2>(Q, P, row0, col0, r, q, p);
-      if (last) break;
-      product<SP, P1, P2>(Q, A, row0, col0, r, q, c);
-      __syncthreads();
-      each([&](int i, int j, int e, int row, int col) {
-        T[row * P2 + col] = c[i][j][e];
-        P[row * P2 + col] = p[i][j][e];
-      });
-      __syncthreads();
-      product<SP, P1, P2>(Q, T, row0, col0, r, q, own);
-      __syncthreads();
-      each([&](int i, int j, int e, int row, int col) {
-        A[row * P2 + col] = own[i][j][e];
-        if (FAR) Q[row * P1 + col] = own[i][j][e];
-      });
-      __syncthreads();
-    }
-    // P / norm as a matrix near 1 and a power of two for X, so that neither leaves fp32's range
-    int expo = 0;
-    const bool fine = isfinite(norm);
-    const double f = fine ? 1.0 / frexp(norm, &expo) : __longlong_as_double(0x7ff8000000000000ll);
-    each([&](int i, int j, int e, int row, int col) {
-      g.p[int64_t(m) * SP * SP + row * SP + col] = float(p[i][j][e] * f);
-    });
-    if (t == 0) g.expo[m] = fine ? -expo : 0;
+    put_parts<SP>(B, norm, p, g.p + int64_t(m) * 3 * SP * SP, SP);
     __syncthreads();
   }
 }
 
 // ---- the result ------------------------------------------------------------------------------
 //
-// A wave takes 64 long positions: their values stay in registers, P comes from LDS, one operand for four
-// v_mfma_f32_16x16x4. The operands' order is chosen so that four values of a register quad lie side by
-// side in the result: along the long side (X is the left operand, and block b of positions is
-// 4 r + b), or along the short one (TALL, P is the left operand).
+// P X by bf16 parts, P in three, fp32 values in three and bf16 ones as they are. A wave takes 64 long
+// positions: lane l has short indexes
+// 8 (l / 16) + 0..7 of each 32 at its positions, P's operands come from LDS. The
+// operands' order is chosen so that four values of a register quad lie side by side in the result: along the
+// long side (X is the left operand, and lane l has positions 4 t(l) + 0..3 of the 64, t the 4 x 4 transpose
+// of l % 16: four lanes then store 64 bytes in a row), or along the short one (TALL, P is
+// the left operand, and a lane's eight short indexes one load).
+
+template <int SP>
+struct ResultShape {
+  static constexpr int PITCH = SP + 8;           // of a part of P in LDS
+};
+
+// Positions begin .. end - 1, those of wave 0 first. p: P's parts in LDS, as put_parts writes them.
+template <int DT, bool TALL, int SP, int WAVES>
+__device__ __forceinline__ void result_part(const StackArgs& g, const char* in, char* out, const uint16_t* p,
+                                            int expo, int expo_out, int begin, int end, int wave, int lane) {
+  constexpr int NB = SP / 16, KS = SP < 32 ? 1 : SP / 32, PARTS = DT ? 3 : 1, PITCH = ResultShape<SP>::PITCH;
+  const int r = lane & 15, q = lane >> 4;
+  const int turned = r / 4 + r % 4 * 4;
+  for (int j0 = begin + 64 * wave; j0 < end; j0 += 64 * WAVES) {
+    f32x4 acc[NB][4] = {};
+#pragma unroll 1
+    for (int k = 0; k < KS; ++k) {
+      const int row = 32 * k + 8 * q;
+      float v[8][4];
+      if constexpr (!TALL) {
+        const int j = j0 + 4 * turned;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          load_n<DT, 4>(in, int64_t(row + e) * g.in_ld + j, row + e < g.s ? end - j : 0, v[e]);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int j = j0 + 16 * b + r;
+          float w[8];
+          load_n<DT, 8>(in, int64_t(j) * g.in_ld + row, j < end ? g.s - row : 0, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e][b] = w[e];
+        }
+      }
+      if (expo)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) v[e][b] = ldexpf(v[e][b], expo);
+      u32x4 x[4][PARTS];                         // of position block b: the lane's 8 short indexes
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[PARTS];
+          split2(v[2 * e][b], v[2 * e + 1][b], w);
+#pragma unroll
+          for (int a = 0; a < PARTS; ++a) x[b][a][e] = w[a];
+        }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        u32x4 o[3];
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+          o[a] = *reinterpret_cast<const u32x4*>(p + (a * SP + 16 * i + r) * PITCH +
+                                                 (SP < 32 ? 8 * (q & 1) : 32 * k + 8 * q));
+          if (SP < 32 && q > 1) o[a] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          acc[i][b] = TALL ? mma_parts(o, x[b], acc[i][b]) : mma_parts(x[b], o, acc[i][b]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (expo_out)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][b][e] = ldexpf(acc[i][b][e], expo_out);
+      if constexpr (TALL) {
+        const int row = 16 * i + 4 * q;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int j = j0 + 16 * b + r;
+          if (j < end) store_4<DT>(out, int64_t(j) * g.out_ld + row, g.s - row, acc[i][b]);
+        }
+      } else {
+        const int row = 16 * i + r;
+        if (row < g.s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = j0 + 16 * e + 4 * q;
+            store_4<DT>(out, int64_t(row) * g.out_ld + at, end - at,
+                        f32x4{acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]});
+          }
+      }
+    }
+  }
+}
+
 template <int DT, bool TALL, int SP>
-__global__ __launch_bounds__(256) void result_kernel(const StackArgs g, int chunks, int chunk) {
-  constexpr int NB = SP / 16, PITCH = TALL ? SP + 4 : SP + 16;
-  __shared__ float P[SP * PITCH];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, q = lane >> 4;
+__global__ __launch_bounds__(256, SP == 128 ? 1 : 2) void result_kernel(const StackArgs g, int chunks, int chunk) {
+  constexpr int PITCH = ResultShape<SP>::PITCH;
+  __shared__ uint4 smem[3 * SP * PITCH / 8];
+  uint16_t* const lds = reinterpret_cast<uint16_t*>(smem);
+  const int t = threadIdx.x;
   const int m = blockIdx.x / chunks, z = blockIdx.x - m * chunks;
   const char* const in = static_cast<const char*>(g.in) +
                          matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
   char* const out = static_cast<char*>(g.out) +
                     matrix_at(g.first + m, g.inner, g.out_outer, g.out_inner) * (DT ? 4 : 2);
-  const float* const p = g.p + int64_t(m) * SP * SP;
-  for (int at = t; at < SP * SP; at += 256) P[at / SP * PITCH + at % SP] = p[at];
-  const int expo = g.expo[m];
+  const uint16_t* const p = g.p + int64_t(m) * 3 * SP * SP;
+  for (int at = t * 8; at < 3 * SP * SP; at += 2048)
+    *reinterpret_cast<u32x4*>(lds + at / SP * PITCH + at % SP) = *reinterpret_cast<const u32x4*>(p + at);
   __syncthreads();
-  const int end = min(g.l, (z + 1) * chunk);
-  for (int j0 = z * chunk + 64 * wave; j0 < end; j0 += 256) {
-    if constexpr (!TALL) {
-      float x[SP / 4][4];
-      const int j = j0 + 4 * r;
+  result_part<DT, TALL, SP, 4>(g, in, out, lds, g.expo[2 * m], g.expo[2 * m + 1], z * chunk,
+                               min(g.l, (z + 1) * chunk), t >> 6, t & 63);
+}
+
+// ---- all of it in one launch -------------------------------------------------------------------
+//
+// Where there are enough matrices, or their long sides are short: a block a matrix, which it reads a second
+// time from the caches. fp32 1200 x 64 x 1600: 665 to 703 us, in three launches 719 to 843 (gram 243, rounds
+// 260, result 230); bf16 1200 x 64 x 1600: 485 and 592; bf16 144 x 64 x 768: 68 and 77 us; 1 x 16 x 768: 15
+// and 21. Of bf16 144 x 64 x 768 the rounds take 42 us (10.4 each, 2.6 a product), which the matrix cores'
+// double rate bounds at 1.3: a wave also turns its operands (6 of 10 issue slots) and waits for LDS.
+
+template <int SP>
+struct WholeShape {
+  static constexpr int WAVES = SP == 32 ? 4 : RoundShape<SP>::WAVES;
+  static constexpr int LDS = RoundShape<SP>::LDS;
+};
+
+template <int DT, bool TALL, int SP>
+__global__ __launch_bounds__(WholeShape<SP>::WAVES * 64, 1) void whole_kernel(const StackArgs g,
+                                                                             const Rounds R) {
+  using S = RoundShape<SP>;
+  constexpr int WAVES = WholeShape<SP>::WAVES;
+  static_assert(3 * SP * ResultShape<SP>::PITCH * 2 <= S::LDS * 8 && GramShape<SP, WAVES>::LDS <= S::LDS,
+                "P's parts and the sums fit");
+  __shared__ double lds[S::LDS];                 // sums, then the rounds' matrices, then P's parts
+  __shared__ double trace_of[SP];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const RoundBlocks<SP> B(min(wave, S::WAVES - 1), lane);
+  const int m = blockIdx.x;
+  const char* const in = static_cast<const char*>(g.in) +
+                         matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
+  char* const out = static_cast<char*>(g.out) +
+                    matrix_at(g.first + m, g.inner, g.out_outer, g.out_inner) * (DT ? 4 : 2);
+  gram_part<DT, TALL, SP, WAVES>(g, in, 0, g.l, wave, lane, lds);
+  f64x4 c[S::OWN], p[S::OWN];
+  B.each([&](int o, int e, int row, int col) {
+    c[o][e] = gram_held<TALL, SP>(row, col) ? lds[row * SP + col] : lds[col * SP + row];
+  });
+  // (a wave beyond the blocks does the last one again: it writes the same values to the same places)
+  const Norm norm = rounds_part<SP>(R, B, lane, lds, nullptr, trace_of, c, p);
+  __syncthreads();
+  uint16_t* const parts = reinterpret_cast<uint16_t*>(lds);
+  put_parts<SP>(B, norm, p, parts, ResultShape<SP>::PITCH);
+  __syncthreads();
+  result_part<DT, TALL, SP, WAVES>(g, in, out, parts, norm.x_expo, norm.out_expo, 0, g.l, wave, lane);
+}
+
+// Up to 16 short indexes a matrix is one block of the 16x16x4 instruction, whose results lie as its
+// operands have to: register e of lane l is row 4 e + l / 16, column l % 16, and the operand of step e,
+// of a symmetric matrix, is that same element. The rounds then take no LDS and no barrier, and every wave
+// does them for itself.
+template <int DT, bool TALL>
+__global__ __launch_bounds__(512) void narrow_kernel(const StackArgs g, const Rounds R) {
+  constexpr int SP = 16, WAVES = 8, PITCH = ResultShape<SP>::PITCH;
+  __shared__ f64x4 sums[WAVES][64];
+  __shared__ uint4 smem[3 * SP * PITCH / 8];
+  uint16_t* const parts = reinterpret_cast<uint16_t*>(smem);
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int m = blockIdx.x;
+  const char* const in = static_cast<const char*>(g.in) +
+                         matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
+  char* const out = static_cast<char*>(g.out) +
+                    matrix_at(g.first + m, g.inner, g.out_outer, g.out_inner) * (DT ? 4 : 2);
+  constexpr int AHEAD = 8;                       // loads of a wave that are out at a time
+  f64x4 acc[2] = {};
+  for (int k0 = 16 * wave; k0 < g.l; k0 += 16 * WAVES * AHEAD) {
+    float x[AHEAD][4];
 #pragma unroll
-      for (int k = 0; k < SP / 4; ++k) {
-        load_n<DT, 4>(in, int64_t(4 * k + q) * g.in_ld + j, 4 * k + q < g.s ? end - j : 0, x[k]);
+    for (int u = 0; u < AHEAD; ++u) {
+      const int k = k0 + 16 * WAVES * u + 4 * q;
+      if constexpr (TALL) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) x[k][b] = ldexpf(x[k][b], expo);
-      }
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        f32x4 acc[4] = {};
-#pragma unroll
-        for (int k = 0; k < SP / 4; ++k) {
-          const float w = P[(4 * k + q) * PITCH + 16 * i + r];
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[k][b], w, acc[b], 0, 0, 0);
+        for (int e = 0; e < 4; ++e) {
+          float v[1];
+          load_n<DT, 1>(in, int64_t(k + e) * g.in_ld + r, k + e < g.l ? g.s - r : 0, v);
+          x[u][e] = v[0];
         }
-        const int row = 16 * i + r;
-        if (row < g.s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = j0 + 16 * q + 4 * e;
-            store_4<DT>(out, int64_t(row) * g.out_ld + at, end - at,
-                        f32x4{acc[0][e], acc[1][e], acc[2][e], acc[3][e]});
-          }
+      } else {
+        load_n<DT, 4>(in, int64_t(r) * g.in_ld + k, r < g.s ? g.l - k : 0, x[u]);
       }
-    } else {
-      float x[4][NB][4];
+    }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = j0 + 16 * b + r;
+    for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          load_n<DT, 4>(in, int64_t(j) * g.in_ld + 16 * k + 4 * q, j < end ? g.s - 16 * k - 4 * q : 0,
-                        x[b][k]);
+      for (int e = 0; e < 4; ++e)
+        acc[e & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[u][e], x[u][e], acc[e & 1], 0, 0, 0);
+  }
+  sums[wave][lane] = acc[0] + acc[1];
+  __syncthreads();
+  f64x4 A = sums[0][lane];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][k][e] = ldexpf(x[b][k][e], expo);
-        }
-      }
+  for (int w = 1; w < WAVES; ++w) A += sums[w][lane];
+  double trace = 0;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        f32x4 acc[4] = {};
+  for (int e = 0; e < 4; ++e) trace += 4 * e + q == r ? A[e] : 0.0;
+  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
+  const Norm norm(trace, R.eps);
+  f64x4 P;
 #pragma unroll
-        for (int k = 0; k < NB; ++k)
+  for (int e = 0; e < 4; ++e) {
+    A[e] = A[e] * norm.scale * norm.scale;
+    P[e] = 4 * e + q == r ? 1.0 : 0.0;
+  }
+  auto product = [](const f64x4& X, const f64x4& Y) {
+    f64x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+    s0 = __builtin_amdgcn_mfma_f64_16x16x4f64(X[0], Y[0], s0, 0, 0, 0);
+    s1 = __builtin_amdgcn_mfma_f64_16x16x4f64(X[1], Y[1], s1, 0, 0, 0);
+    s0 = __builtin_amdgcn_mfma_f64_16x16x4f64(X[2], Y[2], s0, 0, 0, 0);
+    s1 = __builtin_amdgcn_mfma_f64_16x16x4f64(X[3], Y[3], s1, 0, 0, 0);
+    return s0 + s1;
+  };
+  for (int n = 0; n < R.n; ++n) {
+    const double a = R.abc[3 * n], b = R.abc[3 * n + 1], c = R.abc[3 * n + 2];
+    const f64x4 C = product(A, A);
+    f64x4 Q;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = P[(16 * k + 4 * q + e) * PITCH + 16 * i + r];
+    for (int e = 0; e < 4; ++e) Q[e] = (4 * e + q == r ? a : 0.0) + b * A[e] + c * C[e];
+    P = n == 0 ? Q : product(Q, P);
+    if (n + 1 == R.n) break;
+    A = product(Q, product(Q, A));
+  }
+  if (wave == 0) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, x[b][k][e], acc[b], 0, 0, 0);
-          }
-        const int row = 16 * i + 4 * q;
+    for (int e = 0; e < 4; ++e) {
+      float v = float(P[e] * norm.p_scale);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int j = j0 + 16 * b + r;
-          if (j < end) store_4<DT>(out, int64_t(j) * g.out_ld + row, g.s - row, acc[b]);
-        }
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t w = pack_bf16x2(v, 0.f);
+        parts[(k * SP + 4 * e + q) * PITCH + r] = uint16_t(w);
+        v -= __uint_as_float(w << 16);
       }
     }
   }
+  __syncthreads();
+  result_part<DT, TALL, SP, WAVES>(g, in, out, parts, norm.x_expo, norm.out_expo, 0, g.l, wave, lane);
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -404,6 +774,7 @@ __global__ __launch_bounds__(256) void result_kernel(const StackArgs g, int chun
 struct Sizes {
   int s, l, sp;
   int64_t count, batch;
+  bool whole;                                    // in one launch
   int splits, span;
   size_t gram, p, expo, scratch;                 // bytes of a batch
   size_t total() const { return gram + p + expo + scratch; }
@@ -421,6 +792,7 @@ Sizes sizes_of(int64_t count, int64_t rows, int64_t cols) {
   z.l = int(std::max(rows, cols));
   z.sp = z.s <= 16 ? 16 : z.s <= 32 ? 32 : z.s <= 64 ? 64 : 128;
   z.count = count;
+  z.whole = z.sp < 128 && (count >= 64 || z.l <= 1024);
   // pieces of the long side where there are few matrices, of at least 256 positions
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(1024 / count, z.l / 256));
   z.span = int(((z.l + want - 1) / want + 63) / 64 * 64);
@@ -431,29 +803,36 @@ Sizes sizes_of(int64_t count, int64_t rows, int64_t cols) {
   z.batch = std::min(z.batch, std::max<int64_t>(1, (int64_t(1) << 32) / z.l));   // and a launch's blocks
   auto pad = [](size_t b) { return (b + 255) & ~size_t(255); };
   z.gram = pad(size_t(z.batch) * z.splits * elems * 8);
-  z.p = pad(size_t(z.batch) * elems * 4);
-  z.expo = pad(size_t(z.batch) * 4);
+  z.p = pad(size_t(z.batch) * elems * 6);
+  z.expo = pad(size_t(z.batch) * 8);
   z.scratch = z.sp == 128 ? size_t(std::min<int64_t>(z.batch, kBlocks)) * 3 * elems * 8 : 0;
   return z;
 }
 
-template <int SP>
-void launch_rounds(const StackArgs& g, const Rounds& R, hipStream_t s) {
+template <int DT, bool TALL, int SP>
+void launch_all(const StackArgs& g, const Rounds& R, bool whole, hipStream_t s) {
+  if constexpr (SP == 16) {
+    if (whole) {
+      hipLaunchKernelGGL((narrow_kernel<DT, TALL>), dim3((unsigned)g.count), dim3(512), 0, s, g, R);
+      return;
+    }
+  } else if constexpr (SP <= 64) {
+    if (whole) {
+      hipLaunchKernelGGL((whole_kernel<DT, TALL, SP>), dim3((unsigned)g.count),
+                         dim3(WholeShape<SP>::WAVES * 64), 0, s, g, R);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((gram_kernel<DT, TALL, SP>), dim3((unsigned)(g.count * g.splits)), dim3(256), 0, s, g);
   const int blocks = SP == 128 ? std::min(g.count, kBlocks) : g.count;
   hipLaunchKernelGGL(rounds_kernel<SP>, dim3((unsigned)blocks), dim3(RoundShape<SP>::WAVES * 64), 0, s, g, R);
-}
-
-template <int DT, bool TALL, int SP>
-void launch_all(const StackArgs& g, const Rounds& R, hipStream_t s) {
-  hipLaunchKernelGGL((gram_kernel<DT, TALL, SP>), dim3((unsigned)(g.count * g.splits)), dim3(256), 0, s, g);
-  launch_rounds<SP>(g, R, s);
   const int chunk = int64_t(g.count) * g.l >= int64_t(1) << 20 ? 1024 : 256;
   const int chunks = (g.l + chunk - 1) / chunk;
   hipLaunchKernelGGL((result_kernel<DT, TALL, SP>), dim3((unsigned)(g.count * chunks)), dim3(256), 0, s, g,
                      chunks, chunk);
 }
 
-typedef void (*Launch)(const StackArgs&, const Rounds&, hipStream_t);
+typedef void (*Launch)(const StackArgs&, const Rounds&, bool, hipStream_t);
 template <int DT, bool TALL>
 Launch launch_for(int sp) {
   return sp == 16 ? launch_all<DT, TALL, 16> : sp == 32 ? launch_all<DT, TALL, 32>
@@ -561,7 +940,7 @@ int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* wo
     g.span = z.span;
     char* at = static_cast<char*>(workspace);
     g.gram = reinterpret_cast<double*>(at);
-    g.p = reinterpret_cast<float*>(at += z.gram);
+    g.p = reinterpret_cast<uint16_t*>(at += z.gram);
     g.expo = reinterpret_cast<int*>(at += z.p);
     g.scratch = reinterpret_cast<double*>(at += z.expo);
     Rounds R;
@@ -575,7 +954,7 @@ int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* wo
     for (int64_t first = 0; first < z.count; first += z.batch) {
       g.first = first;
       g.count = int(std::min(z.batch, z.count - first));
-      run(g, R, stream);
+      run(g, R, z.whole, stream);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess)
         return fail(MUON_ERR_HIP, "launch of an orthogonalisation kernel failed: %s", hipGetErrorString(err));
