@@ -179,10 +179,16 @@ def args():
     global _args
     if _args is None:
         try:
-            from . import _tensor_args as _args
+            from . import _tensor_args
         except ImportError as e:
             raise RuntimeError("_tensor_args.so is missing: build it with `python -m "
                                "orthogonalized_momentum_optimizer_amd.build`") from e
+        L = lib()
+        _tensor_args.bind(*(address_of(f) for f in (
+            L.muon_mx_quantize, L.muon_mx_dequantize, L.muon_mx_matmul,
+            L.muon_mx_matmul_workspace_size, L.muon_orthogonalize,
+            L.muon_orthogonalize_workspace_size, L.muon_last_error)))
+        _args = _tensor_args
     return _args
 
 

@@ -76,11 +76,14 @@ def build_args() -> None:
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("clang++")
     if not cxx:
         raise RuntimeError("no C++ compiler found: it is required to build _tensor_args.so")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-isystem", os.path.join(rocm, "include"),
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
           *[x for p in include_paths() for x in ("-isystem", p)],
           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, ARGS_SOURCE),
           "-o", ARGS_LIB + ".tmp", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_hip",
           f"-Wl,-rpath,{torch_lib}"])
     os.replace(ARGS_LIB + ".tmp", ARGS_LIB)
 

@@ -9,11 +9,16 @@
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <memory>
+#include <stdexcept>
 #include <vector>
 
 namespace {
@@ -244,6 +249,81 @@ PyObject* grad_norm(PyObject*, PyObject* args) {
   }
 }
 
+// ---- the library's functions that are called without a plan ----
+
+typedef int (*Quantize)(const void*, int64_t, int, uint64_t, void*);
+typedef int (*Dequantize)(const void*, const void*, int64_t, int64_t, void*, int, void*);
+typedef int (*Product)(const void*, const void*, const void*, const void*, int64_t, int64_t, int64_t, void*,
+                       int, void*, size_t, void*);
+typedef size_t (*ProductSize)(int64_t, int64_t, int64_t);
+typedef int (*Stacked)(const void*, const void*, void*, size_t, void*);
+typedef size_t (*StackedSize)(int64_t, int64_t, int64_t, int64_t);
+typedef const char* (*LastError)();
+
+struct Library {
+  Quantize quantize;
+  Dequantize dequantize;
+  Product product;
+  ProductSize product_size;
+  Stacked stacked;
+  StackedSize stacked_size;
+  LastError last_error;
+} library;
+
+// bind(quantize, dequantize, matmul, its workspace, orthogonalize, its workspace, last error): their
+// addresses, before any of the calls below.
+PyObject* bind(PyObject*, PyObject* args) {
+  unsigned long long f[7];
+  if (!PyArg_ParseTuple(args, "KKKKKKK", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6)) return nullptr;
+  library = {reinterpret_cast<Quantize>(f[0]),  reinterpret_cast<Dequantize>(f[1]),
+             reinterpret_cast<Product>(f[2]),   reinterpret_cast<ProductSize>(f[3]),
+             reinterpret_cast<Stacked>(f[4]),   reinterpret_cast<StackedSize>(f[5]),
+             reinterpret_cast<LastError>(f[6])};
+  Py_RETURN_NONE;
+}
+
+void* stream_of(const at::Device& device) {
+  return static_cast<void*>(c10::hip::getCurrentHIPStream(device.index()).stream());
+}
+
+// Why a call was not made: an argument that does not fit, or the library's status.
+struct Refused {
+  PyObject* type;
+  const char* text;
+};
+struct Failed {
+  int status;
+};
+
+void check(int status) {
+  if (status) throw Failed{status};
+}
+
+// What a native call returns to Python: f's result, the library's status as an int, or an error.
+template <typename F>
+PyObject* answer(F&& f) {
+  try {
+    return f();
+  } catch (const Refused& e) {
+    PyErr_SetString(e.type, e.text);
+  } catch (const Failed& e) {
+    return PyLong_FromLong(e.status);
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// Runs f without the interpreter's lock.
+template <typename F>
+auto unlocked(F&& f) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
+}
+
 // ---- microscaled 4-bit values (include/mx4.h) ----
 
 // muon_mx_source, for calls through an address.
@@ -284,87 +364,87 @@ bool rows_of(const at::Tensor& t, MxSource& s, bool& transposed) {
   return true;
 }
 
-// What a native call returns to Python for a refused argument; the text is the error's.
-PyObject* refuse(PyObject* type, const char* text) {
-  PyErr_SetString(type, text);
-  return nullptr;
+// A tensor as rows x cols, and the held form of that and of its transpose, codes and then scales in one
+// uint8 tensor (undefined where not asked for).
+struct Held {
+  int64_t rows = 0, cols = 0;
+  at::Tensor data, data_t;
+};
+
+// kinds: of each tensor 1: rows, 2: transposed, 3: both.
+void quantize(const at::Tensor* const* tensors, const char* kinds, Held* out, int64_t n, bool stochastic,
+              uint64_t seed) {
+  std::vector<MxSource> sources(n);
+  if (n == 0) return;
+  for (int64_t i = 0; i < n; ++i) {
+    const at::Tensor& t = *tensors[i];
+    if (!t.is_cuda() || t.layout() != at::kStrided)
+      throw Refused{PyExc_ValueError, "a CUDA tensor expected"};
+    if (dtype_code(t) != 0 && dtype_code(t) != 1)
+      throw Refused{PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32"};
+    if (t.device() != tensors[0]->device())
+      throw Refused{PyExc_ValueError, "all tensors must be on one device"};
+  }
+  const at::Device device = tensors[0]->device();
+  const c10::DeviceGuard guard(device);
+  for (int64_t i = 0; i < n; ++i) {
+    const at::Tensor& t = *tensors[i];
+    MxSource& s = sources[i];
+    bool turned = false;
+    if (t.is_neg() || !rows_of(t, s, turned))
+      throw Refused{PyExc_ValueError,
+                    "rows of the last dimension expected: a tensor with stride 1 there (or, in two "
+                    "dimensions, along the other) and one stride between rows"};
+    s.x = t.numel() ? t.const_data_ptr() : nullptr;
+    if (!s.x && t.numel()) throw Refused{PyExc_ValueError, "a tensor with memory expected"};
+    s.dtype = dtype_code(t);
+    s.codes = s.scales = s.codes_t = s.scales_t = nullptr;
+    if (s.rows > (int64_t(1) << 31) || s.cols > (int64_t(1) << 31))
+      throw Refused{PyExc_ValueError, "sides up to 2^31 - 256"};
+    const auto options = at::TensorOptions().dtype(at::kByte).device(device);
+    for (int k = 0; k < 2; ++k) {                // 0: as it is in memory, 1: the transpose of that
+      const bool of_t = (k == 1) != turned;
+      if (!(kinds[i] & (of_t ? 2 : 1))) continue;
+      const int64_t codes = k ? mx_codes(s.cols, s.rows) : mx_codes(s.rows, s.cols);
+      const at::Tensor d = at::empty({codes / 16 * 17}, options);
+      char* const p = static_cast<char*>(d.data_ptr());
+      (k ? s.codes_t : s.codes) = p;
+      (k ? s.scales_t : s.scales) = p ? p + codes : nullptr;
+      (of_t ? out[i].data_t : out[i].data) = d;
+    }
+    out[i].rows = turned ? s.cols : s.rows;
+    out[i].cols = turned ? s.rows : s.cols;
+  }
+  check(library.quantize(sources.data(), n, stochastic, seed, stream_of(device)));
 }
 
-// mx_quantize(function, tensors, results, stochastic, seed, stream) -> for each tensor (rows, cols,
-// data, data_t), rows x cols the matrix that it is as rows of its last dimension, data and data_t the
-// held form of that and of its transpose, codes and then scales in one uint8 tensor (None where
-// `results`, a bytes of 1: rows, 2: transposed, 3: both for each tensor, does not ask for it); or the
-// library's status.
+// mx_quantize(tensors, kinds, stochastic, seed) -> for each of a tuple of tensors (rows, cols, data,
+// data_t); or the library's status.
 PyObject* mx_quantize(PyObject*, PyObject* args) {
-  PyObject* tensors;
-  Buffer results;
-  unsigned long long function, seed, stream;
+  PyObject* tuple;
+  Buffer kinds;
+  unsigned long long seed;
   int stochastic;
-  if (!PyArg_ParseTuple(args, "KOy*pKK", &function, &tensors, &results.view, &stochastic, &seed,
-                        &stream))
+  if (!PyArg_ParseTuple(args, "O!y*pK", &PyTuple_Type, &tuple, &kinds.view, &stochastic, &seed))
     return nullptr;
-  if (!PyTuple_Check(tensors) || PyTuple_GET_SIZE(tensors) != results.view.len)
-    return refuse(PyExc_ValueError, "a tuple of tensors and a result kind for each expected");
-  const Py_ssize_t n = PyTuple_GET_SIZE(tensors);
-  const char* const kinds = static_cast<const char*>(results.view.buf);
-  try {
-    std::vector<MxSource> sources(n);
-    std::vector<at::Tensor> out(2 * n);
-    std::vector<bool> turned(n);
-    c10::OptionalDeviceGuard guard;
-    long device = -1;
+  return answer([&]() -> PyObject* {
+    const Py_ssize_t n = PyTuple_GET_SIZE(tuple);
+    if (n != kinds.view.len) throw Refused{PyExc_ValueError, "a kind for each tensor expected"};
+    std::vector<const at::Tensor*> tensors(n);
+    std::vector<Held> out(n);
     for (Py_ssize_t i = 0; i < n; ++i) {
-      PyObject* const o = PyTuple_GET_ITEM(tensors, i);
-      if (!THPVariable_Check(o)) return refuse(PyExc_TypeError, "a tensor expected");
-      const at::Tensor& t = THPVariable_Unpack(o);
-      if (!t.is_cuda() || t.layout() != at::kStrided)
-        return refuse(PyExc_ValueError, "a CUDA tensor expected");
-      if (dtype_code(t) != 0 && dtype_code(t) != 1)
-        return refuse(PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32");
-      if (device < 0) {
-        device = t.get_device();
-        guard.reset_device(t.device());
-      }
-      MxSource& s = sources[i];
-      bool transposed = false;
-      if (t.get_device() != device || t.is_neg() || !rows_of(t, s, transposed))
-        return refuse(PyExc_ValueError, t.get_device() != device
-                          ? "all tensors must be on one device"
-                          : "rows of the last dimension expected: a tensor with stride 1 there (or, in "
-                            "two dimensions, along the other) and one stride between rows");
-      s.x = t.numel() ? t.const_data_ptr() : nullptr;
-      if (!s.x && t.numel()) return refuse(PyExc_ValueError, "a tensor with memory expected");
-      s.dtype = dtype_code(t);
-      turned[i] = transposed;
-      s.codes = s.scales = s.codes_t = s.scales_t = nullptr;
-      if (s.rows > (int64_t(1) << 31) || s.cols > (int64_t(1) << 31))
-        return refuse(PyExc_ValueError, "sides up to 2^31 - 256");
-      const auto options = at::TensorOptions().dtype(at::kByte).device(t.device());
-      for (int k = 0; k < 2; ++k) {              // 0: as it is in memory, 1: the transpose of that
-        if (!(kinds[i] & ((k == 1) != transposed ? 2 : 1))) continue;
-        const int64_t codes = k ? mx_codes(s.cols, s.rows) : mx_codes(s.rows, s.cols);
-        at::Tensor& d = out[2 * i + ((k == 1) != transposed ? 1 : 0)];
-        d = at::empty({codes / 16 * 17}, options);
-        char* const p = static_cast<char*>(d.data_ptr());
-        (k ? s.codes_t : s.codes) = p;
-        (k ? s.scales_t : s.scales) = p ? p + codes : nullptr;
-      }
+      PyObject* const o = PyTuple_GET_ITEM(tuple, i);
+      if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, "a tensor expected"};
+      tensors[i] = &THPVariable_Unpack(o);
     }
-    typedef int (*Quantize)(const void*, int64_t, int, uint64_t, void*);
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<Quantize>(function)(sources.data(), n, stochastic, seed,
-                                                  reinterpret_cast<void*>(stream));
-    Py_END_ALLOW_THREADS
-    if (status) return PyLong_FromLong(status);
+    unlocked([&] {
+      quantize(tensors.data(), static_cast<const char*>(kinds.view.buf), out.data(), n, stochastic, seed);
+    });
     PyObject* const result = PyTuple_New(n);
     if (!result) return nullptr;
     for (Py_ssize_t i = 0; i < n; ++i) {
-      const MxSource& s = sources[i];
-      PyObject* const each =
-          Py_BuildValue("LLNN", (long long)(turned[i] ? s.cols : s.rows),
-                        (long long)(turned[i] ? s.rows : s.cols), THPVariable_Wrap(out[2 * i]),
-                        THPVariable_Wrap(out[2 * i + 1]));
+      PyObject* const each = Py_BuildValue("LLNN", (long long)out[i].rows, (long long)out[i].cols,
+                                           THPVariable_Wrap(out[i].data), THPVariable_Wrap(out[i].data_t));
       if (!each) {
         Py_DECREF(result);
         return nullptr;
@@ -372,90 +452,166 @@ PyObject* mx_quantize(PyObject*, PyObject* args) {
       PyTuple_SET_ITEM(result, i, each);
     }
     return result;
-  } catch (const std::exception& e) {
-    return refuse(PyExc_RuntimeError, e.what());
-  }
+  });
 }
 
-// The held form in `o`: a uint8 tensor of the size that rows x cols take. Null with an error set.
-const char* held(PyObject* o, int64_t rows, int64_t cols, at::Device* device) {
-  if (THPVariable_Check(o)) {
-    const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.is_cuda() && t.scalar_type() == at::kByte && t.is_contiguous() &&
-        t.numel() == mx_codes(rows, cols) / 16 * 17 && (!device->has_index() || t.device() == *device)) {
-      *device = t.device();
-      static const char empty = 0;
-      return t.numel() ? static_cast<const char*>(t.const_data_ptr()) : &empty;
-    }
-  }
-  PyErr_SetString(PyExc_ValueError, "held values of these sizes, on one device, expected");
-  return nullptr;
+// The held form of rows x cols values: a uint8 tensor of the size that they take. (An empty one's
+// address is not null.)
+const char* held(const at::Tensor& t, int64_t rows, int64_t cols) {
+  if (!t.defined() || !t.is_cuda() || t.scalar_type() != at::kByte || !t.is_contiguous() ||
+      t.numel() != mx_codes(rows, cols) / 16 * 17)
+    throw Refused{PyExc_ValueError, "held values of these sizes, on one device, expected"};
+  static const char empty = 0;
+  return t.numel() ? static_cast<const char*>(t.const_data_ptr()) : &empty;
+}
+
+const at::Tensor& tensor_of(PyObject* o) {
+  if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, "a tensor expected"};
+  return THPVariable_Unpack(o);
 }
 
 at::ScalarType out_type(int dtype) { return dtype ? at::kFloat : at::kBFloat16; }
 
-// mx_dequantize(function, data, rows, cols, dtype, stream) -> a rows x cols tensor, or the status.
+// mx_dequantize(data, rows, cols, dtype) -> a rows x cols tensor, or the status.
 PyObject* mx_dequantize(PyObject*, PyObject* args) {
   PyObject* data;
-  unsigned long long function, stream;
   long long rows, cols;
   int dtype;
-  if (!PyArg_ParseTuple(args, "KOLLiK", &function, &data, &rows, &cols, &dtype, &stream))
-    return nullptr;
-  try {
-    at::Device device(at::kCUDA);
-    const char* const p = held(data, rows, cols, &device);
-    if (!p) return nullptr;
-    const c10::DeviceGuard guard(device);
-    const at::Tensor out =
-        at::empty({rows, cols}, at::TensorOptions().dtype(out_type(dtype)).device(device));
-    typedef int (*Back)(const void*, const void*, int64_t, int64_t, void*, int, void*);
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<Back>(function)(p, p + mx_codes(rows, cols), rows, cols,
-                                              out.data_ptr(), dtype,
-                                              reinterpret_cast<void*>(stream));
-    Py_END_ALLOW_THREADS
-    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
-  } catch (const std::exception& e) {
-    return refuse(PyExc_RuntimeError, e.what());
-  }
+  if (!PyArg_ParseTuple(args, "OLLi", &data, &rows, &cols, &dtype)) return nullptr;
+  return answer([&]() -> PyObject* {
+    const at::Tensor& t = tensor_of(data);
+    const char* const p = held(t, rows, cols);
+    const at::Tensor out = unlocked([&] {
+      const c10::DeviceGuard guard(t.device());
+      at::Tensor out = at::empty({rows, cols}, at::TensorOptions().dtype(out_type(dtype)).device(t.device()));
+      check(library.dequantize(p, p + mx_codes(rows, cols), rows, cols, out.data_ptr(), dtype,
+                               stream_of(t.device())));
+      return out;
+    });
+    return THPVariable_Wrap(out);
+  });
 }
 
-// mx_matmul(function, workspace_size, a, b, m, n, k, dtype, stream) -> an m x n tensor, or the status.
+// a b^T of held m x k and n x k values.
+at::Tensor product(const at::Tensor& a, const at::Tensor& b, int64_t m, int64_t n, int64_t k, int dtype) {
+  const char *const p = held(a, m, k), *const q = held(b, n, k);
+  const at::Device device = a.device();
+  if (b.device() != device) throw Refused{PyExc_ValueError, "held values of these sizes, on one device, expected"};
+  const c10::DeviceGuard guard(device);
+  const at::Tensor out = at::empty({m, n}, at::TensorOptions().dtype(out_type(dtype)).device(device));
+  const size_t need = library.product_size(m, n, k);
+  at::Tensor ws;
+  if (need && need != SIZE_MAX)
+    ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(device));
+  check(library.product(p, p + mx_codes(m, k), q, q + mx_codes(n, k), m, n, k, out.data_ptr(), dtype,
+                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? need : 0, stream_of(device)));
+  return out;
+}
+
+// mx_matmul(a, b, m, n, k, dtype) -> an m x n tensor, or the status.
 PyObject* mx_matmul(PyObject*, PyObject* args) {
   PyObject *a, *b;
-  unsigned long long function, size, stream;
   long long m, n, k;
   int dtype;
-  if (!PyArg_ParseTuple(args, "KKOOLLLiK", &function, &size, &a, &b, &m, &n, &k, &dtype, &stream))
-    return nullptr;
-  try {
-    at::Device device(at::kCUDA);
-    const char* const p = held(a, m, k, &device);
-    const char* const q = p ? held(b, n, k, &device) : nullptr;
-    if (!q) return nullptr;
-    const c10::DeviceGuard guard(device);
-    const at::Tensor out =
-        at::empty({m, n}, at::TensorOptions().dtype(out_type(dtype)).device(device));
-    typedef size_t (*Size)(int64_t, int64_t, int64_t);
-    const size_t need = reinterpret_cast<Size>(size)(m, n, k);
-    at::Tensor ws;
-    if (need && need != SIZE_MAX)
-      ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(device));
-    typedef int (*Product)(const void*, const void*, const void*, const void*, int64_t, int64_t,
-                           int64_t, void*, int, void*, size_t, void*);
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<Product>(function)(
-        p, p + mx_codes(m, k), q, q + mx_codes(n, k), m, n, k, out.data_ptr(), dtype,
-        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? need : 0,
-        reinterpret_cast<void*>(stream));
-    Py_END_ALLOW_THREADS
-    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
-  } catch (const std::exception& e) {
-    return refuse(PyExc_RuntimeError, e.what());
+  if (!PyArg_ParseTuple(args, "OOLLLi", &a, &b, &m, &n, &k, &dtype)) return nullptr;
+  return answer([&]() -> PyObject* {
+    const at::Tensor &ta = tensor_of(a), &tb = tensor_of(b);
+    return THPVariable_Wrap(unlocked([&] { return product(ta, tb, m, n, k, dtype); }));
+  });
+}
+
+// A linear layer: y = Q(x) Q(w)^T; dx = Q(dy) Q(w^T)^T; dw = Q(dy^T) Q(x^T)^T. Between the passes it
+// keeps x and w in 4 bits. (As a Python function its two passes take 101 us of host time, 49 of them
+// PyTorch's own for any such function.)
+struct LinearCall {
+  at::Tensor rows, cols;                         // the weight as held, or undefined
+  bool need_x, need_w, stochastic;
+  int64_t seed;
+};
+
+class Linear : public torch::autograd::Function<Linear> {
+ public:
+  static at::Tensor forward(torch::autograd::AutogradContext* ctx, const at::Tensor& x, const at::Tensor& w,
+                            const LinearCall& call) {
+    const int64_t o = w.size(0);
+    Held h[2];
+    const at::Tensor* const tensors[2] = {&x, &w};
+    const char kinds[2] = {char(call.need_w ? 3 : 1), char(call.need_x ? 3 : 1)};
+    const bool own = !call.rows.defined();
+    quantize(tensors, kinds, h, own ? 2 : 1, false, 0);
+    const Held& hx = h[0];
+    const at::Tensor y = product(hx.data, own ? h[1].data : call.rows, hx.rows, o, hx.cols, dtype_code(x));
+    ctx->save_for_backward({call.need_w ? hx.data_t : at::Tensor(),
+                            !call.need_x ? at::Tensor() : own ? h[1].data_t : call.cols});
+    ctx->saved_data["sizes"] = std::vector<int64_t>{hx.rows, hx.cols, o};
+    ctx->saved_data["shape"] = x.sizes().vec();
+    ctx->saved_data["how"] = std::vector<int64_t>{dtype_code(x), dtype_code(w), call.stochastic, call.seed};
+    if (x.dim() == 2) return y;
+    std::vector<int64_t> shape = x.sizes().vec();
+    shape.back() = o;
+    return y.view(shape);
   }
+
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads) {
+    try {
+      return both(ctx, grads[0]);
+    } catch (const Refused& e) {
+      throw std::runtime_error(e.text);
+    } catch (const Failed&) {
+      throw std::runtime_error(library.last_error());
+    }
+  }
+
+ private:
+  static torch::autograd::variable_list both(torch::autograd::AutogradContext* ctx, const at::Tensor& grad) {
+    const auto saved = ctx->get_saved_variables();
+    const auto sizes = ctx->saved_data["sizes"].toIntVector();
+    const auto how = ctx->saved_data["how"].toIntVector();
+    const int64_t t = sizes[0], i = sizes[1], o = sizes[2];
+    const bool need_x = saved[1].defined() && ctx->needs_input_grad(0);
+    const bool need_w = saved[0].defined() && ctx->needs_input_grad(1);
+    at::Tensor dx, dw;
+    if (need_x || need_w) {
+      const at::AutoGradMode no_grad(false);
+      // (an expanded gradient, of a sum say, has no memory of its own for each value)
+      const at::Tensor dy = grad.contiguous().view({t, o});
+      const at::Tensor* const tensor = &dy;
+      const char kind = char((need_x ? 1 : 0) | (need_w ? 2 : 0));
+      Held h;
+      quantize(&tensor, &kind, &h, 1, how[2], uint64_t(how[3]));
+      if (need_x) dx = product(h.data, saved[1], t, i, o, int(how[0])).view(ctx->saved_data["shape"].toIntVector());
+      if (need_w) dw = product(h.data_t, saved[0], o, i, t, int(how[1]));
+    }
+    torch::autograd::variable_list out = {dx, dw};
+    if (at::GradMode::is_enabled() && grad.requires_grad()) {
+      // results of a pass that is itself recorded: what would differentiate them raises
+      const auto error = std::make_shared<torch::autograd::DelayedError>(
+          "mx4_linear is differentiable once", int(out.size()));
+      for (auto& v : out)
+        if (v.defined()) v.requires_grad_(true);
+      out = (*error)(std::move(out));
+    }
+    out.emplace_back();
+    return out;
+  }
+};
+
+// mx_linear(x, weight, rows, cols, stochastic, seed) -> y, or the status. rows, cols: the weight and its
+// transpose as held, or None.
+PyObject* mx_linear(PyObject*, PyObject* args) {
+  PyObject *x, *w, *rows, *cols;
+  int stochastic;
+  long long seed;
+  if (!PyArg_ParseTuple(args, "OOOOpL", &x, &w, &rows, &cols, &stochastic, &seed)) return nullptr;
+  return answer([&]() -> PyObject* {
+    const at::Tensor &tx = tensor_of(x), &tw = tensor_of(w);
+    const bool grad = at::GradMode::is_enabled();
+    LinearCall call{rows == Py_None ? at::Tensor() : tensor_of(rows),
+                    cols == Py_None ? at::Tensor() : tensor_of(cols),
+                    grad && tx.requires_grad(), grad && tw.requires_grad(), bool(stochastic), seed};
+    return THPVariable_Wrap(unlocked([&] { return Linear::apply(tx, tw, call); }));
+  });
 }
 
 // ---- orthogonalisation of stacks (include/orthogonalize.h) ----
@@ -469,25 +625,20 @@ struct Stack {
   int dtype;
 };
 
-// orthogonalize(function, workspace_size, x, out, cfg, stream) -> out (a new tensor in x's order of
-// strides where it is None), or the status. x: at least 2-D, its leading dimensions two strides at
-// most.
+// orthogonalize(x, out, cfg) -> out (a new tensor in x's order of strides where it is None), or the
+// status. x: at least 2-D, its leading dimensions two strides at most.
 PyObject* orthogonalize(PyObject*, PyObject* args) {
   PyObject *xo, *oo;
   Buffer cfg;
-  unsigned long long function, size, stream;
-  if (!PyArg_ParseTuple(args, "KKOOy*K", &function, &size, &xo, &oo, &cfg.view, &stream))
-    return nullptr;
-  if (!THPVariable_Check(xo) || (oo != Py_None && !THPVariable_Check(oo)))
-    return refuse(PyExc_TypeError, "tensors expected");
-  try {
-    const at::Tensor& x = THPVariable_Unpack(xo);
+  if (!PyArg_ParseTuple(args, "OOy*", &xo, &oo, &cfg.view)) return nullptr;
+  return answer([&]() -> PyObject* {
+    const at::Tensor& x = tensor_of(xo);
     if (!x.is_cuda() || x.layout() != at::kStrided || x.is_neg())
-      return refuse(PyExc_ValueError, "a CUDA tensor whose memory holds its values expected");
+      throw Refused{PyExc_ValueError, "a CUDA tensor whose memory holds its values expected"};
     if (dtype_code(x) != 0 && dtype_code(x) != 1)
-      return refuse(PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32");
+      throw Refused{PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32"};
     const int64_t d = x.dim();
-    if (d < 2) return refuse(PyExc_ValueError, "a matrix or a stack of them expected");
+    if (d < 2) throw Refused{PyExc_ValueError, "a matrix or a stack of them expected"};
     const c10::DeviceGuard guard(x.device());
     at::Tensor out;
     if (oo == Py_None) {                         // dense, dimensions in x's order of strides
@@ -504,10 +655,10 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
       }
       out = at::empty_strided(x.sizes(), strides, x.options().requires_grad(false));
     } else {
-      out = THPVariable_Unpack(oo);
+      out = tensor_of(oo);
       if (out.device() != x.device() || out.scalar_type() != x.scalar_type() ||
           out.sizes() != x.sizes() || out.layout() != at::kStrided || out.is_neg())
-        return refuse(PyExc_ValueError, "out must be a tensor of x's shape, dtype and device");
+        throw Refused{PyExc_ValueError, "out must be a tensor of x's shape, dtype and device"};
     }
     Stack k{};
     k.dtype = dtype_code(x);
@@ -524,8 +675,7 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
         sides[groups - 1] *= n;
         continue;
       }
-      if (groups == 2)
-        return refuse(PyExc_ValueError, "leading dimensions of more than two strides");
+      if (groups == 2) throw Refused{PyExc_ValueError, "leading dimensions of more than two strides"};
       sides[groups] = n;
       si[groups] = x.stride(i);
       so[groups] = out.stride(i);
@@ -539,21 +689,16 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
       k.in_stride[2 + j] = x.stride(d - 2 + j);
       k.out_stride[2 + j] = out.stride(d - 2 + j);
     }
-    typedef size_t (*Size)(int64_t, int64_t, int64_t, int64_t);
-    const size_t need = reinterpret_cast<Size>(size)(k.side[0], k.side[1], k.side[2], k.side[3]);
-    at::Tensor ws;
-    if (need && need != SIZE_MAX)
-      ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(x.device()));
-    typedef int (*Run)(const void*, const void*, void*, size_t, void*);
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = reinterpret_cast<Run>(function)(&k, cfg.view.buf, ws.defined() ? ws.data_ptr() : nullptr,
-                                             ws.defined() ? need : 0, reinterpret_cast<void*>(stream));
-    Py_END_ALLOW_THREADS
-    return status ? PyLong_FromLong(status) : THPVariable_Wrap(out);
-  } catch (const std::exception& e) {
-    return refuse(PyExc_RuntimeError, e.what());
-  }
+    unlocked([&] {
+      const size_t need = library.stacked_size(k.side[0], k.side[1], k.side[2], k.side[3]);
+      at::Tensor ws;
+      if (need && need != SIZE_MAX)
+        ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(x.device()));
+      check(library.stacked(&k, cfg.view.buf, ws.defined() ? ws.data_ptr() : nullptr,
+                            ws.defined() ? need : 0, stream_of(x.device())));
+    });
+    return THPVariable_Wrap(out);
+  });
 }
 
 PyMethodDef methods[] = {
@@ -561,6 +706,8 @@ PyMethodDef methods[] = {
     {"mx_quantize", mx_quantize, METH_VARARGS, "muon_mx_quantize of tensors into new ones."},
     {"mx_dequantize", mx_dequantize, METH_VARARGS, "muon_mx_dequantize into a new tensor."},
     {"mx_matmul", mx_matmul, METH_VARARGS, "muon_mx_matmul into a new tensor."},
+    {"mx_linear", mx_linear, METH_VARARGS, "A linear layer of microscaled 4-bit products."},
+    {"bind", bind, METH_VARARGS, "The addresses of the library's functions."},
     {"addresses", addresses, METH_VARARGS, "Addresses of the tensors of a plan's layout."},
     {"entries_at", entries_at, METH_VARARGS, "Whether dicts hold tensors at these addresses."},
     {"adamw_step", adamw_step, METH_VARARGS, "muon_adamw_step over a list of gradients."},

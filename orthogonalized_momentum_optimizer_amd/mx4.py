@@ -12,29 +12,15 @@ hardware multiplies).
 """
 from __future__ import annotations
 
-import math
 from typing import Dict, Iterable, Optional, Tuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 from .adamw import _raw_stream
 from .optim import dtype_code
 
 _ROWS, _COLS, _BOTH = b"\1", b"\2", b"\3"
-_functions: Optional[Tuple[int, ...]] = None
-
-
-def _calls() -> Tuple[int, ...]:
-    """The addresses of the library's functions: quantize, dequantize, matmul, its workspace."""
-    global _functions
-    if _functions is None:
-        lib = L.lib()
-        _functions = tuple(L.address_of(f) for f in (
-            lib.muon_mx_quantize, lib.muon_mx_dequantize, lib.muon_mx_matmul,
-            lib.muon_mx_matmul_workspace_size))
-    return _functions
 
 
 class MX4Tensor:
@@ -98,24 +84,14 @@ class MX4Tensor:
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The values held, exactly, as bfloat16 or float32."""
-        out = L.args().mx_dequantize(_calls()[1], self.data, self.rows, self.cols, dtype_code(dtype),
-                                     _stream_of(self.data))
+        out = L.args().mx_dequantize(self.data, self.rows, self.cols, dtype_code(dtype))
         if type(out) is int:
             L.raise_status(out)
         return out if len(self.shape) == 2 else out.view(self.shape)
 
 
-def _stream_of(t) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("a tensor expected")
-    if not t.is_cuda:
-        raise ValueError("a CUDA tensor expected")
-    return _raw_stream(t.device.index)
-
-
 def _quantize(tensors: tuple, results: bytes, stochastic: bool, seed: int):
-    out = L.args().mx_quantize(_calls()[0], tensors, results, stochastic, seed & (2 ** 64 - 1),
-                               _stream_of(tensors[0]))
+    out = L.args().mx_quantize(tensors, results, stochastic, seed & (2 ** 64 - 1))
     if type(out) is int:
         L.raise_status(out)
     return out
@@ -139,14 +115,6 @@ def mx4_quantize_both(x: torch.Tensor, *, stochastic: bool = False,
             MX4Tensor._of(turned, cols, rows, torch.Size((cols, rows))))
 
 
-def _product(a: torch.Tensor, b: torch.Tensor, m: int, n: int, k: int, dtype: int) -> torch.Tensor:
-    calls = _calls()
-    out = L.args().mx_matmul(calls[2], calls[3], a, b, m, n, k, dtype, _stream_of(a))
-    if type(out) is int:
-        L.raise_status(out)
-    return out
-
-
 def mx4_matmul(a: MX4Tensor, b: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a b^T, along the last dimension of both: summed in float32 and rounded once to ``out_dtype``
     (bfloat16 or float32). The result has a's leading dimensions and b's rows."""
@@ -154,48 +122,10 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, out_dtype: torch.dtype = torch.bfloat
         raise TypeError("two MX4Tensors expected")
     if a.cols != b.cols:
         raise ValueError(f"last dimensions differ: {a.cols} and {b.cols}")
-    out = _product(a.data, b.data, a.rows, b.rows, a.cols, dtype_code(out_dtype))
+    out = L.args().mx_matmul(a.data, b.data, a.rows, b.rows, a.cols, dtype_code(out_dtype))
+    if type(out) is int:
+        L.raise_status(out)
     return out if len(a.shape) == 2 else out.view(*a.shape[:-1], b.rows)
-
-
-class _Linear(torch.autograd.Function):
-    """y = Q(x) Q(w)^T; dx = Q(dy) Q(w^T)^T; dw = Q(dy^T) Q(x^T)^T. Between the passes the layer keeps
-    x and w in 4 bits."""
-
-    @staticmethod
-    def forward(ctx, x, weight, copies, stochastic, seed):
-        need_x, need_w = ctx.needs_input_grad[:2]
-        kinds = (3 if need_w else 1, 3 if need_x else 1)
-        if copies is None:
-            (t, i, xr, xc), (o, _, wr, wc) = _quantize((x, weight), bytes(kinds), False, 0)
-        else:
-            t, i, xr, xc = _quantize((x,), bytes(kinds[:1]), False, 0)[0]
-            o, wr, wc = copies[0].rows, copies[0].data, copies[1].data if need_x else None
-        y = _product(xr, wr, t, o, i, dtype_code(x.dtype))
-        ctx.save_for_backward(xc if need_w else None, wc if need_x else None)
-        ctx.sizes = t, i, o
-        ctx.x_shape, ctx.dtypes = x.shape, (x.dtype, weight.dtype)
-        ctx.how = stochastic, seed
-        return y if x.dim() == 2 else y.view(*x.shape[:-1], o)
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        need_x, need_w = ctx.needs_input_grad[:2]
-        if not (need_x or need_w):
-            return (None,) * 5
-        xc, wc = ctx.saved_tensors
-        t, i, o = ctx.sizes
-        # (an expanded gradient, of a sum say, has no memory of its own for each value)
-        dy = dy.contiguous()
-        kind = bytes(((1 if need_x else 0) | (2 if need_w else 0),))
-        _, _, dr, dc = _quantize((dy.view(t, o),), kind, *ctx.how)[0]
-        dx = dw = None
-        if need_x:
-            dx = _product(dr, wc, t, i, o, dtype_code(ctx.dtypes[0])).view(ctx.x_shape)
-        if need_w:
-            dw = _product(dc, xc, o, i, t, dtype_code(ctx.dtypes[1]))
-        return dx, dw, None, None, None
 
 
 def mx4_linear(x: torch.Tensor, weight: torch.Tensor,
@@ -218,7 +148,12 @@ def mx4_linear(x: torch.Tensor, weight: torch.Tensor,
             raise ValueError("copies of another shape than the weight's")
         if r.device != x.device or c.device != x.device:
             raise ValueError("copies on another device than x")
-    return _Linear.apply(x, weight, copies, bool(stochastic), int(seed))
+    rows, cols = (None, None) if copies is None else (copies[0].data, copies[1].data)
+    seed = int(seed) & (2 ** 64 - 1)
+    y = L.args().mx_linear(x, weight, rows, cols, bool(stochastic), seed - ((seed >> 63) << 64))
+    if type(y) is int:
+        L.raise_status(y)
+    return y
 
 
 class MX4Copies:

@@ -204,7 +204,6 @@ def zeropower_via_newtonschulz5(G: torch.Tensor, steps: int = 5, precision: str 
 
 
 _configs = {}
-_orthogonalize_calls = None
 
 
 def orthogonalize(x: torch.Tensor, steps: int = 5, abc=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
@@ -218,7 +217,6 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, abc=(3.4445, -4.7750, 2.0315)
     result has x's dtype and order of strides. ``out``: where it goes (x itself: in place).
     ``schedule``: None, or ``steps`` triples (a, b, c), one per round. Runs on the current stream and
     may be captured."""
-    global _orthogonalize_calls
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("a CUDA tensor expected")
     if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
@@ -232,12 +230,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, abc=(3.4445, -4.7750, 2.0315)
             cfg = _configs[key] = make_config(ns_steps=steps, abc=abc, eps=eps)
     else:
         cfg = make_config(ns_steps=steps, abc=abc, eps=eps, schedule=schedule)
-    if _orthogonalize_calls is None:
-        lib = L.lib()
-        _orthogonalize_calls = (L.address_of(lib.muon_orthogonalize),
-                                L.address_of(lib.muon_orthogonalize_workspace_size))
-    result = L.args().orthogonalize(*_orthogonalize_calls, x, out, cfg,
-                                    torch.cuda.current_stream(x.device).cuda_stream)
+    result = L.args().orthogonalize(x, out, cfg)
     if type(result) is int:
         L.raise_status(result)
     return result if out is None else out
