@@ -42,7 +42,7 @@ typedef struct {
 } muon_stack;
 
 /* Bytes of workspace (256-byte aligned, no initial contents required) that a stack of these
- * sizes needs: SIZE_MAX for sizes outside the limits (min(rows, cols) <= 128, max <= 2^24,
+ * sizes needs; 0: none. SIZE_MAX for sizes outside the limits (min(rows, cols) <= 128, max <= 2^24,
  * outer * inner <= 2^24). */
 size_t muon_orthogonalize_workspace_size(int64_t outer, int64_t inner, int64_t rows, int64_t cols);
 

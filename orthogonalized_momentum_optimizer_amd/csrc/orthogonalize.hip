@@ -44,7 +44,7 @@ struct StackArgs {
   double* gram;                                  // count x splits x SP x SP
   uint16_t* p;                                   // count x 3 x SP x SP: P in parts
   int* expo;                                     // count x 2: of two, for X and for the result
-  double* scratch;                               // SP = 128: kBlocks x 3 x SP x SP
+  double* scratch;                               // SP = 128: P, a held matrix for each of kBlocks
 };
 
 struct Rounds {
@@ -87,6 +87,36 @@ __device__ __forceinline__ void load_n(const void* base, int64_t i, int left, fl
     for (int k = 0; k < N; ++k) x[k] = k < left ? load_one<DT>(base, i + k) : 0.f;
   }
 }
+
+// The same N values as they lie in memory, all of them there: nothing is done to them before they are used, so
+// that many such loads are on their way at once (load_n's branches make each wait for the one before).
+template <int DT, int N>
+struct Raw {
+  static constexpr int W = N * (DT ? 4 : 2) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(W), aligned(DT ? 4 : 2)));
+  Words w;
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    w = *reinterpret_cast<const Words*>(static_cast<const char*>(base) + i * (DT ? 4 : 2));
+  }
+  __device__ __forceinline__ uint32_t word(int k) const {
+    if constexpr (W == 1) return w[0]; else return w[k];
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    if (DT) return __uint_as_float(word(k));
+    return __uint_as_float(k & 1 ? word(k / 2) & 0xffff0000u : word(k / 2) << 16);
+  }
+  // elements k of this and of a next one, packed (bf16)
+  __device__ __forceinline__ uint32_t pair(const Raw& next, int k) const {
+    return __builtin_amdgcn_perm(next.word(k / 2), word(k / 2), k & 1 ? 0x07060302u : 0x05040100u);
+  }
+};
+template <>
+struct Raw<0, 1> {
+  uint16_t w;
+  __device__ __forceinline__ void load(const void* base, int64_t i) { w = static_cast<const uint16_t*>(base)[i]; }
+  __device__ __forceinline__ float operator[](int) const { return __uint_as_float(uint32_t(w) << 16); }
+  __device__ __forceinline__ uint32_t pair(const Raw& next, int) const { return uint32_t(next.w) << 16 | w; }
+};
 
 template <int DT>
 __device__ __forceinline__ void store_4(void* base, int64_t i, int left, f32x4 v) {
@@ -215,6 +245,13 @@ struct GramValues<0, NB> {
   u32x4 x[NB];
 };
 
+// A lane's loads of a step, as they lie in memory.
+template <int DT, bool TALL, int NB>
+struct GramRaw {
+  static constexpr int V = DT ? 4 : 8;
+  Raw<DT, TALL ? NB : V> x[TALL ? V : NB];
+};
+
 template <int DT, bool TALL, int SP, int WAVES>
 __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, int begin, int end, int wave,
                                           int lane, double* lds) {
@@ -251,13 +288,7 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
       }
     }
   };
-  constexpr bool EARLY = SP < 128;               // (at 128 there are no registers for it)
-  GramValues<DT, NB> x, next;
-  int k0 = begin + STEP * wave;
-  if (EARLY) load(k0, x);
-  for (; k0 < end; k0 += STEP * WAVES) {
-    if (EARLY) load(k0 + STEP * WAVES, next);
-    else load(k0, x);
+  auto add = [&](const GramValues<DT, NB>& x) {
     if constexpr (DT == 0) {
 #pragma unroll
       for (int i = 0, u = 0; i < NB; ++i)
@@ -277,7 +308,64 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
           for (int i = 0; i <= j; ++i) mma_block(double(x.x[i][e]), d, acc[i * NB - i * (i - 1) / 2 + j - i]);
         }
     }
-    if (EARLY) x = next;
+  };
+  // Where a lane's loads are whole or not there at all they are made as whole ones, of a place that is
+  // there; the others value by value.
+  constexpr int V = STEP / 4;
+  const int steps = (end - begin + STEP - 1) / STEP;
+  const bool whole = !TALL || g.s % NB == 0;
+  const int fast = !whole ? 0 : TALL || (end - begin) % V == 0 ? steps : (end - begin) / STEP;
+  GramRaw<DT, TALL, NB> raw, next;
+  auto fetch = [&](int step, GramRaw<DT, TALL, NB>& to) {
+    const int k = begin + STEP * step + V * q;
+    if constexpr (TALL) {
+      const int at = NB * r < g.s ? NB * r : 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) to.x[e].load(base, int64_t(min(k + e, end - 1)) * g.in_ld + at);
+    } else {
+      const int at = min(k, end - V);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) to.x[b].load(base, int64_t(min(16 * b + r, g.s - 1)) * g.in_ld + at);
+    }
+  };
+  auto take = [&](int step, const GramRaw<DT, TALL, NB>& from, GramValues<DT, NB>& to) {
+    const int k = begin + STEP * step + V * q;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (TALL && DT) {
+          to.x[b][e] = NB * r < g.s && k + e < end ? from.x[e][b] : 0.f;
+        } else if constexpr (TALL) {
+          const uint32_t w = from.x[2 * e].pair(from.x[2 * e + 1], b);
+          to.x[b][e] = NB * r < g.s && k + 2 * e < end ? (k + 2 * e + 1 < end ? w : w & 0xffffu) : 0;
+        } else if constexpr (DT) {
+          to.x[b][e] = 16 * b + r < g.s && k < end ? from.x[b][e] : 0.f;
+        } else {
+          to.x[b][e] = 16 * b + r < g.s && k < end ? from.x[b].word(e) : 0;
+        }
+      }
+  };
+  GramValues<DT, NB> x;
+  int step = wave;
+  if constexpr (SP < 128) {
+    if (step < fast) fetch(step, raw);
+    for (; step < fast; step += WAVES) {
+      fetch(min(step + WAVES, fast - 1), next);
+      take(step, raw, x);
+      add(x);
+      raw = next;
+    }
+  } else {                                       // (at 128 there are no registers for the next values)
+    for (; step < fast; step += WAVES) {
+      fetch(step, raw);
+      take(step, raw, x);
+      add(x);
+    }
+  }
+  for (; step < steps; step += WAVES) {
+    load(begin + STEP * step, x);
+    add(x);
   }
   // the waves' sums, the upper half's to the lower half until one wave has them all
 #pragma unroll
@@ -353,35 +441,41 @@ struct Norm {
   }
 };
 
-// A block a matrix, in double. Every product is symmetric, so that a wave computes OWN of the
-// blocks of 16 x 16 on and above the diagonal and writes them twice: 10 of 16 blocks for SP = 64, by as many
-// waves, 36 of 64 for 128. A, Q, P and T = QA lie in LDS up to SP = 64; at 128 (a matrix is 128 KB) Q does,
-// and the others in the block's own scratch, in L2. A round has three parts with a barrier behind each:
-//   A A, written as Q;   Q P and Q A, written as T;   P is written, Q T, written as A.
-// No part writes what it or the part before reads in other waves.
-template <int SP>
+// A block a matrix, in double. Every matrix here is symmetric: of its blocks of 16 x 16 one of each pair
+// across the diagonal is computed and held, 10 of 16 for SP = 64 and 36 of 64 for 128, 17 doubles a row. Column
+// c has rows c, c + 1, .. (mod NB), NB / 2 + 1 of them for c < NB / 2, one fewer for the others, so that the right
+// operand is read and turned once for all of them; over four SIMDs a SIMD's share at SP = 64 is 3 blocks. A
+// column is one wave's, or where there are waves to spare two waves' (H = 2): one wave alone is given a 4x4x4
+// instruction every 30 cycles, two on a SIMD one every 17.
+// A and Q lie in LDS, P too up to SP = 64; at 128 P is in the block's own scratch, in L2. T = Q A takes the
+// place of A.
+template <int SP, int H>
 struct RoundShape {
-  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2, OWN = SP == 128 ? 3 : 1;
-  static constexpr int WAVES = BLOCKS / OWN;
-  static constexpr int PITCH = SP == 128 ? SP + 16 : SP + 4;
+  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2;
+  static constexpr int MOST = NB == 1 ? 1 : NB / 2 + 1;                // blocks of a column
+  static constexpr int OWN = (MOST + H - 1) / H;                       // and of a wave
+  static constexpr int WAVES = NB * H;
+  static constexpr int PITCH = 17, BLOCK = 16 * PITCH, HELD = BLOCKS * BLOCK;  // doubles
   static constexpr bool FAR = SP > 64;
-  static constexpr int LDS = (FAR ? 1 : 4) * SP * PITCH;               // doubles
+  static constexpr int LDS = (FAR ? 2 : 3) * HELD;
 };
 
-template <int SP>
+template <int SP, int H>
 struct RoundBlocks {
-  static constexpr int OWN = RoundShape<SP>::OWN;
-  int row0[OWN], col0[OWN];                      // of this wave's blocks
+  using S = RoundShape<SP, H>;
+  static constexpr int NB = S::NB, OWN = S::OWN;
+  int c, first;                                  // this wave's column, and its first row there less c
+  int own;                                       // blocks: OWN, one fewer or none
+  bool full;                                     // OWN
   int r, q;
   __device__ __forceinline__ RoundBlocks(int wave, int lane) : r(lane & 15), q(lane >> 4) {
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-      int u = wave * OWN + o, i = 0;
-      while (u >= RoundShape<SP>::NB - i) u -= RoundShape<SP>::NB - i++;
-      row0[o] = 16 * i;
-      col0[o] = 16 * (i + u);
-    }
+    c = wave % NB;
+    const int h = wave / NB, all = S::MOST - (NB > 1 && c >= NB / 2 ? 1 : 0), lower = (all + H - 1) / H;
+    first = h == 0 ? 0 : lower;
+    own = h == 0 ? lower : h < H ? all - lower : 0;
+    full = own == OWN;
   }
+  __device__ __forceinline__ int row_of(int o) const { return (c + first + o) % NB; }
   // f(o, e, row, column) for the elements that this thread holds of a product
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
@@ -389,128 +483,207 @@ struct RoundBlocks {
     asm volatile("" : "+v"(lane_r));             // (else every place's address stays in a register: spills at 128)
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
+      if (o + 1 < OWN || full)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f(o, e, row0[o] + block_row(lane_r, q), col0[o] + block_col(lane_r, e));
+        for (int e = 0; e < 4; ++e)
+          f(o, e, 16 * row_of(o) + block_row(lane_r, q), 16 * c + block_col(lane_r, e));
   }
-  // f(at, value) for the element and, outside the diagonal blocks, its mirror image
-  template <typename T>
-  __device__ __forceinline__ void put(T* M, int pitch, int row, int col, T v) const {
-    M[uint32_t(row * pitch + col)] = v;
-    if (row / 16 != col / 16) M[uint32_t(col * pitch + row)] = v;
+  // f(o, e, place) for the same elements, in a held matrix: block (c + d, c) is number d NB + c
+  template <typename F>
+  __device__ __forceinline__ void held(F&& f) const {
+    int lane_r = r;
+    asm volatile("" : "+v"(lane_r));
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+      if (o + 1 < OWN || full)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f(o, e, ((first + o) * NB + c) * S::BLOCK + block_row(lane_r, q) * S::PITCH + block_col(lane_r, e));
   }
 };
 
-// The rounds on c, this wave's blocks of the Gram matrix; p receives its blocks of P. lds: LDS doubles;
-// scratch: 3 SP SP doubles at SP = 128; trace_of: SP doubles of LDS.
-template <int SP>
-__device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<SP>& B, int lane, double* lds,
-                                            double* scratch, double* trace_of,
-                                            f64x4 (&c)[RoundShape<SP>::OWN], f64x4 (&p)[RoundShape<SP>::OWN]) {
-  using S = RoundShape<SP>;
-  constexpr int OWN = S::OWN;
-  constexpr bool FAR = S::FAR;
-  constexpr int P1 = S::PITCH, P2 = FAR ? SP : S::PITCH;
-  double* const Q = lds;
-  double* const A = FAR ? scratch : lds + SP * P1;
-  double* const P = A + SP * P2;
-  double* const T = P + SP * P2;
-  const int r = B.r, q = B.q;
+// The operands of N steps from step 4 k + t0: lane l's of step 4 k + t is element (16 k + 4 t + l / 16,
+// 16 j + l % 16) of a held matrix, d = k - j (mod NB): in block (k, j), or turned in block (j, k).
+template <int SP, int H, int N>
+__device__ __forceinline__ void read_steps(const double* M, int d, int k, int t0, int j, int r, int q,
+                                           double (&v)[N]) {
+  using S = RoundShape<SP, H>;
+  constexpr int NB = S::NB;
+  const bool turned = 2 * d > NB || (2 * d == NB && j >= NB / 2);
+  const int at = (turned ? k : j) * S::BLOCK + (turned ? r * S::PITCH + q : q * S::PITCH + r);
+  const double* const from = M + uint32_t(at);
+  const int block = (turned ? NB - d : d) * NB * S::BLOCK, step = turned ? 4 : 4 * S::PITCH;
+#pragma unroll
+  for (int t = 0; t < N; ++t) v[t] = from[block + step * (t0 + t)];
+}
 
-  // AHEAD steps' operands are read before the first of them is used.
-  constexpr int AHEAD = SP < 32 ? 4 : 8;
-  auto product = [&](const double* X, int px, const double* Y, int py, f64x4 (&acc)[OWN]) {
+// acc = X Y, OWN of this wave's blocks. The next N steps' operands are read while these are multiplied. The
+// matrix cores' double products share the vector units, so that every other vector instruction here costs
+// their time: at 64, wave c goes through the blocks of k from c, and with that where a block's place and turn
+// are a constant's the reads take no address of their own.
+template <int SP, int H, int OWN>
+__device__ __forceinline__ void round_product(const RoundBlocks<SP, H>& B, const double* X, const double* Y,
+                                              f64x4* acc) {
+  constexpr int NB = SP / 16, N = SP == 128 ? 2 : 4, GROUPS = 4 * NB / N;
+  struct Operands {
+    double a[OWN][N], b[N];
+  } v[2];
+  auto read = [&](int n, Operands& to) {
+    const int d = n * N / 4, k = (B.c + d) % NB, t0 = n * N % 4;
+    read_steps<SP, H>(Y, d, k, t0, B.c, B.r, B.q, to.b);
 #pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-      acc[o] = f64x4{0, 0, 0, 0};
-      uint32_t x = q * px + B.row0[o] + r, y = q * py + B.col0[o] + r;
-#pragma unroll 1
-      for (int k = 0; k < SP; k += 4 * AHEAD) {
-        double a[AHEAD], b[AHEAD];
+    for (int o = 0; o < OWN; ++o)
+      read_steps<SP, H>(X, (d + 2 * NB - (H > 1 ? B.first : 0) - o) % NB, k, t0, B.row_of(o), B.r, B.q, to.a[o]);
+  };
+  auto add = [&](const Operands& from) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          a[u] = X[x + uint32_t(4 * u * px)];
-          b[u] = Y[y + uint32_t(4 * u * py)];
-        }
-        x += 4 * AHEAD * px;
-        y += 4 * AHEAD * py;
+    for (int t = 0; t < N; ++t) {
+      const Turns d(from.b[t]);
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) mma_block(a[u], Turns(b[u]), acc[o]);
-      }
+      for (int o = 0; o < OWN; ++o) mma_block(from.a[o][t], d, acc[o]);
     }
   };
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) acc[o] = f64x4{0, 0, 0, 0};
+  read(0, v[0]);
+  if constexpr (GROUPS == 1) {
+    add(v[0]);
+  } else if constexpr (GROUPS <= 4) {
+#pragma unroll
+    for (int n = 0; n < GROUPS; ++n) {
+      if (n + 1 < GROUPS) read(n + 1, v[(n + 1) & 1]);
+      add(v[n & 1]);
+    }
+  } else {
+    // (else the reads of a later group become, together with these, reads at the top of the loop)
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      asm volatile("" : "+v"(v[0].b[t]));
+#pragma unroll
+      for (int o = 0; o < OWN; ++o) asm volatile("" : "+v"(v[0].a[o][t]));
+    }
+#pragma unroll 1
+    for (int n = 0; n < GROUPS; n += 2) {
+      read(n + 1, v[1]);
+      add(v[0]);
+      read((n + 2) % GROUPS, v[0]);
+      add(v[1]);
+    }
+  }
+}
 
-  B.each([&](int o, int e, int row, int col) {
-    if (row == col) trace_of[row] = c[o][e];
-  });
+// The rounds on c, this wave's blocks of the Gram matrix; p receives its blocks of P. lds: LDS doubles;
+// scratch: HELD doubles at SP = 128; trace_of: SP doubles of LDS. Waves beyond WAVES only wait.
+template <int SP, int H>
+__device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<SP, H>& B, int lane, double* lds,
+                                            double* scratch, double* trace_of,
+                                            f64x4 (&c)[RoundShape<SP, H>::OWN], f64x4 (&p)[RoundShape<SP, H>::OWN]) {
+  using S = RoundShape<SP, H>;
+  constexpr int OWN = S::OWN;
+  double* const Q = lds;
+  double* const A = lds + S::HELD;
+  double* const P = S::FAR ? scratch : lds + 2 * S::HELD;
+  const bool works = B.own > 0;
+  auto product = [&](const double* X, const double* Y, f64x4 (&acc)[OWN]) {
+    if (B.full) round_product<SP, H, OWN>(B, X, Y, acc);
+    else round_product<SP, H, (OWN > 1 ? OWN - 1 : 1)>(B, X, Y, acc);
+  };
+  if (works)
+    B.each([&](int o, int e, int row, int col) {
+      if (row == col) trace_of[row] = c[o][e];
+    });
   __syncthreads();
   double trace = 0;                              // the same in every wave
   for (int i = lane; i < SP; i += 64) trace += trace_of[i];
   for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
   const Norm norm(trace, R.eps);
-  B.each([&](int o, int e, int row, int col) {
-    B.put(A, P2, row, col, c[o][e] * norm.scale * norm.scale);
-    p[o][e] = row == col ? 1.0 : 0.0;
-  });
+  if (works) {
+    B.held([&](int o, int e, int at) {
+      c[o][e] = c[o][e] * norm.scale * norm.scale;
+      A[at] = c[o][e];
+    });
+    B.each([&](int o, int e, int row, int col) { p[o][e] = row == col ? 1.0 : 0.0; });
+  }
   __syncthreads();
   for (int n = 0; n < R.n; ++n) {
     const double a = R.abc[3 * n], b = R.abc[3 * n + 1], cc = R.abc[3 * n + 2];
-    product(A, P2, A, P2, c);
-    B.each([&](int o, int e, int row, int col) {
-      const double v = (row == col ? a : 0.0) + b * A[uint32_t(row * P2 + col)] + cc * c[o][e];
-      B.put(Q, P1, row, col, v);
-      if (n == 0) p[o][e] = v;
-    });
+    const bool last = n + 1 == R.n;
+    if (works) {
+      f64x4 sq[OWN];
+      product(A, A, sq);
+      B.each([&](int o, int e, int row, int col) {
+        sq[o][e] = (row == col ? a : 0.0) + b * c[o][e] + cc * sq[o][e];
+      });
+      B.held([&](int o, int e, int at) {
+        Q[at] = sq[o][e];
+        if (n == 0) p[o][e] = sq[o][e];
+      });
+    }
     __syncthreads();
-    if (n > 0) product(Q, P1, P, P2, p);
-    if (n + 1 == R.n) break;
-    product(Q, P1, A, P2, c);
-    B.each([&](int o, int e, int row, int col) { B.put(T, P2, row, col, c[o][e]); });
+    if (works) {
+      if (n > 0) product(Q, P, p);
+      if (!last) product(Q, A, c);
+    }
+    if (last) break;
+    __syncthreads();                             // A and P are read
+    if (works)
+      B.held([&](int o, int e, int at) {
+        A[at] = c[o][e];
+        P[at] = p[o][e];
+      });
     __syncthreads();
-    B.each([&](int o, int e, int row, int col) { B.put(P, P2, row, col, p[o][e]); });
-    product(Q, P1, T, P2, c);
-    B.each([&](int o, int e, int row, int col) { B.put(A, P2, row, col, c[o][e]); });
+    if (works) product(Q, A, c);
+    __syncthreads();                             // and T
+    if (works) B.held([&](int o, int e, int at) { A[at] = c[o][e]; });
     __syncthreads();
   }
   return norm;
 }
 
 // P in three bf16 parts, element (i, j) of part k at (k SP + i) pitch + j.
-template <int SP>
-__device__ __forceinline__ void put_parts(const RoundBlocks<SP>& B, const Norm& norm,
-                                          const f64x4 (&p)[RoundShape<SP>::OWN], uint16_t* out, int pitch) {
+template <int SP, int H>
+__device__ __forceinline__ void put_parts(const RoundBlocks<SP, H>& B, const Norm& norm,
+                                          const f64x4 (&p)[RoundShape<SP, H>::OWN], uint16_t* out, int pitch) {
   B.each([&](int o, int e, int row, int col) {
     float v = float(p[o][e] * norm.p_scale);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const uint32_t w = pack_bf16x2(v, 0.f);
-      B.put(out + k * SP * pitch, pitch, row, col, uint16_t(w));
+      uint16_t* const to = out + k * SP * pitch;
+      to[uint32_t(row * pitch + col)] = uint16_t(w);
+      if (B.first + o > 0) to[uint32_t(col * pitch + row)] = uint16_t(w);
       v -= __uint_as_float(w << 16);
     }
   });
 }
 
+// Of the rounds alone: H, and threads of a block.
+constexpr int halves(int sp) { return sp == 32 ? 2 : 1; }
+constexpr int round_threads(int sp) { return sp / 16 * halves(sp) * 64; }
+
 template <int SP>
-__global__ __launch_bounds__(RoundShape<SP>::WAVES * 64, 1) void rounds_kernel(const StackArgs g,
-                                                                              const Rounds R) {
-  using S = RoundShape<SP>;
+__global__ __launch_bounds__(round_threads(SP), 1) void rounds_kernel(const StackArgs g, const Rounds R) {
+  constexpr int H = halves(SP);
+  using S = RoundShape<SP, H>;
   __shared__ double lds[S::LDS];
   __shared__ double trace_of[SP];
   const int t = threadIdx.x, lane = t & 63;
-  const RoundBlocks<SP> B(__builtin_amdgcn_readfirstlane(t >> 6), lane);
+  const RoundBlocks<SP, H> B(__builtin_amdgcn_readfirstlane(t >> 6), lane);
   for (int m = blockIdx.x; m < g.count; m += gridDim.x) {
     const double* const part = g.gram + int64_t(m) * g.splits * (SP * SP);
     f64x4 c[S::OWN], p[S::OWN];
-    B.each([&](int o, int e, int row, int col) { c[o][e] = part[row * SP + col]; });
-#pragma unroll 4
-    for (int z = 1; z < g.splits; ++z)           // (all elements of a part are on their way at once)
-      B.each([&](int o, int e, int row, int col) { c[o][e] += part[z * (SP * SP) + row * SP + col]; });
-    const Norm norm = rounds_part<SP>(R, B, lane, lds, g.scratch + int64_t(blockIdx.x) * 3 * SP * SP, trace_of,
+    if (B.own > 0) {
+      B.each([&](int o, int e, int row, int col) { c[o][e] = part[row * SP + col]; });
+      for (int z = 1; z < g.splits; ++z)         // (all elements of a part are on their way at once)
+        B.each([&](int o, int e, int row, int col) { c[o][e] += part[z * (SP * SP) + row * SP + col]; });
+    }
+    const Norm norm = rounds_part<SP, H>(R, B, lane, lds, g.scratch + int64_t(blockIdx.x) * S::HELD, trace_of,
                                       c, p);
     if (t == 0) {
       g.expo[2 * m] = norm.x_expo;
       g.expo[2 * m + 1] = norm.out_expo;
     }
-    put_parts<SP>(B, norm, p, g.p + int64_t(m) * 3 * SP * SP, SP);
+    if (B.own > 0) put_parts<SP, H>(B, norm, p, g.p + int64_t(m) * 3 * SP * SP, SP);
     __syncthreads();
   }
 }
@@ -537,13 +710,34 @@ __device__ __forceinline__ void result_part(const StackArgs& g, const char* in, 
   constexpr int NB = SP / 16, KS = SP < 32 ? 1 : SP / 32, PARTS = DT ? 3 : 1, PITCH = ResultShape<SP>::PITCH;
   const int r = lane & 15, q = lane >> 4;
   const int turned = r / 4 + r % 4 * 4;
+  const bool whole = !TALL || g.s % 8 == 0;      // a lane's loads: whole or not there at all
   for (int j0 = begin + 64 * wave; j0 < end; j0 += 64 * WAVES) {
     f32x4 acc[NB][4] = {};
 #pragma unroll 1
     for (int k = 0; k < KS; ++k) {
       const int row = 32 * k + 8 * q;
       float v[8][4];
-      if constexpr (!TALL) {
+      if (whole && (TALL || j0 + 64 <= end || end % 4 == 0)) {
+        if constexpr (!TALL) {
+          const int j = j0 + 4 * turned;
+          Raw<DT, 4> w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e].load(in, int64_t(min(row + e, g.s - 1)) * g.in_ld + min(j, end - 4));
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) v[e][b] = row + e < g.s && j < end ? w[e][b] : 0.f;
+        } else {
+          Raw<DT, 8> w[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            w[b].load(in, int64_t(min(j0 + 16 * b + r, end - 1)) * g.in_ld + (row < g.s ? row : 0));
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e][b] = row < g.s && j0 + 16 * b + r < end ? w[b][e] : 0.f;
+        }
+      } else if constexpr (!TALL) {
         const int j = j0 + 4 * turned;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -637,28 +831,22 @@ __global__ __launch_bounds__(256, SP == 128 ? 1 : 2) void result_kernel(const St
 // ---- all of it in one launch -------------------------------------------------------------------
 //
 // Where there are enough matrices, or their long sides are short: a block a matrix, which it reads a second
-// time from the caches. fp32 1200 x 64 x 1600: 665 to 703 us, in three launches 719 to 843 (gram 243, rounds
-// 260, result 230); bf16 1200 x 64 x 1600: 485 and 592; bf16 144 x 64 x 768: 68 and 77 us; 1 x 16 x 768: 15
-// and 21. Of bf16 144 x 64 x 768 the rounds take 42 us (10.4 each, 2.6 a product), which the matrix cores'
-// double rate bounds at 1.3: a wave also turns its operands (6 of 10 issue slots) and waits for LDS.
+// time from the caches. fp32 1200 x 64 x 1600: 492 us (2.0 TB/s), in three launches 679; bf16 288 and 418; bf16
+// 144 x 64 x 768: 55 and 68 us; fp32 1 x 16 x 768: 15 and 17. Four waves, so that two matrices share a
+// compute unit, or eight where there is one at most: 1200 x 64 x 1600 493 and 546 us, 144 x 64 x 768 57 and 55.
+// Of those 55 us the rounds take 37 (7.3 each, 1.8 a product of 64^3, which the matrix cores bound at 1.3).
 
-template <int SP>
-struct WholeShape {
-  static constexpr int WAVES = SP == 32 ? 4 : RoundShape<SP>::WAVES;
-  static constexpr int LDS = RoundShape<SP>::LDS;
-};
-
-template <int DT, bool TALL, int SP>
-__global__ __launch_bounds__(WholeShape<SP>::WAVES * 64, 1) void whole_kernel(const StackArgs g,
-                                                                             const Rounds R) {
-  using S = RoundShape<SP>;
-  constexpr int WAVES = WholeShape<SP>::WAVES;
-  static_assert(3 * SP * ResultShape<SP>::PITCH * 2 <= S::LDS * 8 && GramShape<SP, WAVES>::LDS <= S::LDS,
-                "P's parts and the sums fit");
-  __shared__ double lds[S::LDS];                 // sums, then the rounds' matrices, then P's parts
+template <int DT, bool TALL, int SP, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void whole_kernel(const StackArgs g,
+                                                                              const Rounds R) {
+  constexpr int H = halves(SP);
+  using S = RoundShape<SP, H>;
+  constexpr int SUMS = GramShape<SP, WAVES>::LDS;
+  static_assert(3 * SP * ResultShape<SP>::PITCH * 2 <= S::LDS * 8 && S::WAVES <= WAVES, "P's parts fit");
+  __shared__ double lds[SUMS > S::LDS ? SUMS : S::LDS];  // sums, then the rounds' matrices, then P's parts
   __shared__ double trace_of[SP];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const RoundBlocks<SP> B(min(wave, S::WAVES - 1), lane);
+  const RoundBlocks<SP, H> B(wave, lane);
   const int m = blockIdx.x;
   const char* const in = static_cast<const char*>(g.in) +
                          matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
@@ -666,14 +854,14 @@ __global__ __launch_bounds__(WholeShape<SP>::WAVES * 64, 1) void whole_kernel(co
                     matrix_at(g.first + m, g.inner, g.out_outer, g.out_inner) * (DT ? 4 : 2);
   gram_part<DT, TALL, SP, WAVES>(g, in, 0, g.l, wave, lane, lds);
   f64x4 c[S::OWN], p[S::OWN];
-  B.each([&](int o, int e, int row, int col) {
-    c[o][e] = gram_held<TALL, SP>(row, col) ? lds[row * SP + col] : lds[col * SP + row];
-  });
-  // (a wave beyond the blocks does the last one again: it writes the same values to the same places)
-  const Norm norm = rounds_part<SP>(R, B, lane, lds, nullptr, trace_of, c, p);
+  if (B.own > 0)
+    B.each([&](int o, int e, int row, int col) {
+      c[o][e] = gram_held<TALL, SP>(row, col) ? lds[row * SP + col] : lds[col * SP + row];
+    });
+  const Norm norm = rounds_part<SP, H>(R, B, lane, lds, nullptr, trace_of, c, p);
   __syncthreads();
   uint16_t* const parts = reinterpret_cast<uint16_t*>(lds);
-  put_parts<SP>(B, norm, p, parts, ResultShape<SP>::PITCH);
+  if (B.own > 0) put_parts<SP, H>(B, norm, p, parts, ResultShape<SP>::PITCH);
   __syncthreads();
   result_part<DT, TALL, SP, WAVES>(g, in, out, parts, norm.x_expo, norm.out_expo, 0, g.l, wave, lane);
 }
@@ -699,17 +887,31 @@ __global__ __launch_bounds__(512) void narrow_kernel(const StackArgs g, const Ro
   f64x4 acc[2] = {};
   for (int k0 = 16 * wave; k0 < g.l; k0 += 16 * WAVES * AHEAD) {
     float x[AHEAD][4];
+    if (TALL || g.l % 4 == 0) {
+      Raw<DT, TALL ? 1 : 4> w[AHEAD][TALL ? 4 : 1];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int k = k0 + 16 * WAVES * u + 4 * q;
-      if constexpr (TALL) {
+      for (int u = 0; u < AHEAD; ++u) {
+        const int k = k0 + 16 * WAVES * u + 4 * q;
+        if constexpr (TALL) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[u][e].load(in, int64_t(min(k + e, g.l - 1)) * g.in_ld + min(r, g.s - 1));
+        } else {
+          w[u][0].load(in, int64_t(min(r, g.s - 1)) * g.in_ld + min(k, g.l - 4));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v[1];
-          load_n<DT, 1>(in, int64_t(k + e) * g.in_ld + r, k + e < g.l ? g.s - r : 0, v);
-          x[u][e] = v[0];
+          const int k = k0 + 16 * WAVES * u + 4 * q + e;
+          float v;
+          if constexpr (TALL) v = w[u][e][0]; else v = w[u][0][e];
+          x[u][e] = r < g.s && k < g.l ? v : 0.f;
         }
-      } else {
+    } else {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int k = k0 + 16 * WAVES * u + 4 * q;
         load_n<DT, 4>(in, int64_t(r) * g.in_ld + k, r < g.s ? g.l - k : 0, x[u]);
       }
     }
@@ -793,6 +995,13 @@ Sizes sizes_of(int64_t count, int64_t rows, int64_t cols) {
   z.sp = z.s <= 16 ? 16 : z.s <= 32 ? 32 : z.s <= 64 ? 64 : 128;
   z.count = count;
   z.whole = z.sp < 128 && (count >= 64 || z.l <= 1024);
+  if (z.whole) {                                 // in the kernel's own memory
+    z.batch = std::min<int64_t>(count, int64_t(1) << 20);
+    z.splits = 1;
+    z.span = z.l;
+    z.gram = z.p = z.expo = z.scratch = 0;
+    return z;
+  }
   // pieces of the long side where there are few matrices, of at least 256 positions
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(1024 / count, z.l / 256));
   z.span = int(((z.l + want - 1) / want + 63) / 64 * 64);
@@ -805,7 +1014,7 @@ Sizes sizes_of(int64_t count, int64_t rows, int64_t cols) {
   z.gram = pad(size_t(z.batch) * z.splits * elems * 8);
   z.p = pad(size_t(z.batch) * elems * 6);
   z.expo = pad(size_t(z.batch) * 8);
-  z.scratch = z.sp == 128 ? size_t(std::min<int64_t>(z.batch, kBlocks)) * 3 * elems * 8 : 0;
+  z.scratch = z.sp == 128 ? size_t(std::min<int64_t>(z.batch, kBlocks)) * RoundShape<128, 1>::HELD * 8 : 0;
   return z;
 }
 
@@ -818,14 +1027,16 @@ void launch_all(const StackArgs& g, const Rounds& R, bool whole, hipStream_t s) 
     }
   } else if constexpr (SP <= 64) {
     if (whole) {
-      hipLaunchKernelGGL((whole_kernel<DT, TALL, SP>), dim3((unsigned)g.count),
-                         dim3(WholeShape<SP>::WAVES * 64), 0, s, g, R);
+      if (g.count > kBlocks)
+        hipLaunchKernelGGL((whole_kernel<DT, TALL, SP, 4>), dim3((unsigned)g.count), dim3(256), 0, s, g, R);
+      else
+        hipLaunchKernelGGL((whole_kernel<DT, TALL, SP, 8>), dim3((unsigned)g.count), dim3(512), 0, s, g, R);
       return;
     }
   }
   hipLaunchKernelGGL((gram_kernel<DT, TALL, SP>), dim3((unsigned)(g.count * g.splits)), dim3(256), 0, s, g);
   const int blocks = SP == 128 ? std::min(g.count, kBlocks) : g.count;
-  hipLaunchKernelGGL(rounds_kernel<SP>, dim3((unsigned)blocks), dim3(RoundShape<SP>::WAVES * 64), 0, s, g, R);
+  hipLaunchKernelGGL((rounds_kernel<SP>), dim3((unsigned)blocks), dim3(round_threads(SP)), 0, s, g, R);
   const int chunk = int64_t(g.count) * g.l >= int64_t(1) << 20 ? 1024 : 256;
   const int chunks = (g.l + chunk - 1) / chunk;
   hipLaunchKernelGGL((result_kernel<DT, TALL, SP>), dim3((unsigned)(g.count * chunks)), dim3(256), 0, s, g,
@@ -909,13 +1120,15 @@ int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* wo
     if (!distinct(k, k.out_stride))
       return fail(MUON_ERR_INVALID_ARG, "two elements of out share a place");
     const Sizes z = sizes_of(k.outer * k.inner, k.rows, k.cols);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < z.total())
+    if (z.total() > 0 &&
+        (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < z.total()))
       return fail(MUON_ERR_WORKSPACE, "a workspace of %zu bytes, 256-byte aligned, is needed", z.total());
     auto range = [](const void* p, size_t bytes, bool written) {
       const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
       return Range{lo, lo + bytes, written};
     };
-    std::vector<Range> rs = {range(k.out, size_t(out_elems) * e, true), range(workspace, z.total(), true)};
+    std::vector<Range> rs = {range(k.out, size_t(out_elems) * e, true)};
+    if (z.total() > 0) rs.push_back(range(workspace, z.total(), true));
     if (k.in != k.out || !std::equal(k.in_stride, k.in_stride + 4, k.out_stride))
       rs.push_back(range(k.in, size_t(in_elems) * e, false));
     if (int st = check_overlaps(rs)) return st;
