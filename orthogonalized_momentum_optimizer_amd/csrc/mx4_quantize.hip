@@ -477,6 +477,10 @@ int muon_mx_dequantize(const void* codes, const void* scales, int64_t rows, int6
     if (!mx_sides_ok(rows, cols))
       return fail(MUON_ERR_UNSUPPORTED, "sides up to 2^31 - 256 and 2^40 values");
     if (rows == 0 || cols == 0) return MUON_OK;
+    const int64_t steps = mx_steps(cols), tiles = mx_panels(rows) * steps;
+    const int64_t blocks = (tiles + 3) / 4;
+    if (blocks > kMostTiles)
+      return fail(MUON_ERR_UNSUPPORTED, "more than 2^25 tiles of 16 x 128");
     const size_t e = dtype_bytes(dtype);
     if (!codes || !scales || !is_aligned16(codes) || !is_aligned16(scales))
       return fail(MUON_ERR_INVALID_ARG, "codes and scales must be non-NULL and 16-byte aligned");
@@ -486,10 +490,6 @@ int muon_mx_dequantize(const void* codes, const void* scales, int64_t rows, int6
                              mx_range(scales, muon_mx_scales_size(rows, cols), false),
                              mx_range(out, size_t(rows) * size_t(cols) * e, true)};
     if (int st = check_overlaps(rs)) return st;
-    const int64_t steps = mx_steps(cols), tiles = mx_panels(rows) * steps;
-    const int64_t blocks = (tiles + 3) / 4;
-    if (blocks > kMostTiles)
-      return fail(MUON_ERR_UNSUPPORTED, "more than 2^25 tiles of 16 x 128");
     auto kernel = dtype == MUON_DT_F32 ? mx_dequantize_kernel<1> : mx_dequantize_kernel<0>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream,
                        static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales),

@@ -697,6 +697,8 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
       check(library.stacked(&k, cfg.view.buf, ws.defined() ? ws.data_ptr() : nullptr,
                             ws.defined() ? need : 0, stream_of(x.device())));
     });
+    // (what autograd saved of the result's tensor before is not its value any more)
+    if (oo != Py_None && !out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
     return THPVariable_Wrap(out);
   });
 }

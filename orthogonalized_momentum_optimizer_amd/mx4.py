@@ -135,13 +135,17 @@ def mx4_linear(x: torch.Tensor, weight: torch.Tensor,
     and weight (outputs, inputs), bfloat16 or float32. The result has x's dtype, gradients those of
     x and weight. ``copies``: the weight and its transpose as held (``MX4Copies``), else the
     weight is quantised in this call. Values are rounded to nearest; ``stochastic``: but the incoming
-    gradients stochastically, with the random bits of ``seed`` (give another for every step and layer)."""
+    gradients stochastically, with the random bits of ``seed`` (give another for every step and layer; a
+    captured pass repeats its own). As with any layer, let go of what an eager pass left of the graph of
+    these leaves before a backward pass is captured. Differentiable once."""
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
         raise TypeError("x and weight must be tensors")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError(f"x (.., inputs) and weight (outputs, inputs) expected, got {tuple(x.shape)} "
                          f"and {tuple(weight.shape)}")
     dtype_code(x.dtype), dtype_code(weight.dtype)
+    if not x.is_cuda or weight.device != x.device:
+        raise ValueError("x and weight must be on one CUDA device")
     if copies is not None:
         r, c = copies
         if (r.rows, r.cols) != tuple(weight.shape) or (c.cols, c.rows) != tuple(weight.shape):
