@@ -197,6 +197,7 @@ __device__ __forceinline__ double row_rotate(double x) {
 // x of the lanes 0, 4, 8 and 12 further on in each 16.
 struct Turns {
   double v[4];
+  Turns() = default;
   __device__ __forceinline__ explicit Turns(double x)
       : v{x, row_rotate<0x12C>(x), row_rotate<0x128>(x), row_rotate<0x124>(x)} {}
 };
@@ -231,9 +232,7 @@ __device__ __forceinline__ bool gram_held(int i, int j) {
 template <int SP, int WAVES>
 struct GramShape {
   static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2, HALF = (WAVES + 1) / 2;
-  // what a wave passes on at a time: all its blocks, or at 128 a sixth of them
-  static constexpr int PASS = SP == 128 ? 6 : BLOCKS;
-  static constexpr int LDS = (WAVES / 2) * PASS * 256 > SP * SP ? (WAVES / 2) * PASS * 256 : SP * SP;
+  static constexpr int LDS = (WAVES / 2) * BLOCKS * 256 > SP * SP ? (WAVES / 2) * BLOCKS * 256 : SP * SP;
 };
 
 template <int DT, int NB>
@@ -252,22 +251,27 @@ struct GramRaw {
   Raw<DT, TALL ? NB : V> x[TALL ? V : NB];
 };
 
-template <int DT, bool TALL, int SP, int WAVES>
-__device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, int begin, int end, int wave,
-                                          int lane, double* lds) {
-  using S = GramShape<SP, WAVES>;
-  constexpr int NB = SP / 16, STEP = DT ? 16 : 32;
-  const int r = lane & 15, q = lane >> 4;
-  f64x4 acc[S::BLOCKS];                          // blocks i <= j, row by row
-#pragma unroll
-  for (int u = 0; u < S::BLOCKS; ++u) acc[u] = f64x4{0, 0, 0, 0};
-  auto load = [&](int k0, GramValues<DT, NB>& to) {
-    const int k = k0 + STEP / 4 * q;
+// The loads of a block's positions begin .. end - 1. Where a lane's loads of a step are whole or not there at all
+// (the first `fast` steps) they are made as whole ones, of a place that is there; the others value by value.
+template <int DT, bool TALL, int SP>
+struct GramLoads {
+  static constexpr int NB = SP / 16, STEP = DT ? 16 : 32, V = STEP / 4;
+  const char* base;
+  int64_t ld;
+  int s, begin, end, r, q;
+  int steps, fast;
+  __device__ __forceinline__ GramLoads(const StackArgs& g, const char* base, int begin, int end, int lane)
+      : base(base), ld(g.in_ld), s(g.s), begin(begin), end(end), r(lane & 15), q(lane >> 4) {
+    steps = (end - begin + STEP - 1) / STEP;
+    fast = TALL && s % NB != 0 ? 0 : TALL || (end - begin) % V == 0 ? steps : (end - begin) / STEP;
+  }
+  __device__ __forceinline__ void load(int step, GramValues<DT, NB>& to) const {
+    const int k = begin + STEP * step + V * q;
     if constexpr (TALL) {
-      float v[STEP / 4][NB];
+      float v[V][NB];
 #pragma unroll
-      for (int e = 0; e < STEP / 4; ++e)
-        load_n<DT, NB>(base, int64_t(k + e) * g.in_ld + NB * r, k + e < end ? g.s - NB * r : 0, v[e]);
+      for (int e = 0; e < V; ++e)
+        load_n<DT, NB>(base, int64_t(k + e) * ld + NB * r, k + e < end ? s - NB * r : 0, v[e]);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -278,8 +282,8 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
     } else {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float v[STEP / 4];
-        load_n<DT, STEP / 4>(base, int64_t(16 * b + r) * g.in_ld + k, 16 * b + r < g.s ? end - k : 0, v);
+        float v[V];
+        load_n<DT, V>(base, int64_t(16 * b + r) * ld + k, 16 * b + r < s ? end - k : 0, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (DT) to.x[b][e] = v[e];
@@ -287,8 +291,67 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
         }
       }
     }
-  };
-  auto add = [&](const GramValues<DT, NB>& x) {
+  }
+  __device__ __forceinline__ void fetch(int step, GramRaw<DT, TALL, NB>& to) const {
+    const int k = begin + STEP * step + V * q;
+    if constexpr (TALL) {
+      const int at = NB * r < s ? NB * r : 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) to.x[e].load(base, int64_t(min(k + e, end - 1)) * ld + at);
+    } else {
+      const int at = min(k, end - V);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) to.x[b].load(base, int64_t(min(16 * b + r, s - 1)) * ld + at);
+    }
+  }
+  __device__ __forceinline__ void take(int step, const GramRaw<DT, TALL, NB>& from, GramValues<DT, NB>& to) const {
+    const int k = begin + STEP * step + V * q;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (TALL && DT) {
+          to.x[b][e] = NB * r < s && k + e < end ? from.x[e][b] : 0.f;
+        } else if constexpr (TALL) {
+          const uint32_t w = from.x[2 * e].pair(from.x[2 * e + 1], b);
+          to.x[b][e] = NB * r < s && k + 2 * e < end ? (k + 2 * e + 1 < end ? w : w & 0xffffu) : 0;
+        } else if constexpr (DT) {
+          to.x[b][e] = 16 * b + r < s && k < end ? from.x[b][e] : 0.f;
+        } else {
+          to.x[b][e] = 16 * b + r < s && k < end ? from.x[b].word(e) : 0;
+        }
+      }
+  }
+  // add(values) for steps first, first + by, ..
+  template <typename F>
+  __device__ __forceinline__ void each(int first, int by, F&& add) const {
+    GramRaw<DT, TALL, NB> raw, next;
+    GramValues<DT, NB> x;
+    int step = first;
+    if (step < fast) fetch(step, raw);
+    for (; step < fast; step += by) {
+      fetch(min(step + by, fast - 1), next);
+      take(step, raw, x);
+      add(x);
+      raw = next;
+    }
+    for (; step < steps; step += by) {
+      load(step, x);
+      add(x);
+    }
+  }
+};
+
+template <int DT, bool TALL, int SP, int WAVES>
+__device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, int begin, int end, int wave,
+                                          int lane, double* lds) {
+  using S = GramShape<SP, WAVES>;
+  constexpr int NB = SP / 16;
+  const int r = lane & 15, q = lane >> 4;
+  f64x4 acc[S::BLOCKS];                          // blocks i <= j, row by row
+#pragma unroll
+  for (int u = 0; u < S::BLOCKS; ++u) acc[u] = f64x4{0, 0, 0, 0};
+  GramLoads<DT, TALL, SP>(g, base, begin, end, lane).each(wave, WAVES, [&](const GramValues<DT, NB>& x) {
     if constexpr (DT == 0) {
 #pragma unroll
       for (int i = 0, u = 0; i < NB; ++i)
@@ -308,81 +371,20 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
           for (int i = 0; i <= j; ++i) mma_block(double(x.x[i][e]), d, acc[i * NB - i * (i - 1) / 2 + j - i]);
         }
     }
-  };
-  // Where a lane's loads are whole or not there at all they are made as whole ones, of a place that is
-  // there; the others value by value.
-  constexpr int V = STEP / 4;
-  const int steps = (end - begin + STEP - 1) / STEP;
-  const bool whole = !TALL || g.s % NB == 0;
-  const int fast = !whole ? 0 : TALL || (end - begin) % V == 0 ? steps : (end - begin) / STEP;
-  GramRaw<DT, TALL, NB> raw, next;
-  auto fetch = [&](int step, GramRaw<DT, TALL, NB>& to) {
-    const int k = begin + STEP * step + V * q;
-    if constexpr (TALL) {
-      const int at = NB * r < g.s ? NB * r : 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) to.x[e].load(base, int64_t(min(k + e, end - 1)) * g.in_ld + at);
-    } else {
-      const int at = min(k, end - V);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) to.x[b].load(base, int64_t(min(16 * b + r, g.s - 1)) * g.in_ld + at);
-    }
-  };
-  auto take = [&](int step, const GramRaw<DT, TALL, NB>& from, GramValues<DT, NB>& to) {
-    const int k = begin + STEP * step + V * q;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (TALL && DT) {
-          to.x[b][e] = NB * r < g.s && k + e < end ? from.x[e][b] : 0.f;
-        } else if constexpr (TALL) {
-          const uint32_t w = from.x[2 * e].pair(from.x[2 * e + 1], b);
-          to.x[b][e] = NB * r < g.s && k + 2 * e < end ? (k + 2 * e + 1 < end ? w : w & 0xffffu) : 0;
-        } else if constexpr (DT) {
-          to.x[b][e] = 16 * b + r < g.s && k < end ? from.x[b][e] : 0.f;
-        } else {
-          to.x[b][e] = 16 * b + r < g.s && k < end ? from.x[b].word(e) : 0;
-        }
-      }
-  };
-  GramValues<DT, NB> x;
-  int step = wave;
-  if constexpr (SP < 128) {
-    if (step < fast) fetch(step, raw);
-    for (; step < fast; step += WAVES) {
-      fetch(min(step + WAVES, fast - 1), next);
-      take(step, raw, x);
-      add(x);
-      raw = next;
-    }
-  } else {                                       // (at 128 there are no registers for the next values)
-    for (; step < fast; step += WAVES) {
-      fetch(step, raw);
-      take(step, raw, x);
-      add(x);
-    }
-  }
-  for (; step < steps; step += WAVES) {
-    load(begin + STEP * step, x);
-    add(x);
-  }
+  });
   // the waves' sums, the upper half's to the lower half until one wave has them all
 #pragma unroll
   for (int n = WAVES; n > 1; n = (n + 1) / 2) {
     const int half = (n + 1) / 2;
+    f64x4* const pass = reinterpret_cast<f64x4*>(lds) + lane;
+    if (wave >= half && wave < n)
 #pragma unroll
-    for (int u0 = 0; u0 < S::BLOCKS; u0 += S::PASS) {
-      f64x4* const pass = reinterpret_cast<f64x4*>(lds) + lane;
-      if (wave >= half && wave < n)
+      for (int u = 0; u < S::BLOCKS; ++u) pass[((wave - half) * S::BLOCKS + u) * 64] = acc[u];
+    __syncthreads();
+    if (wave < n - half)
 #pragma unroll
-        for (int u = 0; u < S::PASS; ++u) pass[((wave - half) * S::PASS + u) * 64] = acc[u0 + u];
-      __syncthreads();
-      if (wave < n - half)
-#pragma unroll
-        for (int u = 0; u < S::PASS; ++u) acc[u0 + u] += pass[(wave * S::PASS + u) * 64];
-      __syncthreads();
-    }
+      for (int u = 0; u < S::BLOCKS; ++u) acc[u] += pass[(wave * S::BLOCKS + u) * 64];
+    __syncthreads();
   }
   if (wave == 0) {
 #pragma unroll
@@ -398,20 +400,76 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
   __syncthreads();
 }
 
+// At 128 the 36 blocks are 288 registers, so that they are shared out: wave W of four goes through all positions (the
+// loads of the other waves come from the L1 cache) with the blocks of columns W and W + 4, rows c, c + 1, .. (mod 8).
+// Straight into `out`. fp32 300 x 128 x 1024: 155 us (all blocks in every wave, with spills: 237), which the matrix
+// cores bound at 72; bf16 58 (87).
+template <int DT, bool TALL, int W>
+__device__ __forceinline__ void gram_shared(const StackArgs& g, const char* base, int begin, int end, int lane,
+                                            double* out) {
+  constexpr int SP = 128, NB = 8;
+  f64x4 acc[9];
+#pragma unroll
+  for (int u = 0; u < 9; ++u) acc[u] = f64x4{0, 0, 0, 0};
+  GramLoads<DT, TALL, SP>(g, base, begin, end, lane).each(0, 1, [&](const GramValues<DT, NB>& x) {
+#pragma unroll
+    for (int u = 0; u < 9; ++u) {
+      if constexpr (DT == 0) {
+        const int j = u < 5 ? W : W + 4, i = (j + u % 5) % NB;
+        const f32x4 c = mma(x.x[i], x.x[j], f32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[u][e] += double(c[e]);
+      }
+    }
+    if constexpr (DT) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = W + 4 * h;
+          const Turns d(x.x[j][e]);
+#pragma unroll
+          for (int o = 0; o < 5 - h; ++o) mma_block(double(x.x[(j + o) % NB][e]), d, acc[5 * h + o]);
+        }
+    }
+  });
+  const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 9; ++u) {
+    const int j = u < 5 ? W : W + 4, i = (j + u % 5) % NB;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int a = DT ? block_row(r, q) : 4 * q + e, c = DT ? block_col(r, e) : r;
+      const int row = TALL ? NB * a + i : 16 * i + a, col = TALL ? NB * c + j : 16 * j + c;
+      out[row * SP + col] = acc[u][e];
+      if (i != j) out[col * SP + row] = acc[u][e];
+    }
+  }
+}
+
 // A part of a matrix's long side (grid: count * splits) into its own whole matrix.
 template <int DT, bool TALL, int SP>
-__global__ __launch_bounds__(256, 1) void gram_kernel(const StackArgs g) {
-  __shared__ double sum[GramShape<SP, 4>::LDS];
+__global__ __launch_bounds__(256, SP == 128 ? 2 : 1) void gram_kernel(const StackArgs g) {
   const int t = threadIdx.x;
   const int m = blockIdx.x / g.splits, z = blockIdx.x - m * g.splits;
   const char* const base = static_cast<const char*>(g.in) +
                            matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
   const int begin = z * g.span;
-  gram_part<DT, TALL, SP, 4>(g, base, begin, min(g.l, begin + g.span), t >> 6, t & 63, sum);
+  const int end = min(g.l, begin + g.span);
   double* const out = g.gram + int64_t(blockIdx.x) * (SP * SP);
-  for (int at = t; at < SP * SP; at += 256) {
-    const int i = at / SP, j = at % SP;
-    out[at] = gram_held<TALL, SP>(i, j) ? sum[at] : sum[j * SP + i];
+  if constexpr (SP == 128) {
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    if (wave == 0) gram_shared<DT, TALL, 0>(g, base, begin, end, t & 63, out);
+    else if (wave == 1) gram_shared<DT, TALL, 1>(g, base, begin, end, t & 63, out);
+    else if (wave == 2) gram_shared<DT, TALL, 2>(g, base, begin, end, t & 63, out);
+    else gram_shared<DT, TALL, 3>(g, base, begin, end, t & 63, out);
+  } else {
+    __shared__ double sum[GramShape<SP, 4>::LDS];
+    gram_part<DT, TALL, SP, 4>(g, base, begin, end, t >> 6, t & 63, sum);
+    for (int at = t; at < SP * SP; at += 256) {
+      const int i = at / SP, j = at % SP;
+      out[at] = gram_held<TALL, SP>(i, j) ? sum[at] : sum[j * SP + i];
+    }
   }
 }
 
@@ -519,8 +577,10 @@ __device__ __forceinline__ void read_steps(const double* M, int d, int k, int t0
 
 // acc = X Y, OWN of this wave's blocks. The next N steps' operands are read while these are multiplied. The
 // matrix cores' double products share the vector units, so that every other vector instruction here costs
-// their time: at 64, wave c goes through the blocks of k from c, and with that where a block's place and turn
-// are a constant's the reads take no address of their own.
+// their time. Wave c goes through the blocks of k from c: a block's number and turn are then constants, and reads
+// take no address of their own (at 128, rolled up and with addresses: 290 us a matrix for 211; all of it in code
+// twice, for waves of OWN and of fewer blocks, would not fit the instruction cache there, so that the last block
+// is a branch).
 template <int SP, int H, int OWN>
 __device__ __forceinline__ void round_product(const RoundBlocks<SP, H>& B, const double* X, const double* Y,
                                               f64x4* acc) {
@@ -528,47 +588,34 @@ __device__ __forceinline__ void round_product(const RoundBlocks<SP, H>& B, const
   struct Operands {
     double a[OWN][N], b[N];
   } v[2];
+  int r = B.r, q = B.q;
+  if (SP == 128) asm volatile("" : "+v"(r), "+v"(q));  // (else the addresses of all products stay in registers)
   auto read = [&](int n, Operands& to) {
     const int d = n * N / 4, k = (B.c + d) % NB, t0 = n * N % 4;
-    read_steps<SP, H>(Y, d, k, t0, B.c, B.r, B.q, to.b);
+    read_steps<SP, H>(Y, d, k, t0, B.c, r, q, to.b);
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
-      read_steps<SP, H>(X, (d + 2 * NB - (H > 1 ? B.first : 0) - o) % NB, k, t0, B.row_of(o), B.r, B.q, to.a[o]);
+      read_steps<SP, H>(X, (d + 2 * NB - (H > 1 ? B.first : 0) - o) % NB, k, t0, B.row_of(o), r, q, to.a[o]);
   };
   auto add = [&](const Operands& from) {
+    Turns d[N];
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      const Turns d(from.b[t]);
+      d[t] = Turns(from.b[t]);
 #pragma unroll
-      for (int o = 0; o < OWN; ++o) mma_block(from.a[o][t], d, acc[o]);
+      for (int o = 0; o < OWN - (SP == 128); ++o) mma_block(from.a[o][t], d[t], acc[o]);
     }
+    if (SP == 128 && B.full)
+#pragma unroll
+      for (int t = 0; t < N; ++t) mma_block(from.a[OWN - 1][t], d[t], acc[OWN - 1]);
   };
 #pragma unroll
   for (int o = 0; o < OWN; ++o) acc[o] = f64x4{0, 0, 0, 0};
   read(0, v[0]);
-  if constexpr (GROUPS == 1) {
-    add(v[0]);
-  } else if constexpr (GROUPS <= 4) {
 #pragma unroll
-    for (int n = 0; n < GROUPS; ++n) {
-      if (n + 1 < GROUPS) read(n + 1, v[(n + 1) & 1]);
-      add(v[n & 1]);
-    }
-  } else {
-    // (else the reads of a later group become, together with these, reads at the top of the loop)
-#pragma unroll
-    for (int t = 0; t < N; ++t) {
-      asm volatile("" : "+v"(v[0].b[t]));
-#pragma unroll
-      for (int o = 0; o < OWN; ++o) asm volatile("" : "+v"(v[0].a[o][t]));
-    }
-#pragma unroll 1
-    for (int n = 0; n < GROUPS; n += 2) {
-      read(n + 1, v[1]);
-      add(v[0]);
-      read((n + 2) % GROUPS, v[0]);
-      add(v[1]);
-    }
+  for (int n = 0; n < GROUPS; ++n) {
+    if (n + 1 < GROUPS) read(n + 1, v[(n + 1) & 1]);
+    add(v[n & 1]);
   }
 }
 
@@ -585,7 +632,7 @@ __device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<S
   double* const P = S::FAR ? scratch : lds + 2 * S::HELD;
   const bool works = B.own > 0;
   auto product = [&](const double* X, const double* Y, f64x4 (&acc)[OWN]) {
-    if (B.full) round_product<SP, H, OWN>(B, X, Y, acc);
+    if (SP == 128 || B.full) round_product<SP, H, OWN>(B, X, Y, acc);
     else round_product<SP, H, (OWN > 1 ? OWN - 1 : 1)>(B, X, Y, acc);
   };
   if (works)
