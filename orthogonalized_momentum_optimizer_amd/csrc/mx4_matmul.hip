@@ -90,7 +90,14 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int left, f32x4 v)
 // c ^ (r / 4 % 4), so that a fragment's 64 lanes read all banks alike. In a stage the two slices of
 // 64 columns are read in turn: while the matrix cores work on the first, the second's fragments
 // arrive; then a barrier for the next stage; while they work on the second, the loads of the stage
-// S ahead go out (into the buffer just read) and the next stage's first fragments arrive.
+// S ahead go out (into the buffer just read) and the next stage's first fragments arrive. Conditions
+// on the stage are the compiler's (whole stages, the last ones), or it moves products past the reads
+// (455 for 368 us below). Results leave through LDS as whole rows (368 for 325 us).
+//
+// bf16 out: 8192^3 245 us, 4.5 PFLOP/s; 16384 x 6400 x 6400 325 to 347, 3.9 to 4.1; 16384 x 6400 x 1600 103.
+// The matrix cores alone would take 165 us for 8192^3 (6.6 PFLOP/s, with data-like operands, where power
+// bounds them), without the loads it takes 222, without the stores 241. Tried: a stage's loads in two
+// halves, one a slice (2 to 5% slower).
 template <int WM, int WN, int S, int OUT>
 __device__ __forceinline__ void mx_tile(const MmArgs& g) {
   constexpr int TM = 64 * WM, TN = 64 * WN;
@@ -320,16 +327,17 @@ __global__ __launch_bounds__(256, WM * WN == 16 ? 1 : 2) void mx_matmul_kernel(c
 
 // ---- few rows ----------------------------------------------------------------------------------
 //
-// Where one side has at most 64 rows the other operand (X) is read once and nothing else takes time: a
+// Where one side has few rows the other operand (X) is read once and nothing else takes time: a
 // block takes one panel of it, its waves the steps in turn, straight from memory into the 16x16x128
-// instruction (a panel's step is a contiguous kilobyte, 16 bytes a lane), with up to four panels Y
+// instruction (a panel's step is a contiguous kilobyte, 16 bytes a lane), with one or two panels Y
 // of the short side, which stay in the caches. The waves' sums are added in LDS in their order. LEFT:
-// X is A. The operands' order puts four consecutive columns of out into a lane.
+// X is A. The operands' order puts four consecutive columns of out into a lane. One row x 6400 x 1600:
+// 4.0 us in the kernel, 4.6 with the call, of which a launch is 3.6; 16 x 12800 x 6400 13.3 us, 3.3 TB/s.
 template <int PANELS, int WAVES, bool LEFT, int OUT>
 __device__ __forceinline__ void mx_few_tile(const MmArgs& g) {
   __shared__ f32x4 sums[PANELS][WAVES][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int panels_x = LEFT ? g.panels_a : g.panels_b, panels_y = LEFT ? g.panels_b : g.panels_a;
+  const int panels_y = LEFT ? g.panels_b : g.panels_a;
   const uint8_t* const y = LEFT ? g.b : g.a;
   const uint8_t* const sy = LEFT ? g.sb : g.sa;
   // lane l: row l % 16, block l / 16
@@ -339,49 +347,47 @@ __device__ __forceinline__ void mx_few_tile(const MmArgs& g) {
   };
   auto wide = [](u32x4 v) { return i32x8{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0}; };
   constexpr int AHEAD = 4;                       // steps whose loads are out at a time
-  for (int panel = blockIdx.x; panel < panels_x; panel += gridDim.x) {
-    const uint8_t* const x = (LEFT ? g.a : g.b) + int64_t(panel) * g.steps * kMxTileBytes;
-    const uint8_t* const sx = (LEFT ? g.sa : g.sb) + int64_t(panel) * g.steps * kMxTileScales;
-    f32x4 acc[PANELS] = {};
-    for (int k = wave; k < g.steps; k += WAVES * AHEAD) {
-      u32x4 cx[AHEAD], cy[AHEAD][PANELS];
-      int bx[AHEAD], by[AHEAD][PANELS];
+  const int panel = blockIdx.x;
+  const uint8_t* const x = (LEFT ? g.a : g.b) + int64_t(panel) * g.steps * kMxTileBytes;
+  const uint8_t* const sx = (LEFT ? g.sa : g.sb) + int64_t(panel) * g.steps * kMxTileScales;
+  f32x4 acc[PANELS] = {};
+  for (int k = wave; k < g.steps; k += WAVES * AHEAD) {
+    u32x4 cx[AHEAD], cy[AHEAD][PANELS];
+    int bx[AHEAD], by[AHEAD][PANELS];
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int ku = min(k + u * WAVES, g.steps - 1);
-        cx[u] = code(x, ku);
-        bx[u] = sx[int64_t(ku) * kMxTileScales + sat];
+    for (int u = 0; u < AHEAD; ++u) {
+      const int ku = min(k + u * WAVES, g.steps - 1);
+      cx[u] = code(x, ku);
+      bx[u] = sx[int64_t(ku) * kMxTileScales + sat];
 #pragma unroll
-        for (int p = 0; p < PANELS; ++p) {
-          const int64_t tile = int64_t(min(p, panels_y - 1)) * g.steps + ku;
-          cy[u][p] = code(y, tile);
-          by[u][p] = sy[tile * kMxTileScales + sat];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        // (a step beyond the last is the last again with codes of 0: it adds 0, or a NaN that is there)
-        if (k + u * WAVES >= g.steps) cx[u] = u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int p = 0; p < PANELS; ++p)
-          acc[p] = LEFT ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cy[u][p]), wide(cx[u]), acc[p],
-                                                                          4, 4, 0, by[u][p], 0, bx[u])
-                        : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cx[u]), wide(cy[u][p]), acc[p],
-                                                                          4, 4, 0, bx[u], 0, by[u][p]);
+      for (int p = 0; p < PANELS; ++p) {
+        const int64_t tile = int64_t(min(p, panels_y - 1)) * g.steps + ku;
+        cy[u][p] = code(y, tile);
+        by[u][p] = sy[tile * kMxTileScales + sat];
       }
     }
 #pragma unroll
-    for (int p = 0; p < PANELS; ++p) sums[p][wave][lane] = acc[p];
-    __syncthreads();
-    // register e of lane l: row l % 16 of the second operand's panel, row 4 (l / 16) + e of the first's
-    for (int p = wave; p < PANELS; p += WAVES) {
-      f32x4 v = sums[p][0][lane];
+    for (int u = 0; u < AHEAD; ++u) {
+      // (a step beyond the last is the last again with codes of 0: it adds 0, or a NaN that is there)
+      if (k + u * WAVES >= g.steps) cx[u] = u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) v += sums[p][w][lane];
-      const int row = 16 * (LEFT ? panel : p) + lane % 16, col = 16 * (LEFT ? p : panel) + lane / 16 * 4;
-      if (row < g.m) store4<OUT>(g.out, int64_t(row) * g.n + col, g.n - col, v);
+      for (int p = 0; p < PANELS; ++p)
+        acc[p] = LEFT ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cy[u][p]), wide(cx[u]), acc[p],
+                                                                        4, 4, 0, by[u][p], 0, bx[u])
+                      : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(cx[u]), wide(cy[u][p]), acc[p],
+                                                                        4, 4, 0, bx[u], 0, by[u][p]);
     }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int p = 0; p < PANELS; ++p) sums[p][wave][lane] = acc[p];
+  __syncthreads();
+  // register e of lane l: row l % 16 of the second operand's panel, row 4 (l / 16) + e of the first's
+  for (int p = wave; p < PANELS; p += WAVES) {
+    f32x4 v = sums[p][0][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += sums[p][w][lane];
+    const int row = 16 * (LEFT ? panel : p) + lane % 16, col = 16 * (LEFT ? p : panel) + lane / 16 * 4;
+    if (row < g.m) store4<OUT>(g.out, int64_t(row) * g.n + col, g.n - col, v);
   }
 }
 
@@ -419,7 +425,10 @@ struct Choice {
   int wm, wn, splits;
 };
 
-constexpr int kFewRows = 64;
+// Few rows: up to 32, a long side of up to 16384 (8192 where there are more than 16 rows) and sums of up to
+// 16384 (8192). Few rows and tiles, us: 1 x 6400 x 1600 5.1 and 8.3, 16 x 6400 x 6400 7.9 and 11.8,
+// 1 x 12800 x 6400 13.2 and 14.8, 32 x 6400 x 6400 10.4 and 13.8; beyond, 1 x 50257 x 1600 11.0 and 10.2,
+// 32 x 50257 x 1600 16.4 and 10.7, 32 x 12800 x 6400 18.5 and 14.3, 48 x 6400 x 6400 15.9 and 11.7.
 
 // The tiles by estimated time, in us, from products measured on 256 compute units: a round of tiles
 // takes `stage` for each step and `fixed` (first loads, results); tiles of 256 x 256 have a compute
@@ -434,10 +443,10 @@ constexpr TileCost kTiles[] = {{4, 4, 256, 0.86, 6.0}, {2, 4, 512, 0.99, 1.6}, {
 
 Choice choose(int64_t m, int64_t n, int64_t steps) {
   Choice c{0, false, 4, 4, 1};
-  if (std::min(m, n) <= kFewRows) {
+  const int64_t few = mx_panels(std::min(m, n));
+  if (few <= 2 && few * mx_panels(std::max(m, n)) <= 1024 && few * steps <= 128) {
     c.left = m > n;
-    c.few = int((std::min(m, n) + 15) / 16);
-    if (c.few == 3) c.few = 4;
+    c.few = int(few);
     return c;
   }
   double best = 1e300;
@@ -471,7 +480,7 @@ int parts_of(const Choice& c, int64_t steps) {
 
 template <int OUT, int PANELS, bool LEFT>
 void launch_few(const MmArgs& g, hipStream_t s) {
-  const unsigned blocks = unsigned(std::min(LEFT ? g.panels_a : g.panels_b, 1 << 20));
+  const unsigned blocks = unsigned(LEFT ? g.panels_a : g.panels_b);
   if (g.steps <= 16)
     hipLaunchKernelGGL((mx_few_kernel<PANELS, 4, LEFT, OUT>), dim3(blocks), dim3(256), 0, s, g);
   else
@@ -482,7 +491,6 @@ template <int OUT>
 void launch(const Choice& c, const MmArgs& g, hipStream_t s) {
   if (c.few == 1) return c.left ? launch_few<OUT, 1, true>(g, s) : launch_few<OUT, 1, false>(g, s);
   if (c.few == 2) return c.left ? launch_few<OUT, 2, true>(g, s) : launch_few<OUT, 2, false>(g, s);
-  if (c.few) return c.left ? launch_few<OUT, 4, true>(g, s) : launch_few<OUT, 4, false>(g, s);
   const dim3 grid((unsigned)g.total), block(256);
   if (c.wm == 4 && c.wn == 4) hipLaunchKernelGGL((mx_matmul_kernel<4, 4, 4, OUT>), grid, block, 0, s, g);
   else if (c.wm == 4) hipLaunchKernelGGL((mx_matmul_kernel<4, 2, 3, OUT>), grid, block, 0, s, g);

@@ -197,7 +197,12 @@ struct Eight {
 // LDS: a thread then takes two neighbouring columns of 32 rows, four threads in a row their 128 rows,
 // and 16 bytes of codes leave for each column. A row's 64-byte quarters are exchanged by the block of
 // rows (XOR with row / 32), so that the 64 lanes of a read, 16 column pairs by four blocks of rows,
-// fall on 64 different banks.
+// fall on 64 different banks. Tiles are taken whole so that one read serves both results: two passes
+// would read 2 or 4 bytes a value again, more than all that is written.
+//
+// bf16 16384 x 6400 in both layouts: 67 to 82 us, 4.0 TB/s of the 321 MB that move (a copy of 1 GB: 4.8 to
+// 5.0); stochastically 104 to 114: the random bits and the step around each value are instructions that
+// the same traffic does not cover. fp32 1013 x 1601, 104 blocks, stochastically: 12.6.
 template <int DT, bool ROWS, bool COLS, bool STOCH>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantLaunch L) {
   constexpr int E = DT ? 4 : 2;
@@ -304,6 +309,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantLaunch
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 // A thread takes a dword of codes, 8 values; a block four panel's steps, in the order of the codes.
+// bf16 16384 x 6400: 48 to 51 us, 5.3 TB/s, the rate of writes.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint32_t* codes,
                                                                 const uint8_t* scales, int rows,
