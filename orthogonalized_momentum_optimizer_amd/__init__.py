@@ -11,6 +11,14 @@ or, for all parameters at once, with 8-bit states and clipping inside the step:
     from orthogonalized_momentum_optimizer_amd import AdamW
     opt = AdamW(params, lr=6e-4, weight_decay=0.1, state_bits=8, max_grad_norm=1.0)
 
+and for the products of a model whose weights Muon steps, in microscaled 4-bit values:
+
+    copies = MX4Copies(model_matrices)
+    opt = Muon(model_matrices, lr=0.02, mx4_copies=copies)
+    y = mx4_linear(x, w, copies[w])
+
+``orthogonalize`` runs the Newton-Schulz rounds on stacks of small matrices (attention heads).
+
 The library must be built first (``python -m orthogonalized_momentum_optimizer_amd.build``);
 importing the optimizer never falls back to another implementation.
 """

@@ -4,7 +4,7 @@ Codes and scales are compared byte by byte: quantisation has one answer for each
 tolerance: operands are exact, a product of two has at most 8 bits and sums are fp32. With s the sum
 of |a b| over k, an fp32 sum of k terms in any order is off by at most k 2^-24 s (to first order); the
 matrix cores may cut instead of rounding, which doubles it. bf16 results are rounded once more, by at
-most 2^-8 of the result (2^-9 to nearest; counted twice). Tests whose partial sums all fit 24 bits
+most half a step, 2^-8 of the result. Tests whose partial sums all fit 24 bits
 ask for equality.
 """
 import numpy as np

@@ -7,7 +7,9 @@ the normalised matrix, short side as rows:
 * the Gram matrix and rounds in double: errors of 10 (l + s) 2^-53 in A (||A|| <= 1) change P by at
   most that times D = max |dQ/dlambda| over [0, 1.02], Q the rounds' scalar polynomial, and so an
   element by that times the norm of its column of x;
-* bf16: 2^-8 of the result (twice half a step).
+* bf16: 2^-8 of the result, half a step. (A bf16 stack's Gram matrix is made of fp32 sums of 32 exact
+  products, added in double. What those are off by, up to 32 2^-24 |x| |x|^T times D, is not allowed for:
+  the bound asked for is the smaller one without it.)
 """
 import numpy as np
 import pytest
