@@ -231,7 +231,7 @@ __device__ __forceinline__ bool gram_held(int i, int j) {
 // LDS doubles that gram_part needs.
 template <int SP, int WAVES>
 struct GramShape {
-  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2, HALF = (WAVES + 1) / 2;
+  static constexpr int NB = SP / 16, BLOCKS = NB * (NB + 1) / 2;
   static constexpr int LDS = (WAVES / 2) * BLOCKS * 256 > SP * SP ? (WAVES / 2) * BLOCKS * 256 : SP * SP;
 };
 
@@ -503,8 +503,8 @@ struct Norm {
 // across the diagonal is computed and held, 10 of 16 for SP = 64 and 36 of 64 for 128, 17 doubles a row. Column
 // c has rows c, c + 1, .. (mod NB), NB / 2 + 1 of them for c < NB / 2, one fewer for the others, so that the right
 // operand is read and turned once for all of them; over four SIMDs a SIMD's share at SP = 64 is 3 blocks. A
-// column is one wave's, or where there are waves to spare two waves' (H = 2): one wave alone is given a 4x4x4
-// instruction every 30 cycles, two on a SIMD one every 17.
+// column is one wave's, at 32, where there are waves to spare, two waves' (H = 2: bf16 1500 x 31 x 800 162 -> 143
+// us; at 64 3% slower, as both waves read and turn the right operand).
 // A and Q lie in LDS, P too up to SP = 64; at 128 P is in the block's own scratch, in L2. T = Q A takes the
 // place of A.
 template <int SP, int H>
