@@ -10,10 +10,12 @@
  * A_0 = X_0 X_0^T, so the stack is read once for A_0 and once for P X_0, whatever the rounds.
  * A small singular value is known from A_0 to the square root of its precision only, and so the
  * Gram matrix and the rounds are formed in double (bf16 stacks: of sums of 32 exact products in
- * fp32) and P is rounded to fp32 once; the result is as exact as rounds in fp32 on X itself, or
- * rounded to bf16 once where that is its dtype.
+ * fp32, where fp32's range holds them) and P is rounded to fp32 once; the result is as exact as
+ * rounds in fp32 on X itself, or rounded to bf16 once where that is its dtype. The sums in fp32 leave
+ * A_0 (trace 1, long side l) off by up to about 2^-19 / sqrt(l) in norm; after five rounds of the
+ * default coefficients that is a small part of what rounding the result to bf16 takes.
  *
- * Every finite fp32 value is in range. A matrix of zeros gives zeros (for eps > 0). A NaN or
+ * Every finite value of either dtype is in range. A matrix of zeros gives zeros (for eps > 0). A NaN or
  * infinity makes its own matrix NaN and no other. Equal inputs give equal bits, wherever in a
  * stack a matrix stands, as long as the stack's sizes are equal.
  *

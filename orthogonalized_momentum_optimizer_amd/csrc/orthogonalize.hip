@@ -214,8 +214,9 @@ __device__ __forceinline__ int block_col(int r, int t) { return (r + 4 * t) % 16
 // fp32: a wave takes 16 long positions at a time: lane l holds, for each 16 short indexes (a block), the
 // values of short index r = l % 16 of it at positions 4 (l / 16) + 0..3, operands of four steps in double for
 // every pair of blocks. bf16: 32 positions, eight a lane, are one operand of the bf16 instruction, whose
-// products are exact; its sums of 32 are fp32 and are added in double (in double throughout 64 x 768 takes a
-// compute unit 13 us more).
+// products are exact; its sums of 32 are fp32 and are added in double (in double throughout, EXACT, 64 x 768
+// takes a compute unit 13 us more). Their trace says whether fp32 held them (fits_fp32); where it does not,
+// they are formed again in double, the lane's eight values operands of eight steps.
 // Rows contiguous along the long side give a lane's values by one load; contiguous along the short side
 // (TALL) a load gives the values of all NB blocks at one position, if block b has the short indexes
 // NB r + b. The next positions' values are on their way while these are multiplied.
@@ -243,6 +244,24 @@ template <int NB>
 struct GramValues<0, NB> {
   u32x4 x[NB];
 };
+
+// Value e of a lane's values of block b.
+template <int DT, int NB>
+__device__ __forceinline__ double gram_value(const GramValues<DT, NB>& v, int b, int e) {
+  if constexpr (DT) return v.x[b][e];
+  else return __uint_as_float(e & 1 ? v.x[b][e / 2] & 0xffff0000u : v.x[b][e / 2] << 16);
+}
+
+// Whether sums in fp32 hold what they stand for, by the trace of a matrix, or of a piece: no diagonal sum of 32
+// and so no other can have passed fp32's range (2^128), and products lost below it (2^-126, 2^24 of them at most)
+// are 2^-42 of the trace. A trace that is not finite, or of zeros, is formed again too.
+__device__ __forceinline__ bool fits_fp32(double trace) { return trace >= 0x1p-60 && trace <= 0x1p120; }
+
+// The sum of x over a wave, in each lane.
+__device__ __forceinline__ double wave_sum(double x) {
+  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
 
 // A lane's loads of a step, as they lie in memory.
 template <int DT, bool TALL, int NB>
@@ -342,7 +361,7 @@ struct GramLoads {
   }
 };
 
-template <int DT, bool TALL, int SP, int WAVES>
+template <int DT, bool TALL, int SP, int WAVES, bool EXACT>
 __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, int begin, int end, int wave,
                                           int lane, double* lds) {
   using S = GramShape<SP, WAVES>;
@@ -352,7 +371,7 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
 #pragma unroll
   for (int u = 0; u < S::BLOCKS; ++u) acc[u] = f64x4{0, 0, 0, 0};
   GramLoads<DT, TALL, SP>(g, base, begin, end, lane).each(wave, WAVES, [&](const GramValues<DT, NB>& x) {
-    if constexpr (DT == 0) {
+    if constexpr (!EXACT) {
 #pragma unroll
       for (int i = 0, u = 0; i < NB; ++i)
 #pragma unroll
@@ -363,12 +382,13 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
         }
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < (DT ? 4 : 8); ++e)
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const Turns d(x.x[j][e]);
+          const Turns d(gram_value(x, j, e));
 #pragma unroll
-          for (int i = 0; i <= j; ++i) mma_block(double(x.x[i][e]), d, acc[i * NB - i * (i - 1) / 2 + j - i]);
+          for (int i = 0; i <= j; ++i)
+            mma_block(gram_value(x, i, e), d, acc[i * NB - i * (i - 1) / 2 + j - i]);
         }
     }
   });
@@ -393,20 +413,34 @@ __device__ __forceinline__ void gram_part(const StackArgs& g, const char* base, 
       for (int j = i; j < NB; ++j, ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int a = DT ? block_row(r, q) : 4 * q + e, c = DT ? block_col(r, e) : r;
+          const int a = EXACT ? block_row(r, q) : 4 * q + e, c = EXACT ? block_col(r, e) : r;
           lds[TALL ? (NB * a + i) * SP + NB * c + j : (16 * i + a) * SP + 16 * j + c] = acc[u][e];
         }
   }
   __syncthreads();
 }
 
+// The Gram matrix of the block's positions begin .. end - 1 into lds, by fp32 sums where they hold it.
+template <int DT, bool TALL, int SP, int WAVES>
+__device__ __forceinline__ void gram_of(const StackArgs& g, const char* base, int begin, int end, int wave,
+                                        int lane, double* lds) {
+  if constexpr (DT == 0) {
+    gram_part<DT, TALL, SP, WAVES, false>(g, base, begin, end, wave, lane, lds);
+    double trace = 0;                            // the same in every wave
+    for (int i = lane; i < SP; i += 64) trace += lds[i * SP + i];
+    if (__builtin_amdgcn_readfirstlane(fits_fp32(wave_sum(trace)))) return;
+    __syncthreads();                             // everyone has read it
+  }
+  gram_part<DT, TALL, SP, WAVES, true>(g, base, begin, end, wave, lane, lds);
+}
+
 // At 128 the 36 blocks are 288 registers, so that they are shared out: wave W of four goes through all positions (the
 // loads of the other waves come from the L1 cache) with the blocks of columns W and W + 4, rows c, c + 1, .. (mod 8).
-// Straight into `out`. fp32 300 x 128 x 1024: 155 us (all blocks in every wave, with spills: 237), which the matrix
+// Straight into `out`; returns the wave's part of the trace. fp32 300 x 128 x 1024: 155 us (all blocks in every wave, with spills: 237), which the matrix
 // cores bound at 72; bf16 58 (87).
-template <int DT, bool TALL, int W>
-__device__ __forceinline__ void gram_shared(const StackArgs& g, const char* base, int begin, int end, int lane,
-                                            double* out) {
+template <int DT, bool TALL, bool EXACT, int W>
+__device__ __forceinline__ double gram_shared(const StackArgs& g, const char* base, int begin, int end, int lane,
+                                              double* out) {
   constexpr int SP = 128, NB = 8;
   f64x4 acc[9];
 #pragma unroll
@@ -414,37 +448,49 @@ __device__ __forceinline__ void gram_shared(const StackArgs& g, const char* base
   GramLoads<DT, TALL, SP>(g, base, begin, end, lane).each(0, 1, [&](const GramValues<DT, NB>& x) {
 #pragma unroll
     for (int u = 0; u < 9; ++u) {
-      if constexpr (DT == 0) {
+      if constexpr (!EXACT) {
         const int j = u < 5 ? W : W + 4, i = (j + u % 5) % NB;
         const f32x4 c = mma(x.x[i], x.x[j], f32x4{0, 0, 0, 0});
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[u][e] += double(c[e]);
       }
     }
-    if constexpr (DT) {
+    if constexpr (EXACT) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < (DT ? 4 : 8); ++e)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int j = W + 4 * h;
-          const Turns d(x.x[j][e]);
+          const Turns d(gram_value(x, j, e));
 #pragma unroll
-          for (int o = 0; o < 5 - h; ++o) mma_block(double(x.x[(j + o) % NB][e]), d, acc[5 * h + o]);
+          for (int o = 0; o < 5 - h; ++o) mma_block(gram_value(x, (j + o) % NB, e), d, acc[5 * h + o]);
         }
     }
   });
   const int r = lane & 15, q = lane >> 4;
+  double trace = 0;
 #pragma unroll
   for (int u = 0; u < 9; ++u) {
     const int j = u < 5 ? W : W + 4, i = (j + u % 5) % NB;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int a = DT ? block_row(r, q) : 4 * q + e, c = DT ? block_col(r, e) : r;
+      const int a = EXACT ? block_row(r, q) : 4 * q + e, c = EXACT ? block_col(r, e) : r;
       const int row = TALL ? NB * a + i : 16 * i + a, col = TALL ? NB * c + j : 16 * j + c;
       out[row * SP + col] = acc[u][e];
       if (i != j) out[col * SP + row] = acc[u][e];
+      else if (a == c) trace += acc[u][e];
     }
   }
+  return EXACT ? 0.0 : wave_sum(trace);
+}
+
+template <int DT, bool TALL, bool EXACT>
+__device__ __forceinline__ double gram_shared(const StackArgs& g, const char* base, int begin, int end, int wave,
+                                              int lane, double* out) {
+  if (wave == 0) return gram_shared<DT, TALL, EXACT, 0>(g, base, begin, end, lane, out);
+  if (wave == 1) return gram_shared<DT, TALL, EXACT, 1>(g, base, begin, end, lane, out);
+  if (wave == 2) return gram_shared<DT, TALL, EXACT, 2>(g, base, begin, end, lane, out);
+  return gram_shared<DT, TALL, EXACT, 3>(g, base, begin, end, lane, out);
 }
 
 // A part of a matrix's long side (grid: count * splits) into its own whole matrix.
@@ -459,13 +505,17 @@ __global__ __launch_bounds__(256, SP == 128 ? 2 : 1) void gram_kernel(const Stac
   double* const out = g.gram + int64_t(blockIdx.x) * (SP * SP);
   if constexpr (SP == 128) {
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    if (wave == 0) gram_shared<DT, TALL, 0>(g, base, begin, end, t & 63, out);
-    else if (wave == 1) gram_shared<DT, TALL, 1>(g, base, begin, end, t & 63, out);
-    else if (wave == 2) gram_shared<DT, TALL, 2>(g, base, begin, end, t & 63, out);
-    else gram_shared<DT, TALL, 3>(g, base, begin, end, t & 63, out);
+    if constexpr (DT == 0) {
+      __shared__ double traces[4];
+      const double trace = gram_shared<DT, TALL, false>(g, base, begin, end, wave, t & 63, out);
+      if ((t & 63) == 0) traces[wave] = trace;
+      __syncthreads();                           // (and what the waves stored is ordered before the second form)
+      if (__builtin_amdgcn_readfirstlane(fits_fp32(traces[0] + traces[1] + traces[2] + traces[3]))) return;
+    }
+    gram_shared<DT, TALL, true>(g, base, begin, end, wave, t & 63, out);
   } else {
     __shared__ double sum[GramShape<SP, 4>::LDS];
-    gram_part<DT, TALL, SP, 4>(g, base, begin, end, t >> 6, t & 63, sum);
+    gram_of<DT, TALL, SP, 4>(g, base, begin, end, __builtin_amdgcn_readfirstlane(t >> 6), t & 63, sum);
     for (int at = t; at < SP * SP; at += 256) {
       const int i = at / SP, j = at % SP;
       out[at] = gram_held<TALL, SP>(i, j) ? sum[at] : sum[j * SP + i];
@@ -642,8 +692,7 @@ __device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<S
   __syncthreads();
   double trace = 0;                              // the same in every wave
   for (int i = lane; i < SP; i += 64) trace += trace_of[i];
-  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
-  const Norm norm(trace, R.eps);
+  const Norm norm(wave_sum(trace), R.eps);
   if (works) {
     B.held([&](int o, int e, int at) {
       c[o][e] = c[o][e] * norm.scale * norm.scale;
@@ -899,7 +948,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void whole_kernel(c
                          matrix_at(g.first + m, g.inner, g.in_outer, g.in_inner) * (DT ? 4 : 2);
   char* const out = static_cast<char*>(g.out) +
                     matrix_at(g.first + m, g.inner, g.out_outer, g.out_inner) * (DT ? 4 : 2);
-  gram_part<DT, TALL, SP, WAVES>(g, in, 0, g.l, wave, lane, lds);
+  gram_of<DT, TALL, SP, WAVES>(g, in, 0, g.l, wave, lane, lds);
   f64x4 c[S::OWN], p[S::OWN];
   if (B.own > 0)
     B.each([&](int o, int e, int row, int col) {
@@ -976,8 +1025,7 @@ __global__ __launch_bounds__(512) void narrow_kernel(const StackArgs g, const Ro
   double trace = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) trace += 4 * e + q == r ? A[e] : 0.0;
-  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
-  const Norm norm(trace, R.eps);
+  const Norm norm(wave_sum(trace), R.eps);
   f64x4 P;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
