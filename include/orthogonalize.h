@@ -15,6 +15,12 @@
  * A_0 (trace 1, long side l) off by up to about 2^-19 / sqrt(l) in norm; after five rounds of the
  * default coefficients that is a small part of what rounding the result to bf16 takes.
  *
+ * Rounds that could lift a direction of X by more than 2^15 in all (eight of the default coefficients
+ * lift by 2^14.3) are done in several passes over the stack, each with a Gram matrix of its own, as the
+ * rounds on a matrix without full rank otherwise run off. Between passes an fp32 stack is held in out;
+ * a bf16 stack is refused for such rounds (MUON_ERR_UNSUPPORTED): convert it to fp32. bf16 stacks
+ * whose rounds lift by more than 2^9 (five of the default ones: 485) are summed in double.
+ *
  * Every finite value of either dtype is in range. A matrix of zeros gives zeros (for eps > 0). A NaN or
  * infinity makes its own matrix NaN and no other. Equal inputs give equal bits, wherever in a
  * stack a matrix stands, as long as the stack's sizes are equal.
@@ -47,6 +53,10 @@ typedef struct {
  * sizes needs; 0: none. SIZE_MAX for sizes outside the limits (min(rows, cols) <= 128, max <= 2^24,
  * outer * inner <= 2^24). */
 size_t muon_orthogonalize_workspace_size(int64_t outer, int64_t inner, int64_t rows, int64_t cols);
+
+/* The passes over a stack that the rounds of cfg take (ns_steps, a, b, c, schedule; above), 1 or more,
+ * or the (negative) status of a configuration that is refused. */
+int muon_orthogonalize_passes(const muon_config *cfg);
 
 /* out <- the orthogonalised matrices; of cfg: ns_steps (>= 0), a, b, c, schedule and eps. in and
  * out may not overlap (but in == out with equal strides is taken: in place). */

@@ -42,7 +42,7 @@ EXPORTED = (
     "muon_grad_norm", "muon_grad_scale", "muon_grad_plan_destroy",
     "muon_mx_codes_size", "muon_mx_scales_size", "muon_mx_quantize", "muon_mx_dequantize",
     "muon_mx_matmul_workspace_size", "muon_mx_matmul",
-    "muon_orthogonalize_workspace_size", "muon_orthogonalize",
+    "muon_orthogonalize_workspace_size", "muon_orthogonalize_passes", "muon_orthogonalize",
 )
 MUON_MAX_STREAMS = 4
 MUON_ADAMW_F32 = 0
@@ -187,7 +187,7 @@ def args():
         _tensor_args.bind(*(address_of(f) for f in (
             L.muon_mx_quantize, L.muon_mx_dequantize, L.muon_mx_matmul,
             L.muon_mx_matmul_workspace_size, L.muon_orthogonalize,
-            L.muon_orthogonalize_workspace_size, L.muon_last_error)))
+            L.muon_orthogonalize_workspace_size, L.muon_orthogonalize_passes, L.muon_last_error)))
         _args = _tensor_args
     return _args
 
@@ -291,6 +291,8 @@ def lib() -> ctypes.CDLL:
     L.muon_mx_matmul.restype = ctypes.c_int
     L.muon_orthogonalize_workspace_size.argtypes = [i64, i64, i64, i64]
     L.muon_orthogonalize_workspace_size.restype = sz
+    L.muon_orthogonalize_passes.argtypes = [ctypes.POINTER(muon_config)]
+    L.muon_orthogonalize_passes.restype = ctypes.c_int
     L.muon_orthogonalize.argtypes = [ctypes.POINTER(muon_stack), ctypes.POINTER(muon_config), vp, sz, vp]
     L.muon_orthogonalize.restype = ctypes.c_int
     L.muon_status_string.argtypes = [ctypes.c_int]
@@ -544,6 +546,12 @@ def muon_mx_matmul(a_codes: int, a_scales: int, b_codes: int, b_scales: int, m: 
 
 def muon_orthogonalize_workspace_size(outer: int, inner: int, rows: int, cols: int) -> int:
     return int(lib().muon_orthogonalize_workspace_size(outer, inner, rows, cols))
+
+
+def muon_orthogonalize_passes(cfg: muon_config) -> int:
+    passes = lib().muon_orthogonalize_passes(ctypes.byref(cfg))
+    _check(min(passes, 0))
+    return passes
 
 
 def muon_orthogonalize(stack: muon_stack, cfg: muon_config, workspace, workspace_bytes: int,

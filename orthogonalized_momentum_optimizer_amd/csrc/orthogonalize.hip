@@ -13,6 +13,12 @@
 // rounds lift the small ones (by up to a^2 each), so that the result is off by about E / 2 sigma^2 for
 // ||X_0||_F = 1. With fp32 sums a spectrum of sigma^2 = 1e-5, a square matrix's, would be off by
 // several 1e-3 in its smallest directions; in double it is not.
+//
+// What rounds on A cost: an eigenvalue of A_0 that should be 0 comes out as +-E, and every round multiplies it by
+// up to the square of what it multiplies X by. Past 0.1 below zero it runs off to minus infinity, where rounds on X
+// itself keep it at 0 or at the noise of X; and P, in fp32 where it meets X, has grown as much. So rounds are done in
+// passes (rounds_of_pass): P is applied, and the Gram matrix of the result formed anew, before the rounds of a pass
+// could have lifted anything by more than 2^15.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -41,6 +47,7 @@ struct StackArgs {
   int inner, s, l;
   int count;                                     // of the batch
   int splits, span;                              // pieces of the long side, and a piece's length
+  bool exact;                                    // bf16: sums of products in double throughout
   double* gram;                                  // count x splits x SP x SP
   uint16_t* p;                                   // count x 3 x SP x SP: P in parts
   int* expo;                                     // count x 2: of two, for X and for the result
@@ -50,6 +57,7 @@ struct StackArgs {
 struct Rounds {
   int n;
   float eps;
+  bool as_is;                                    // a later pass: X is not divided by its norm
   float abc[3 * kMaxRounds];
 };
 
@@ -425,11 +433,13 @@ template <int DT, bool TALL, int SP, int WAVES>
 __device__ __forceinline__ void gram_of(const StackArgs& g, const char* base, int begin, int end, int wave,
                                         int lane, double* lds) {
   if constexpr (DT == 0) {
-    gram_part<DT, TALL, SP, WAVES, false>(g, base, begin, end, wave, lane, lds);
-    double trace = 0;                            // the same in every wave
-    for (int i = lane; i < SP; i += 64) trace += lds[i * SP + i];
-    if (__builtin_amdgcn_readfirstlane(fits_fp32(wave_sum(trace)))) return;
-    __syncthreads();                             // everyone has read it
+    if (!g.exact) {
+      gram_part<DT, TALL, SP, WAVES, false>(g, base, begin, end, wave, lane, lds);
+      double trace = 0;                          // the same in every wave
+      for (int i = lane; i < SP; i += 64) trace += lds[i * SP + i];
+      if (__builtin_amdgcn_readfirstlane(fits_fp32(wave_sum(trace)))) return;
+      __syncthreads();                           // everyone has read it
+    }
   }
   gram_part<DT, TALL, SP, WAVES, true>(g, base, begin, end, wave, lane, lds);
 }
@@ -507,10 +517,12 @@ __global__ __launch_bounds__(256, SP == 128 ? 2 : 1) void gram_kernel(const Stac
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     if constexpr (DT == 0) {
       __shared__ double traces[4];
-      const double trace = gram_shared<DT, TALL, false>(g, base, begin, end, wave, t & 63, out);
-      if ((t & 63) == 0) traces[wave] = trace;
-      __syncthreads();                           // (and what the waves stored is ordered before the second form)
-      if (__builtin_amdgcn_readfirstlane(fits_fp32(traces[0] + traces[1] + traces[2] + traces[3]))) return;
+      if (!g.exact) {
+        const double trace = gram_shared<DT, TALL, false>(g, base, begin, end, wave, t & 63, out);
+        if ((t & 63) == 0) traces[wave] = trace;
+        __syncthreads();                         // (and what the waves stored is ordered before the second form)
+        if (__builtin_amdgcn_readfirstlane(fits_fp32(traces[0] + traces[1] + traces[2] + traces[3]))) return;
+      }
     }
     gram_shared<DT, TALL, true>(g, base, begin, end, wave, t & 63, out);
   } else {
@@ -531,10 +543,15 @@ __global__ __launch_bounds__(256, SP == 128 ? 2 : 1) void gram_kernel(const Stac
 struct Norm {
   double scale, p_scale;
   int x_expo, out_expo;
-  __device__ __forceinline__ Norm(double trace, float eps) {
-    const double plain = sqrt(trace), norm = plain + double(eps);
-    scale = 1.0 / norm;
+  __device__ __forceinline__ Norm(double trace, const Rounds& R) {
     x_expo = out_expo = 0;
+    if (R.as_is) {
+      scale = 1.0;
+      p_scale = isfinite(trace) ? 1.0 : __longlong_as_double(0x7ff8000000000000ll);
+      return;
+    }
+    const double plain = sqrt(trace), norm = plain + double(R.eps);
+    scale = 1.0 / norm;
     const bool fine = isfinite(norm) && norm > 0;
     p_scale = fine ? scale : __longlong_as_double(0x7ff8000000000000ll);
     if (!fine) return;
@@ -692,7 +709,7 @@ __device__ __forceinline__ Norm rounds_part(const Rounds& R, const RoundBlocks<S
   __syncthreads();
   double trace = 0;                              // the same in every wave
   for (int i = lane; i < SP; i += 64) trace += trace_of[i];
-  const Norm norm(wave_sum(trace), R.eps);
+  const Norm norm(wave_sum(trace), R);
   if (works) {
     B.held([&](int o, int e, int at) {
       c[o][e] = c[o][e] * norm.scale * norm.scale;
@@ -1025,7 +1042,7 @@ __global__ __launch_bounds__(512) void narrow_kernel(const StackArgs g, const Ro
   double trace = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) trace += 4 * e + q == r ? A[e] : 0.0;
-  const Norm norm(wave_sum(trace), R.eps);
+  const Norm norm(wave_sum(trace), R);
   f64x4 P;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -1145,6 +1162,48 @@ Launch launch_for(int sp) {
        : sp == 64 ? launch_all<DT, TALL, 64> : launch_all<DT, TALL, 128>;
 }
 
+// What a round can multiply a direction of X by: the largest |q| over [0, top], q(x) = a + b x + c x^2, top the
+// largest eigenvalue that A can have; and that one after it, the largest x q(x)^2.
+double round_gain(const float* abc, double* top) {
+  const double a = abc[0], b = abc[1], c = abc[2], t = *top;
+  auto q = [&](double x) { return std::fabs(a + b * x + c * x * x); };
+  double gain = std::max(q(0), q(t)), next = t * q(t) * q(t);
+  if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < t) gain = std::max(gain, q(-b / (2 * c)));
+  // where (x q^2)' = q (a + 3 b x + 5 c x^2) is 0
+  const double d = 9 * b * b - 20 * a * c;
+  for (int sign = -1; sign <= 1; sign += 2) {
+    const double x = c != 0 ? (d >= 0 ? (-3 * b + sign * std::sqrt(d)) / (10 * c) : 0) : b != 0 ? -a / (3 * b) : 0;
+    if (x > 0 && x < t) next = std::max(next, x * q(x) * q(x));
+  }
+  *top = next;
+  return gain;
+}
+
+// The rounds from `first` on that one pass does: as many as lift nothing by more than 2^15, one at least. By
+// then an error of 1e-15 of an eigenvalue of A (double) is 1e-6 and P's rounding to fp32 1e-3 in directions in which X
+// has nothing, as with rounds on X in fp32, where the noise of the first is lifted alike (a 64 x 768 matrix of
+// rank 8, default coefficients, off by, in norm: 8 rounds 4e-4 here and there, 12 rounds 4e-2 and 5e-2).
+// *lift: by how much these do. Eight rounds of the default coefficients are one pass, any number of (1.5, -0.5, 0)
+// up to 25.
+constexpr double kMostLift = 0x1p15;
+// Up to here bf16 stacks are summed by the bf16 instructions, whose errors of 2e-9 of an eigenvalue (64 x 768; up to 1e-8
+// for short sums) this lifts to 3e-3; beyond, in double. Five rounds of the default coefficients lift by 485.
+constexpr double kMostLiftBf16 = 0x1p9;
+
+int rounds_of_pass(const muon_config* cfg, int first, double* top, double* lift) {
+  double run = 1;                                // what the rounds up to here lift most, from whichever on
+  *lift = 1;
+  int n = first;
+  for (; n < cfg->ns_steps; ++n) {
+    double after = *top;
+    run = std::max(run, 1.0) * round_gain(cfg->schedule ? cfg->schedule + 3 * n : &cfg->a, &after);
+    if (n > first && !(run <= kMostLift)) break;
+    *lift = std::max(*lift, run);
+    *top = after;
+  }
+  return n - first;
+}
+
 // The elements from the first to behind the last of a strided stack; false if it does not fit.
 bool extent(const muon_stack& k, const int64_t* stride, int64_t* elems) {
   const int64_t side[4] = {k.outer, k.inner, k.rows, k.cols};
@@ -1184,6 +1243,17 @@ size_t muon_orthogonalize_workspace_size(int64_t outer, int64_t inner, int64_t r
   if (!limits_ok(outer, inner, rows, cols)) return SIZE_MAX;
   if (outer == 0 || inner == 0 || rows == 0 || cols == 0) return 0;
   return sizes_of(outer * inner, rows, cols).total();
+}
+
+int muon_orthogonalize_passes(const muon_config* cfg) {
+  return c_entry([&]() -> int {
+    if (int st = check_config(cfg)) return st;
+    int passes = 0;
+    double top = 1, lift;
+    for (int first = 0; passes == 0 || first < cfg->ns_steps; ++passes)
+      first += rounds_of_pass(cfg, first, &top, &lift);
+    return passes;
+  });
 }
 
 int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* workspace,
@@ -1228,46 +1298,63 @@ int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* wo
       rs.push_back(range(k.in, size_t(in_elems) * e, false));
     if (int st = check_overlaps(rs)) return st;
 
-    // the contiguous side is the long one, or the short one (TALL)
+    double top = 1, lift;
+    int rounds = rounds_of_pass(cfg, 0, &top, &lift);
+    if (k.dtype == MUON_DT_BF16 && rounds < cfg->ns_steps)
+      return fail(MUON_ERR_UNSUPPORTED, "these rounds take more than one pass, which bf16 stacks cannot (between "
+                  "passes values are held in the result's dtype): convert to fp32");
+
     const bool long_is_cols = k.cols >= k.rows;
-    const bool tall = long_is_cols ? !by_cols : !by_rows;
-    const int other = long_is_cols != tall ? 2 : 3;    // the side whose stride is free
     StackArgs g;
-    g.in = k.in;
     g.out = k.out;
-    g.in_outer = k.in_stride[0];
-    g.in_inner = k.in_stride[1];
-    g.in_ld = k.in_stride[other];
     g.out_outer = k.out_stride[0];
     g.out_inner = k.out_stride[1];
-    g.out_ld = k.out_stride[other];
     g.inner = int(k.inner);
     g.s = z.s;
     g.l = z.l;
     g.splits = z.splits;
     g.span = z.span;
+    g.exact = lift > kMostLiftBf16;
     char* at = static_cast<char*>(workspace);
     g.gram = reinterpret_cast<double*>(at);
     g.p = reinterpret_cast<uint16_t*>(at += z.gram);
     g.expo = reinterpret_cast<int*>(at += z.p);
     g.scratch = reinterpret_cast<double*>(at += z.expo);
     Rounds R;
-    R.n = cfg->ns_steps;
     R.eps = cfg->eps;
-    for (int n = 0; n < R.n; ++n)
-      for (int c = 0; c < 3; ++c) R.abc[3 * n + c] = cfg->schedule ? cfg->schedule[3 * n + c] : (&cfg->a)[c];
-    const Launch run = k.dtype == MUON_DT_F32
-        ? (tall ? launch_for<1, true>(z.sp) : launch_for<1, false>(z.sp))
-        : (tall ? launch_for<0, true>(z.sp) : launch_for<0, false>(z.sp));
-    for (int64_t first = 0; first < z.count; first += z.batch) {
-      g.first = first;
-      g.count = int(std::min(z.batch, z.count - first));
-      run(g, R, z.whole, stream);
-      const hipError_t err = hipGetLastError();
-      if (err != hipSuccess)
-        return fail(MUON_ERR_HIP, "launch of an orthogonalisation kernel failed: %s", hipGetErrorString(err));
+    // a pass reads the stack, or what the one before has left in out
+    for (int first = 0;;) {
+      const int64_t* const in_stride = first ? k.out_stride : k.in_stride;
+      // the contiguous side is the long one, or the short one (TALL)
+      const bool cols_lie = unit(in_stride, 3) && unit(k.out_stride, 3);
+      const bool rows_lie = unit(in_stride, 2) && unit(k.out_stride, 2);
+      const bool tall = long_is_cols ? !cols_lie : !rows_lie;
+      const int other = long_is_cols != tall ? 2 : 3;  // the side whose stride is free
+      g.in = first ? k.out : k.in;
+      g.in_outer = in_stride[0];
+      g.in_inner = in_stride[1];
+      g.in_ld = in_stride[other];
+      g.out_ld = k.out_stride[other];
+      R.n = rounds;
+      R.as_is = first > 0;
+      for (int n = 0; n < rounds; ++n)
+        for (int c = 0; c < 3; ++c)
+          R.abc[3 * n + c] = cfg->schedule ? cfg->schedule[3 * (first + n) + c] : (&cfg->a)[c];
+      const Launch run = k.dtype == MUON_DT_F32
+          ? (tall ? launch_for<1, true>(z.sp) : launch_for<1, false>(z.sp))
+          : (tall ? launch_for<0, true>(z.sp) : launch_for<0, false>(z.sp));
+      for (int64_t m = 0; m < z.count; m += z.batch) {
+        g.first = m;
+        g.count = int(std::min(z.batch, z.count - m));
+        run(g, R, z.whole, stream);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess)
+          return fail(MUON_ERR_HIP, "launch of an orthogonalisation kernel failed: %s", hipGetErrorString(err));
+      }
+      first += rounds;
+      if (first >= cfg->ns_steps) return MUON_OK;
+      rounds = rounds_of_pass(cfg, first, &top, &lift);
     }
-    return MUON_OK;
   });
 }
 

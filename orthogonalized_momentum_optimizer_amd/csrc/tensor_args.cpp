@@ -258,6 +258,7 @@ typedef int (*Product)(const void*, const void*, const void*, const void*, int64
 typedef size_t (*ProductSize)(int64_t, int64_t, int64_t);
 typedef int (*Stacked)(const void*, const void*, void*, size_t, void*);
 typedef size_t (*StackedSize)(int64_t, int64_t, int64_t, int64_t);
+typedef int (*Passes)(const void*);
 typedef const char* (*LastError)();
 
 struct Library {
@@ -267,18 +268,19 @@ struct Library {
   ProductSize product_size;
   Stacked stacked;
   StackedSize stacked_size;
+  Passes passes;
   LastError last_error;
 } library;
 
-// bind(quantize, dequantize, matmul, its workspace, orthogonalize, its workspace, last error): their
-// addresses, before any of the calls below.
+// bind(quantize, dequantize, matmul, its workspace, orthogonalize, its workspace, its passes, last error):
+// their addresses, before any of the calls below.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long f[7];
-  if (!PyArg_ParseTuple(args, "KKKKKKK", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6)) return nullptr;
+  unsigned long long f[8];
+  if (!PyArg_ParseTuple(args, "KKKKKKKK", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7)) return nullptr;
   library = {reinterpret_cast<Quantize>(f[0]),  reinterpret_cast<Dequantize>(f[1]),
              reinterpret_cast<Product>(f[2]),   reinterpret_cast<ProductSize>(f[3]),
              reinterpret_cast<Stacked>(f[4]),   reinterpret_cast<StackedSize>(f[5]),
-             reinterpret_cast<LastError>(f[6])};
+             reinterpret_cast<Passes>(f[6]),    reinterpret_cast<LastError>(f[7])};
   Py_RETURN_NONE;
 }
 
@@ -625,6 +627,63 @@ struct Stack {
   int dtype;
 };
 
+// A new tensor of x's shape, dense, its dimensions in x's order of strides.
+at::Tensor dense_like(const at::Tensor& x, at::ScalarType type) {
+  const int64_t d = x.dim();
+  std::vector<int64_t> order(d), strides(d);
+  for (int64_t i = 0; i < d; ++i) order[i] = i;
+  auto far = [&](int64_t i) {                    // (a dimension without strides goes outside)
+    return x.size(i) > 1 && x.stride(i) == 0 ? INT64_MAX : x.stride(i);
+  };
+  std::stable_sort(order.begin(), order.end(), [&](int64_t a, int64_t b) { return far(a) > far(b); });
+  int64_t step = 1;
+  for (int64_t i = d; i-- > 0;) {
+    strides[order[i]] = step;
+    step *= std::max<int64_t>(x.size(order[i]), 1);
+  }
+  return at::empty_strided(x.sizes(), strides, at::TensorOptions().dtype(type).device(x.device()));
+}
+
+// muon_orthogonalize of x into out, tensors of equal sizes, dtypes and devices.
+void orthogonalize_into(const at::Tensor& x, const at::Tensor& out, const void* cfg) {
+  const int64_t d = x.dim();
+  Stack k{};
+  k.dtype = dtype_code(x);
+  k.in = x.numel() ? x.const_data_ptr() : nullptr;
+  k.out = x.numel() ? out.data_ptr() : nullptr;
+  // leading dimensions, from the last: each joins the group behind it or opens the next one outside
+  int64_t sides[2] = {1, 1}, si[2] = {0, 0}, so[2] = {0, 0};
+  int groups = 0;
+  for (int64_t i = d - 3; i >= 0; --i) {
+    const int64_t n = x.size(i);
+    if (n == 1) continue;
+    if (groups && x.stride(i) == si[groups - 1] * sides[groups - 1] &&
+        out.stride(i) == so[groups - 1] * sides[groups - 1]) {
+      sides[groups - 1] *= n;
+      continue;
+    }
+    if (groups == 2) throw Refused{PyExc_ValueError, "leading dimensions of more than two strides"};
+    sides[groups] = n;
+    si[groups] = x.stride(i);
+    so[groups] = out.stride(i);
+    ++groups;
+  }
+  for (int j = 0; j < 2; ++j) {                  // group 0 is the inner one
+    k.side[1 - j] = sides[j];
+    k.in_stride[1 - j] = si[j];
+    k.out_stride[1 - j] = so[j];
+    k.side[2 + j] = x.size(d - 2 + j);
+    k.in_stride[2 + j] = x.stride(d - 2 + j);
+    k.out_stride[2 + j] = out.stride(d - 2 + j);
+  }
+  const size_t need = library.stacked_size(k.side[0], k.side[1], k.side[2], k.side[3]);
+  at::Tensor ws;
+  if (need && need != SIZE_MAX)
+    ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(x.device()));
+  check(library.stacked(&k, cfg, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? need : 0,
+                        stream_of(x.device())));
+}
+
 // orthogonalize(x, out, cfg) -> out (a new tensor in x's order of strides where it is None), or the
 // status. x: at least 2-D, its leading dimensions two strides at most.
 PyObject* orthogonalize(PyObject*, PyObject* args) {
@@ -637,65 +696,29 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
       throw Refused{PyExc_ValueError, "a CUDA tensor whose memory holds its values expected"};
     if (dtype_code(x) != 0 && dtype_code(x) != 1)
       throw Refused{PyExc_TypeError, "unsupported dtype: the library takes bfloat16 or float32"};
-    const int64_t d = x.dim();
-    if (d < 2) throw Refused{PyExc_ValueError, "a matrix or a stack of them expected"};
+    if (x.dim() < 2) throw Refused{PyExc_ValueError, "a matrix or a stack of them expected"};
     const c10::DeviceGuard guard(x.device());
     at::Tensor out;
-    if (oo == Py_None) {                         // dense, dimensions in x's order of strides
-      std::vector<int64_t> order(d), strides(d);
-      for (int64_t i = 0; i < d; ++i) order[i] = i;
-      auto far = [&](int64_t i) {                // (a dimension without strides goes outside)
-        return x.size(i) > 1 && x.stride(i) == 0 ? INT64_MAX : x.stride(i);
-      };
-      std::stable_sort(order.begin(), order.end(), [&](int64_t a, int64_t b) { return far(a) > far(b); });
-      int64_t step = 1;
-      for (int64_t i = d; i-- > 0;) {
-        strides[order[i]] = step;
-        step *= std::max<int64_t>(x.size(order[i]), 1);
-      }
-      out = at::empty_strided(x.sizes(), strides, x.options().requires_grad(false));
+    if (oo == Py_None) {
+      out = dense_like(x, x.scalar_type());
     } else {
       out = tensor_of(oo);
       if (out.device() != x.device() || out.scalar_type() != x.scalar_type() ||
           out.sizes() != x.sizes() || out.layout() != at::kStrided || out.is_neg())
         throw Refused{PyExc_ValueError, "out must be a tensor of x's shape, dtype and device"};
     }
-    Stack k{};
-    k.dtype = dtype_code(x);
-    k.in = x.numel() ? x.const_data_ptr() : nullptr;
-    k.out = x.numel() ? out.data_ptr() : nullptr;
-    // leading dimensions, from the last: each joins the group behind it or opens the next one outside
-    int64_t sides[2] = {1, 1}, si[2] = {0, 0}, so[2] = {0, 0};
-    int groups = 0;
-    for (int64_t i = d - 3; i >= 0; --i) {
-      const int64_t n = x.size(i);
-      if (n == 1) continue;
-      if (groups && x.stride(i) == si[groups - 1] * sides[groups - 1] &&
-          out.stride(i) == so[groups - 1] * sides[groups - 1]) {
-        sides[groups - 1] *= n;
-        continue;
-      }
-      if (groups == 2) throw Refused{PyExc_ValueError, "leading dimensions of more than two strides"};
-      sides[groups] = n;
-      si[groups] = x.stride(i);
-      so[groups] = out.stride(i);
-      ++groups;
-    }
-    for (int j = 0; j < 2; ++j) {                // group 0 is the inner one
-      k.side[1 - j] = sides[j];
-      k.in_stride[1 - j] = si[j];
-      k.out_stride[1 - j] = so[j];
-      k.side[2 + j] = x.size(d - 2 + j);
-      k.in_stride[2 + j] = x.stride(d - 2 + j);
-      k.out_stride[2 + j] = out.stride(d - 2 + j);
-    }
+    const int passes = library.passes(cfg.view.buf);
+    check(std::min(passes, 0));
     unlocked([&] {
-      const size_t need = library.stacked_size(k.side[0], k.side[1], k.side[2], k.side[3]);
-      at::Tensor ws;
-      if (need && need != SIZE_MAX)
-        ws = at::empty({int64_t(need)}, at::TensorOptions().dtype(at::kByte).device(x.device()));
-      check(library.stacked(&k, cfg.view.buf, ws.defined() ? ws.data_ptr() : nullptr,
-                            ws.defined() ? need : 0, stream_of(x.device())));
+      if (passes > 1 && dtype_code(x) == 0) {    // bf16 values are held in fp32 between passes
+        const at::AutoGradMode no_grad(false);
+        at::Tensor wide = dense_like(x, at::kFloat);
+        wide.copy_(x);
+        orthogonalize_into(wide, wide, cfg.view.buf);
+        out.copy_(wide);
+      } else {
+        orthogonalize_into(x, out, cfg.view.buf);
+      }
     });
     // (what autograd saved of the result's tensor before is not its value any more)
     if (oo != Py_None && !out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
