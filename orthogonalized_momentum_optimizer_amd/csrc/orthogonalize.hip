@@ -1130,16 +1130,17 @@ Sizes sizes_of(int64_t count, int64_t rows, int64_t cols) {
   return z;
 }
 
+// A batch of z.count matrices. What decides about a sum's order goes by the stack, not by the batch.
 template <int DT, bool TALL, int SP>
-void launch_all(const StackArgs& g, const Rounds& R, bool whole, hipStream_t s) {
+void launch_all(const StackArgs& g, const Rounds& R, const Sizes& z, hipStream_t s) {
   if constexpr (SP == 16) {
-    if (whole) {
+    if (z.whole) {
       hipLaunchKernelGGL((narrow_kernel<DT, TALL>), dim3((unsigned)g.count), dim3(512), 0, s, g, R);
       return;
     }
   } else if constexpr (SP <= 64) {
-    if (whole) {
-      if (g.count > kBlocks)
+    if (z.whole) {
+      if (z.count > kBlocks)
         hipLaunchKernelGGL((whole_kernel<DT, TALL, SP, 4>), dim3((unsigned)g.count), dim3(256), 0, s, g, R);
       else
         hipLaunchKernelGGL((whole_kernel<DT, TALL, SP, 8>), dim3((unsigned)g.count), dim3(512), 0, s, g, R);
@@ -1155,7 +1156,7 @@ void launch_all(const StackArgs& g, const Rounds& R, bool whole, hipStream_t s) 
                      chunks, chunk);
 }
 
-typedef void (*Launch)(const StackArgs&, const Rounds&, bool, hipStream_t);
+typedef void (*Launch)(const StackArgs&, const Rounds&, const Sizes&, hipStream_t);
 template <int DT, bool TALL>
 Launch launch_for(int sp) {
   return sp == 16 ? launch_all<DT, TALL, 16> : sp == 32 ? launch_all<DT, TALL, 32>
@@ -1346,7 +1347,7 @@ int muon_orthogonalize(const muon_stack* stack, const muon_config* cfg, void* wo
       for (int64_t m = 0; m < z.count; m += z.batch) {
         g.first = m;
         g.count = int(std::min(z.batch, z.count - m));
-        run(g, R, z.whole, stream);
+        run(g, R, z, stream);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess)
           return fail(MUON_ERR_HIP, "launch of an orthogonalisation kernel failed: %s", hipGetErrorString(err));

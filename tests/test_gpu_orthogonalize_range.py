@@ -98,3 +98,15 @@ def test_small_directions_and_low_rank(dtype):
                   r.normal(size=(8, l))[np.arange(s) % 8]):
             x = torch.tensor(m).to(torch.bfloat16 if dtype == "bf16" else torch.float32).to(dev())
             (norm_check if dtype == "bf16" else check)(f64(x), om.orthogonalize(x), [ABC] * 5)
+
+
+def test_equal_matrices_in_every_batch():
+    """More matrices than a launch takes: the last, small batch is summed as the others are. (Small
+    directions and eight rounds show a sum's last bits in the result.)"""
+    r = np.random.default_rng(4)
+    u, _ = np.linalg.qr(r.normal(size=(256, 17, 17)))
+    v, _ = np.linalg.qr(r.normal(size=(256, 150, 17)))
+    m = torch.tensor(u * np.logspace(0, -5, 17) @ v.swapaxes(1, 2), dtype=torch.float32, device=dev())
+    x = m[torch.arange(2 ** 20 + 256, device=dev()) % 256]
+    out = om.orthogonalize(x, steps=8)
+    assert torch.equal(out[-256:], out[:256]) and torch.equal(out[2 ** 19:2 ** 19 + 256], out[:256])
