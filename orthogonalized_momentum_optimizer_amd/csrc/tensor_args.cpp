@@ -551,7 +551,7 @@ class Linear : public torch::autograd::Function<Linear> {
     if (x.dim() == 2) return y;
     std::vector<int64_t> shape = x.sizes().vec();
     shape.back() = o;
-    return y.view(shape);
+    return at::_unsafe_view(y, shape);           // (autograd refuses to change a view made in here)
   }
 
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,

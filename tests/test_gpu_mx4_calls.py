@@ -1,0 +1,35 @@
+"""GPU tests of how a program may call the linear layer in microscaled 4-bit values and go on with its
+results. What it computes is compared bit by bit with the plain call's, which test_gpu_mx4_linear
+compares with the oracle.
+"""
+import pytest
+import torch
+
+import orthogonalized_momentum_optimizer_amd as om
+from test_gpu_mx4_linear import case, dev, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("shape", [(64,), (6, 64), (2, 3, 64), (2, 1, 3, 64), (0, 3, 64)])
+def test_the_result_may_be_changed_in_place(shape, held):
+    """y += bias, relu_(y): as after any layer."""
+    x = normal(shape, "f32", 1).requires_grad_()
+    w, bias = normal((40, 64), "f32", 2).requires_grad_(), normal((40,), "f32", 3).requires_grad_()
+    copies = om.MX4Copies([w])[w] if held else None
+    dy = normal(shape[:-1] + (40,), "f32", 4)
+    want = torch.relu(om.mx4_linear(x, w, copies) * 2 + bias)
+    grads = torch.autograd.grad(want, (x, w, bias), dy)
+    y = om.mx4_linear(x, w, copies)
+    y *= 2
+    y += bias
+    torch.relu_(y)
+    assert torch.equal(y, want)
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (x, w, bias), dy), grads))
+    with torch.no_grad():
+        y = om.mx4_linear(x, w, copies)
+    y.mul_(2).add_(bias)                          # made without a graph, changed with one
+    torch.relu_(y)
+    assert torch.equal(y, want)
+    assert torch.equal(torch.autograd.grad(y, bias, dy)[0], grads[2])
