@@ -582,7 +582,9 @@ class Linear : public torch::autograd::Function<Linear> {
       const char kind = char((need_x ? 1 : 0) | (need_w ? 2 : 0));
       Held h;
       quantize(&tensor, &kind, &h, 1, how[2], uint64_t(how[3]));
-      if (need_x) dx = product(h.data, saved[1], t, i, o, int(how[0])).view(ctx->saved_data["shape"].toIntVector());
+      if (need_x)
+        dx = at::_unsafe_view(product(h.data, saved[1], t, i, o, int(how[0])),
+                              ctx->saved_data["shape"].toIntVector());
       if (need_w) dw = product(h.data_t, saved[0], o, i, t, int(how[1]));
     }
     torch::autograd::variable_list out = {dx, dw};

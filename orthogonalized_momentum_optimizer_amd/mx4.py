@@ -87,7 +87,12 @@ class MX4Tensor:
         out = L.args().mx_dequantize(self.data, self.rows, self.cols, dtype_code(dtype))
         if type(out) is int:
             L.raise_status(out)
-        return out if len(self.shape) == 2 else out.view(self.shape)
+        return _shaped(out, self.shape)
+
+
+def _shaped(out: torch.Tensor, shape) -> torch.Tensor:
+    """out in another shape, and no view: one made under no_grad may not be changed with a graph later."""
+    return out if len(shape) == 2 else torch.ops.aten._unsafe_view(out, shape)
 
 
 def _quantize(tensors: tuple, results: bytes, stochastic: bool, seed: int):
@@ -125,7 +130,7 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, out_dtype: torch.dtype = torch.bfloat
     out = L.args().mx_matmul(a.data, b.data, a.rows, b.rows, a.cols, dtype_code(out_dtype))
     if type(out) is int:
         L.raise_status(out)
-    return out if len(a.shape) == 2 else out.view(*a.shape[:-1], b.rows)
+    return _shaped(out, (*a.shape[:-1], b.rows))
 
 
 def mx4_linear(x: torch.Tensor, weight: torch.Tensor,

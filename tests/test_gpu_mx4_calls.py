@@ -33,3 +33,20 @@ def test_the_result_may_be_changed_in_place(shape, held):
     torch.relu_(y)
     assert torch.equal(y, want)
     assert torch.equal(torch.autograd.grad(y, bias, dy)[0], grads[2])
+
+
+@pytest.mark.parametrize("shape", [(64,), (6, 64), (2, 3, 64)])
+def test_values_and_gradients_made_without_a_graph_may_be_changed_with_one(shape):
+    x, b = normal(shape, "f32", 1), normal((40, 64), "f32", 2)
+    p = torch.ones((), device=dev(), requires_grad=True)
+    with torch.no_grad():
+        q = om.mx4_quantize(x)
+        values, y = q.dequantize(torch.float32), om.mx4_matmul(q, om.mx4_quantize(b), torch.float32)
+    dx, = torch.autograd.grad(om.mx4_linear(x.requires_grad_(), b).sum(), x)
+    assert values.shape == x.shape and y.shape == shape[:-1] + (40,) and dx.shape == x.shape
+    for t in (values, y, dx):
+        want = t + p
+        t += p
+        assert torch.equal(t, want)
+        t.sum().backward()
+    assert float(p.grad) == values.numel() + y.numel() + dx.numel()
