@@ -587,17 +587,19 @@ class Linear : public torch::autograd::Function<Linear> {
                               ctx->saved_data["shape"].toIntVector());
       if (need_w) dw = product(h.data_t, saved[0], o, i, t, int(how[1]));
     }
-    torch::autograd::variable_list out = {dx, dw};
-    if (at::GradMode::is_enabled() && grad.requires_grad()) {
-      // results of a pass that is itself recorded: what would differentiate them raises
-      const auto error = std::make_shared<torch::autograd::DelayedError>(
-          "mx4_linear is differentiable once", int(out.size()));
-      for (auto& v : out)
-        if (v.defined()) v.requires_grad_(true);
-      out = (*error)(std::move(out));
+    if (at::GradMode::is_enabled()) {
+      // results of a pass that is itself recorded: what would differentiate them raises. dx is a function of
+      // the weight, dw of x, also where dy is a constant
+      auto guard = [](at::Tensor& v) {
+        if (!v.defined()) return;
+        const auto error = std::make_shared<torch::autograd::DelayedError>("mx4_linear is differentiable once", 1);
+        v.requires_grad_(true);
+        v = (*error)({v})[0];
+      };
+      if (grad.requires_grad() || saved[0].defined()) guard(dx);
+      if (grad.requires_grad() || saved[1].defined()) guard(dw);
     }
-    out.emplace_back();
-    return out;
+    return {dx, dw, at::Tensor()};
   }
 };
 

@@ -50,3 +50,19 @@ def test_values_and_gradients_made_without_a_graph_may_be_changed_with_one(shape
         assert torch.equal(t, want)
         t.sum().backward()
     assert float(p.grad) == values.numel() + y.numel() + dx.numel()
+
+
+def test_a_second_derivative_is_refused_also_of_constant_gradients():
+    """A penalty on dx depends on the weight though dy does not: refused, not left out of the gradient."""
+    x, w, dy = case(8, 64, 40, "f32", "f32")
+    y = om.mx4_linear(x, w)
+    dx, dw = torch.autograd.grad(y, (x, w), dy, create_graph=True)
+    want = torch.autograd.grad(om.mx4_linear(x, w), (x, w), dy)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    for penalty in (dx.square().sum(), dw.square().sum()):
+        with pytest.raises(RuntimeError, match="once"):
+            (om.mx4_linear(x, w).sum() + penalty).backward()
+    # a function of constants alone: nothing to refuse
+    dx, = torch.autograd.grad(om.mx4_linear(x, w.detach()).sum(), x, create_graph=True)
+    dw, = torch.autograd.grad(om.mx4_linear(x.detach(), w).sum(), w, create_graph=True)
+    assert not dx.requires_grad and not dw.requires_grad
