@@ -531,15 +531,23 @@ struct LinearCall {
   int64_t seed;
 };
 
+// t, or a copy of it in rows of its last dimension where it does not lie as quantize takes it.
+at::Tensor rows_laid(const at::Tensor& t) {
+  MxSource s;
+  bool transposed;
+  return !t.is_neg() && rows_of(t, s, transposed) ? t : t.resolve_neg().contiguous();
+}
+
 class Linear : public torch::autograd::Function<Linear> {
  public:
   static at::Tensor forward(torch::autograd::AutogradContext* ctx, const at::Tensor& x, const at::Tensor& w,
                             const LinearCall& call) {
     const int64_t o = w.size(0);
-    Held h[2];
-    const at::Tensor* const tensors[2] = {&x, &w};
-    const char kinds[2] = {char(call.need_w ? 3 : 1), char(call.need_x ? 3 : 1)};
     const bool own = !call.rows.defined();
+    const at::Tensor xr = rows_laid(x), wr = own ? rows_laid(w) : w;
+    Held h[2];
+    const at::Tensor* const tensors[2] = {&xr, &wr};
+    const char kinds[2] = {char(call.need_w ? 3 : 1), char(call.need_x ? 3 : 1)};
     quantize(tensors, kinds, h, own ? 2 : 1, false, 0);
     const Held& hx = h[0];
     const at::Tensor y = product(hx.data, own ? h[1].data : call.rows, hx.rows, o, hx.cols, dtype_code(x));
@@ -577,7 +585,7 @@ class Linear : public torch::autograd::Function<Linear> {
     if (need_x || need_w) {
       const at::AutoGradMode no_grad(false);
       // (an expanded gradient, of a sum say, has no memory of its own for each value)
-      const at::Tensor dy = grad.contiguous().view({t, o});
+      const at::Tensor dy = grad.resolve_neg().contiguous().view({t, o});
       const at::Tensor* const tensor = &dy;
       const char kind = char((need_x ? 1 : 0) | (need_w ? 2 : 0));
       Held h;

@@ -138,7 +138,7 @@ def mx4_linear(x: torch.Tensor, weight: torch.Tensor,
                seed: int = 0) -> torch.Tensor:
     """x weight^T with all three products of the layer in microscaled 4-bit values: x (.., inputs)
     and weight (outputs, inputs), bfloat16 or float32. The result has x's dtype, gradients those of
-    x and weight. ``copies``: the weight and its transpose as held (``MX4Copies``), else the
+    x and weight. Either may lie in any way; what ``mx4_quantize`` does not take is copied first. ``copies``: the weight and its transpose as held (``MX4Copies``), else the
     weight is quantised in this call. Values are rounded to nearest; ``stochastic``: but the incoming
     gradients stochastically, with the random bits of ``seed`` (give another for every step and layer; a
     captured pass repeats its own). As with any layer, let go of what an eager pass left of the graph of

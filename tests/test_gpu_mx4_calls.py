@@ -66,3 +66,27 @@ def test_a_second_derivative_is_refused_also_of_constant_gradients():
     dx, = torch.autograd.grad(om.mx4_linear(x, w.detach()).sum(), x, create_graph=True)
     dw, = torch.autograd.grad(om.mx4_linear(x.detach(), w).sum(), w, create_graph=True)
     assert not dx.requires_grad and not dw.requires_grad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_operands_may_lie_in_any_way(dtype):
+    """Permuted activations, sliced columns, expanded ones, negated views."""
+    w = normal((40, 64), dtype, 1)
+    base = normal((5, 64, 7), dtype, 2)
+    pairs = torch.complex(normal((6, 64), "f32", 3), normal((6, 64), "f32", 4)).conj()
+    for x in (base.permute(0, 2, 1), base.permute(2, 0, 1), normal((4, 5, 128), dtype, 5)[:, 1:4, ::2],
+              normal((3, 1, 64), dtype, 6).expand(3, 4, 64), normal((64, 9), dtype, 7).t(), normal((), dtype, 8).expand(6, 64),
+              *([pairs.imag] if dtype == "f32" else [])):
+        v = torch.empty_strided((40, 64), (1, 100), dtype=w.dtype, device=dev()).copy_(w)
+        wide = torch.empty((40, 128), dtype=w.dtype, device=dev())[:, ::2].copy_(w)
+        dy = normal((40,) + tuple(x.shape[:-1]), dtype, 9).movedim(0, -1)
+        flat = x.detach().clone(memory_format=torch.contiguous_format).requires_grad_()
+        w.requires_grad_()
+        want = om.mx4_linear(flat, w)
+        grads = torch.autograd.grad(want, (flat, w), dy.clone(memory_format=torch.contiguous_format))
+        x = x.detach().requires_grad_()
+        for u in (w, v.requires_grad_(), wide.requires_grad_()):
+            y = om.mx4_linear(x, u)
+            assert torch.equal(y, want)
+            assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (x, u), dy), grads))
+        w.requires_grad_(False)
