@@ -719,6 +719,8 @@ PyObject* orthogonalize(PyObject*, PyObject* args) {
           out.sizes() != x.sizes() || out.layout() != at::kStrided || out.is_neg())
         throw Refused{PyExc_ValueError, "out must be a tensor of x's shape, dtype and device"};
     }
+    if (x._fw_grad(0).defined() || out._fw_grad(0).defined())
+      throw Refused{PyExc_ValueError, "orthogonalize has no forward-mode derivative: call it on primal values"};
     const int passes = library.passes(cfg.view.buf);
     check(std::min(passes, 0));
     unlocked([&] {

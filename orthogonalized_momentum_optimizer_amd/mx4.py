@@ -25,7 +25,8 @@ _ROWS, _COLS, _BOTH = b"\1", b"\2", b"\3"
 
 class MX4Tensor:
     """A matrix in microscaled 4-bit values, rows of its last dimension (leading dimensions, if
-    any, are kept in ``shape``). ``data``: its codes and scales in the layout of include/mx4.h.
+    any, are kept in ``shape``), outside of autograd: no derivative passes through it. ``data``: its
+    codes and scales in the layout of include/mx4.h.
 
     ``MX4Tensor(codes, scales, cols)`` makes one from the usual layout: ``codes`` uint8, rows x at
     least ceil(cols / 2), the first of two codes in the low half; ``scales`` uint8 (or

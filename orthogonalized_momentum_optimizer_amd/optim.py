@@ -217,7 +217,8 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, abc=(3.4445, -4.7750, 2.0315)
     result has x's dtype and order of strides. ``out``: where it goes (x itself: in place).
     ``schedule``: None, or ``steps`` triples (a, b, c), one per round. Rounds that could lift small
     directions by more than 2^15 in all (over eight of the default ones) take several passes over x, held
-    in float32 between them. Runs on the current stream and may be captured."""
+    in float32 between them. It has no derivative, and refuses what asks for one. Runs on the current
+    stream and may be captured."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("a CUDA tensor expected")
     if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):

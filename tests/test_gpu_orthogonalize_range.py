@@ -110,3 +110,17 @@ def test_equal_matrices_in_every_batch():
     x = m[torch.arange(2 ** 20 + 256, device=dev()) % 256]
     out = om.orthogonalize(x, steps=8)
     assert torch.equal(out[-256:], out[:256]) and torch.equal(out[2 ** 19:2 ** 19 + 256], out[:256])
+
+
+def test_forward_mode_derivatives_are_refused():
+    """Where a backward pass is refused a tangent is not dropped either."""
+    from torch.autograd import forward_ad
+    x, t = gradients((2, 8, 16), "f32", 1), gradients((2, 8, 16), "f32", 2)
+    want = om.orthogonalize(x)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, t)
+        for call in (lambda: om.orthogonalize(dual), lambda: om.orthogonalize(x, out=dual),
+                     lambda: om.orthogonalize(dual, out=torch.empty_like(x))):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+        assert torch.equal(om.orthogonalize(forward_ad.unpack_dual(dual).primal), want)
