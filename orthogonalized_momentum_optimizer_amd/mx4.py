@@ -209,9 +209,11 @@ class MX4Copies:
     @torch.no_grad()
     def refresh(self) -> None:
         """Quantises the parameters as they are now, on the current stream."""
-        if not self._params:
-            return
-        # a parameter may have been given other memory since (p.data = ...)
+        self._look()
+        self._make()
+
+    def _look(self):
+        """Where the parameters are now: one may have been given other memory since (p.data = ...)."""
         now = [(p.data_ptr(), p.dtype, p.shape, p.is_contiguous()) for p in self._params]
         if now != self._at:
             for p in self._params:
@@ -221,6 +223,10 @@ class MX4Copies:
                                      "copies were made")
             self._sources = L.make_mx_sources(self._entry(p) for p in self._params)
             self._at = now
+
+    def _make(self):
+        if not self._params:
+            return
         device = self._params[0].device
         with torch.cuda.device(device):
             L.muon_mx_quantize(self._sources, len(self._params), 0, 0, _raw_stream(device.index))

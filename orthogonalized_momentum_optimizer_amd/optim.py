@@ -256,6 +256,10 @@ class Muon(torch.optim.Optimizer):
         super().__init__(params, defaults)
         if precision not in _PREC:
             raise ValueError(f"precision must be one of {sorted(_PREC)}")
+        if mx4_copies is not None:
+            from .mx4 import MX4Copies
+            if not isinstance(mx4_copies, MX4Copies):
+                raise TypeError("mx4_copies must be an MX4Copies")
         self.precision = precision
         self.mx4_copies = mx4_copies
         for group in self.param_groups:
@@ -277,6 +281,8 @@ class Muon(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if self.mx4_copies is not None:
+            self.mx4_copies._look()               # what it refuses is refused before any parameter is stepped
         for gi, group in enumerate(self.param_groups):
             params, grads, moms, rvars = [], [], [], []
             for p in group["params"]:
@@ -311,7 +317,7 @@ class Muon(torch.optim.Optimizer):
                               row_eps=group["row_eps"])
             plan.step(params, grads, moms, cfg, row_vars=rvars if group["row_equalize"] else None)
         if self.mx4_copies is not None:
-            self.mx4_copies.refresh()
+            self.mx4_copies._make()
         return loss
 
 

@@ -90,3 +90,23 @@ def test_operands_may_lie_in_any_way(dtype):
             assert torch.equal(y, want)
             assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (x, u), dy), grads))
         w.requires_grad_(False)
+
+
+def test_muon_looks_at_its_copies_before_it_steps():
+    w = torch.nn.Parameter(normal((96, 64), "bf16", 1))
+    for wrong in ([w], w, om.MX4Copies, om.MX4Copies([w])[w], object()):
+        with pytest.raises(TypeError):
+            om.Muon([w], mx4_copies=wrong)
+    other = normal((32, 64), "bf16", 2)
+    opt = om.Muon([w], mx4_copies=om.MX4Copies([w, other]))
+    w.grad = normal((96, 64), "bf16", 3)
+    before = w.detach().clone()
+    for bad, error in ((normal((33, 64), "bf16", 4), ValueError), (normal((32, 64), "f32", 4).half(), TypeError)):
+        good, other.data = other.data, bad
+        with pytest.raises(error):
+            opt.step()
+        assert torch.equal(w, before) and not opt.state
+        other.data = good
+    opt.step()
+    assert not torch.equal(w, before) and torch.equal(opt.mx4_copies[w][0].data, om.mx4_quantize(w).data)
+    om.Muon([w], mx4_copies=om.MX4Copies([])).step()       # nothing held
