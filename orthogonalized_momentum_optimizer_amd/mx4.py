@@ -78,8 +78,8 @@ class MX4Tensor:
         """(codes, scales): uint8, rows x ceil(cols / 2) and rows x ceil(cols / 32)."""
         panels, steps = -(-self.rows // 16), -(-self.cols // 128)
         at = panels * steps * 1024
-        codes = self.data[:at].view(panels, steps, 16, 64).transpose(1, 2).reshape(panels * 16, -1)
-        scales = self.data[at:].view(panels, steps, 16, 4).transpose(1, 2).reshape(panels * 16, -1)
+        codes = self.data[:at].view(panels, steps, 16, 64).transpose(1, 2).reshape(panels * 16, steps * 64)
+        scales = self.data[at:].view(panels, steps, 16, 4).transpose(1, 2).reshape(panels * 16, steps * 4)
         return (codes[:self.rows, :-(-self.cols // 2)].contiguous(),
                 scales[:self.rows, :-(-self.cols // 32)].contiguous())
 
