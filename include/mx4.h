@@ -62,12 +62,14 @@ typedef struct {
 
 /* Quantises n matrices (one launch for up to 60 of one dtype and the same results asked for).
  * stochastic 0 or 1; seed: of the random bits, which depend on it and on a value's place in
- * its matrix alone. No result may overlap another or a source. */
+ * its matrix alone. No result may overlap another or a source. A source may have up to 2^23 tiles of
+ * 64 x 128 values (128 x 128 where its transpose is asked for), else MUON_ERR_UNSUPPORTED. */
 int muon_mx_quantize(const muon_mx_source *sources, int64_t n, int stochastic, uint64_t seed,
                      hipStream_t stream);
 
 /* out (rows x cols, row-major, contiguous) receives the values that codes and scales stand
- * for, exactly. */
+ * for, exactly (infinity beyond fp32's range, which scales of 2^126 and 2^127 can reach). Up to 2^25 tiles of
+ * 16 x 128 values, else MUON_ERR_UNSUPPORTED. */
 int muon_mx_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
                        void *out, muon_dtype dtype, hipStream_t stream);
 
@@ -75,7 +77,7 @@ int muon_mx_dequantize(const void *codes, const void *scales, int64_t rows, int6
  * required; 0: none). SIZE_MAX for sizes outside the library's limits. */
 size_t muon_mx_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
 
-/* out (m x n of dtype) = A B^T. */
+/* out (m x n of dtype) = A B^T; m x n up to 2^23 tiles of 128 x 128, else MUON_ERR_UNSUPPORTED. */
 int muon_mx_matmul(const void *a_codes, const void *a_scales, const void *b_codes,
                    const void *b_scales, int64_t m, int64_t n, int64_t k, void *out,
                    muon_dtype dtype, void *workspace, size_t workspace_bytes,
