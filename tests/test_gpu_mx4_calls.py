@@ -110,3 +110,48 @@ def test_muon_looks_at_its_copies_before_it_steps():
     opt.step()
     assert not torch.equal(w, before) and torch.equal(opt.mx4_copies[w][0].data, om.mx4_quantize(w).data)
     om.Muon([w], mx4_copies=om.MX4Copies([])).step()       # nothing held
+
+
+@pytest.mark.parametrize("held", [False, True])
+def test_recomputed_and_offloaded_passes(held):
+    """Activations that are recomputed in the backward pass, or wait for it on the host."""
+    from torch.utils.checkpoint import checkpoint
+    x, w, _ = case(24, 64, 64, "bf16", "bf16")
+    copies = om.MX4Copies([w])[w] if held else None
+
+    def net(x):
+        return om.mx4_linear(torch.relu(om.mx4_linear(x.view(4, 6, 64), w, copies)), w, copies).float().square().mean()
+    want = torch.autograd.grad(net(x), (x, w))
+    for reentrant in (False, True):
+        x.grad = w.grad = None
+        checkpoint(net, x, use_reentrant=reentrant).backward()
+        assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1])
+    with torch.autograd.graph.save_on_cpu():
+        got = torch.autograd.grad(net(x), (x, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_modes():
+    """Inference mode, autocast, forward-mode and functional transforms."""
+    x, w, dy = case(24, 64, 40, "bf16", "bf16")
+    want = om.mx4_linear(x, w).detach()
+    with torch.inference_mode():
+        copies = om.MX4Copies([w])
+        copies.refresh()
+        y = om.mx4_linear(x, w, copies[w])
+        z = om.mx4_linear(x.clone(), w)
+        h = om.orthogonalize(x.view(2, 12, 64).clone(), steps=20)
+    assert torch.equal(y, want) and torch.equal(z, want) and h.isfinite().all()
+    copies.refresh()
+    with torch.autocast("cuda", torch.bfloat16):
+        assert torch.equal(om.mx4_linear(x, w), want)
+    from torch.autograd import forward_ad
+    with forward_ad.dual_level():
+        with pytest.raises(RuntimeError):
+            om.mx4_linear(forward_ad.make_dual(x.detach(), x.detach()), w)
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda v: om.mx4_linear(x.detach(), v).sum())(w.detach())
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda v: om.mx4_linear(v, w.detach()))(x.detach().view(4, 6, 64))
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(om.orthogonalize)(x.detach().view(4, 6, 64))
