@@ -4,8 +4,8 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 takes 32 rows x 64 values of either operand, one block of 32 values
 // a lane (lane l: row l % 32, block l / 32), and that block's scale byte beside it, so that codes and
 // scales go from memory into the instruction as they are held. Products are exact and sums are
-// fp32. (With data-like operands and nothing else the matrix cores give 6.2 PFLOP/s by these and 3.7
-// by the 16x16x128 form.)
+// fp32. (With data-like operands and nothing else the matrix cores give 6.2 to 6.6 PFLOP/s by these and
+// 3.7 by the 16x16x128 form.)
 #include <algorithm>
 #include <cmath>
 #include <vector>
