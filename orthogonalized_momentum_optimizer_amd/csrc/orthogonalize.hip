@@ -260,10 +260,12 @@ __device__ __forceinline__ double gram_value(const GramValues<DT, NB>& v, int b,
   else return __uint_as_float(e & 1 ? v.x[b][e / 2] & 0xffff0000u : v.x[b][e / 2] << 16);
 }
 
-// Whether sums in fp32 hold what they stand for, by the trace of a matrix, or of a piece: no diagonal sum of 32
-// and so no other can have passed fp32's range (2^128), and products lost below it (2^-126, 2^24 of them at most)
-// are 2^-42 of the trace. A trace that is not finite, or of zeros, is formed again too.
-__device__ __forceinline__ bool fits_fp32(double trace) { return trace >= 0x1p-60 && trace <= 0x1p120; }
+// Whether sums in fp32 over n positions hold what they stand for, by their trace: no diagonal sum of 32 and so
+// no other can have passed fp32's range (2^128), and products lost below it, n 2^-126 of an element at most, are
+// 2^-30 of the trace. A trace that is not finite, or of zeros, is formed again too.
+__device__ __forceinline__ bool fits_fp32(double trace, int n) {
+  return trace >= n * 0x1p-96 && trace <= 0x1p120;
+}
 
 // The sum of x over a wave, in each lane.
 __device__ __forceinline__ double wave_sum(double x) {
@@ -437,7 +439,7 @@ __device__ __forceinline__ void gram_of(const StackArgs& g, const char* base, in
       gram_part<DT, TALL, SP, WAVES, false>(g, base, begin, end, wave, lane, lds);
       double trace = 0;                          // the same in every wave
       for (int i = lane; i < SP; i += 64) trace += lds[i * SP + i];
-      if (__builtin_amdgcn_readfirstlane(fits_fp32(wave_sum(trace)))) return;
+      if (__builtin_amdgcn_readfirstlane(fits_fp32(wave_sum(trace), end - begin))) return;
       __syncthreads();                           // everyone has read it
     }
   }
@@ -521,7 +523,8 @@ __global__ __launch_bounds__(256, SP == 128 ? 2 : 1) void gram_kernel(const Stac
         const double trace = gram_shared<DT, TALL, false>(g, base, begin, end, wave, t & 63, out);
         if ((t & 63) == 0) traces[wave] = trace;
         __syncthreads();                         // (and what the waves stored is ordered before the second form)
-        if (__builtin_amdgcn_readfirstlane(fits_fp32(traces[0] + traces[1] + traces[2] + traces[3]))) return;
+        const double trace_all = traces[0] + traces[1] + traces[2] + traces[3];
+        if (__builtin_amdgcn_readfirstlane(fits_fp32(trace_all, end - begin))) return;
       }
     }
     gram_shared<DT, TALL, true>(g, base, begin, end, wave, t & 63, out);

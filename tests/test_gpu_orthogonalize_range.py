@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("tall", [False, True])
 @pytest.mark.parametrize("s,l", [(12, 40), (12, 1100), (20, 50), (30, 1300), (64, 200), (64, 1500), (100, 140),
                                  (100, 700)])
-@pytest.mark.parametrize("scale", [1e-37, 1e-22, 1e-10, 1e10, 1e18, 1e20, 1e36])
+@pytest.mark.parametrize("scale", [1e-37, 1e-22, 1e-18, 1e-15, 1e-13, 1e-10, 1e10, 1e18, 1e20, 1e36])
 def test_every_finite_value_is_in_range(scale, s, l, tall, dtype):
     """In one launch, and in three where few matrices are long or the short side is over 64."""
     x = gradients((2, l, s) if tall else (2, s, l), dtype, s + l, scale=scale)
